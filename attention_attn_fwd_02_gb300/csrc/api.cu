@@ -16,6 +16,8 @@
 #include "common.cuh"
 #include "prefill_tc.h"
 #include "decode.h"
+#include "visible.cuh"
+#include "prep.h"
 
 namespace attn {
 
@@ -325,7 +327,74 @@ int decode_impl(const attn_problem* p, const void* q, const void* k_cache, const
   }
   return from_cuda(launch_combine(r, s, p->dtype, st));
 }
+// The partial-result arrays of a split pass over `rows` rows in a workspace.
+Split split_in(void* workspace, size_t rows, int n_splits, int split_len, int D) {
+  Split s;
+  s.n_splits = n_splits;
+  s.split_len = split_len;
+  s.part_o = static_cast<float*>(workspace);
+  s.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        round256(rows * n_splits * D * sizeof(float)));
+  return s;
+}
+
+constexpr int32_t kMaxFirst = 1 << 30;
+
+int check_window(const attn_problem* p, int32_t first_keys) {
+  const int rc = check_problem(p);
+  if (rc) return rc;
+  if (first_keys < 0 || first_keys > kMaxFirst) return ATTN_ERR_INVALID_ARG;
+  if (p->k_len > kMaxFirst || p->q_len > kMaxFirst) return ATTN_ERR_UNSUPPORTED;   // key and row indices in 32 bits
+  if (first_keys > 0 && (!p->causal || p->window_left < 0)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+// attn_fwd_window's plan: parts of each query block's list of key tiles, by
+// the rule of fwd_plan with the longest list a block can have for the keys.
+int window_plan(const attn_problem* p, int32_t first_keys) {
+  if (p->k_len <= 0 || p->q_len <= 0 || p->batch <= 0) return 1;
+  if (p->key_splits > 0) return p->key_splits < kMaxRanges ? p->key_splits : kMaxRanges;
+  const int rows = p->head_dim <= 128 ? 256 : 128;
+  const int64_t blocks = (int64_t)((p->q_len + rows - 1) / rows) * p->heads * p->batch;
+  if (blocks >= kFillBlocks) return 1;
+  int64_t span = (int64_t)p->window_left + first_keys + rows;
+  span = span < p->k_len ? span : p->k_len;
+  int64_t n = (kFillBlocks + blocks - 1) / blocks;
+  n = n < kMaxRanges ? n : kMaxRanges;
+  n = n < span / 1024 ? n : span / 1024;
+  return n < 1 ? 1 : (int)n;
+}
+
+int check_paged(const attn_problem* p, const attn_pages* pages, int32_t first_keys) {
+  const int rc = check_window(p, first_keys);
+  if (rc) return rc;
+  if (p->q_len != 1) return ATTN_ERR_INVALID_ARG;
+  return check_pages(pages, p->k_len);
+}
+
+// attn_decode_paged's plan: ranges of each entry's own visible keys.
+int paged_plan(const attn_problem* p, int32_t first_keys) {
+  int64_t span = p->k_len;
+  if (p->causal && p->window_left >= 0) {
+    const int64_t w = (int64_t)p->window_left + 1 + first_keys;
+    span = w < span ? w : span;
+  }
+  const int64_t pairs = (int64_t)(p->batch > 0 ? p->batch : 1) * p->kv_heads;
+  int64_t n = (4096 + pairs - 1) / pairs;
+  n = n < 64 ? n : 64;
+  const int64_t tiles = (span + 127) / 128;
+  n = n < tiles ? n : tiles;
+  return n < 1 ? 1 : (int)n;
+}
+
 }  // namespace
+
+int check_pages(const attn_pages* pages, int64_t rows) {
+  if (!pages || pages->page_size < 1 || pages->n_pages < 0 || pages->table_stride < 0) return ATTN_ERR_INVALID_ARG;
+  if (rows > 0 && !pages->table) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(pages->table, 4)) return ATTN_ERR_ALIGNMENT;
+  return ATTN_OK;
+}
 }  // namespace attn
 
 using namespace attn;
@@ -406,6 +475,71 @@ int attn_decode_append(const attn_problem* p, const void* q, const void* k_new, 
                            stream, k_new, v_new);
 }
 
+size_t attn_fwd_window_workspace_size(const attn_problem* p, int32_t first_keys) {
+  if (check_window(p, first_keys) != ATTN_OK) return 0;
+  if (first_keys == 0) return attn_fwd_workspace_size(p);
+  const int n = window_plan(p, first_keys);
+  return n > 1 ? decode_ws_bytes(p, n) : 0;
+}
+
+int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, const void* k, const void* v, void* o,
+                    const float* mask, const int32_t* seg, const int32_t* k_lens, float* lse, void* workspace,
+                    size_t workspace_bytes, attn_stream stream) {
+  int rc = check_window(p, first_keys);
+  if (rc) return rc;
+  if (!p->causal || p->window_left < 0) return ATTN_ERR_INVALID_ARG;
+  if (first_keys == 0) return attn_fwd(p, q, k, v, o, mask, seg, k_lens, lse, workspace, workspace_bytes, stream);
+  if (p->batch == 0 || p->q_len == 0) return ATTN_OK;
+  rc = check_pointers(p, q, k, v, o, mask, seg, k_lens, lse);
+  if (rc) return rc;
+  const int n = window_plan(p, first_keys);
+  Split s{1, p->k_len > 0 ? p->k_len : 1, nullptr, nullptr};
+  if (n > 1) {
+    const bool enough = workspace && workspace_bytes >= decode_ws_bytes(p, n);
+    if (enough && aligned(workspace, 256))
+      s = split_in(workspace, (size_t)p->batch * p->heads * p->q_len, n, 0, p->head_dim);
+    else if (p->key_splits > 1)
+      return enough ? ATTN_ERR_ALIGNMENT : ATTN_ERR_WORKSPACE;
+  }
+  int* status = nullptr;
+  rc = status_ptr(&status);
+  if (rc) return rc;
+  const Problem r = resolve(p, q, k, v, o, mask, seg, k_lens, lse, status);
+  const Ext x{first_keys, 0, 0u, nullptr, 0};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rc = from_cuda(launch_simt_ext(r, x, s, st));
+  if (rc) return rc;
+  return s.n_splits > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;
+}
+
+size_t attn_decode_paged_workspace_size(const attn_problem* p, const attn_pages* pages, int32_t first_keys) {
+  if (check_paged(p, pages, first_keys) != ATTN_OK) return 0;
+  return decode_ws_bytes(p, paged_plan(p, first_keys));
+}
+
+int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t first_keys, const void* q,
+                      const void* k_pool, const void* v_pool, void* o, const float* mask, const int32_t* k_lens,
+                      float* lse, void* workspace, size_t workspace_bytes, attn_stream stream) {
+  int rc = check_paged(p, pages, first_keys);
+  if (rc) return rc;
+  if (p->batch == 0) return ATTN_OK;
+  rc = check_pointers(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse);
+  if (rc) return rc;
+  const int n = paged_plan(p, first_keys);
+  if (!workspace || workspace_bytes < decode_ws_bytes(p, n)) return ATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  int* status = nullptr;
+  rc = status_ptr(&status);
+  if (rc) return rc;
+  const Problem r = resolve(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse, status);
+  const Ext x{first_keys, pages->page_size, (uint32_t)pages->n_pages, pages->table, pages->table_stride};
+  const Split s = split_in(workspace, (size_t)p->batch * p->heads, n, 0, p->head_dim);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rc = from_cuda(launch_simt_ext(r, x, s, st));
+  if (rc) return rc;
+  return from_cuda(launch_combine(r, s, p->dtype, st));
+}
+
 int attn_combine(int32_t n_splits, int32_t rows, int32_t head_dim, const float* part_o, const float* part_lse,
                  int32_t out_dtype, void* o, int64_t o_row_stride, float* lse, int32_t masked_rows,
                  attn_stream stream) {
@@ -457,6 +591,6 @@ int attn_test_inject(int32_t fault) {
   return ATTN_OK;
 }
 
-int attn_version(void) { return 250; }
+int attn_version(void) { return 260; }
 
 }  // extern "C"

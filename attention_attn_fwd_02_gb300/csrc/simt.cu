@@ -121,7 +121,7 @@ cudaError_t combine_dispatch(int32_t dt, int n_splits, int64_t rows, int D, cons
 
 cudaError_t launch_simt(const Problem& p, const Split& s, cudaStream_t st) {
   if (p.D == 32 || p.D == 64 || p.D == 128 || p.D == 256) return launch_simt_full(p, s, st);
-  return launch_simt_all<false>(p, s, st);
+  return launch_simt_all<false, false>(p, s, st, Ext{});
 }
 
 cudaError_t launch_combine(const Problem& p, const Split& s, int32_t out_dtype, cudaStream_t st) {

@@ -6,7 +6,7 @@
 namespace attn {
 
 cudaError_t launch_simt_full(const Problem& p, const Split& s, cudaStream_t st) {
-  return launch_simt_all<true>(p, s, st);
+  return launch_simt_all<true, false>(p, s, st, Ext{});
 }
 
 }  // namespace attn

@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "visible.cuh"
 
 namespace attn {
 
@@ -47,8 +48,12 @@ constexpr int kTile = 32;    // keys per staged tile
 // float32 problem 15.0 -> 13.0 us a call against three CTAs' 168 registers,
 // larger problems 10-15 % slower than with three, still 1.1-1.4x faster than
 // the per-key branching form).
-template <typename T, int TPR, bool KV8, bool FULL>
-__global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split sp, int64_t row_blocks) {
+//
+// EXT: windows with first keys and paged caches (visible.cuh).  The CTA then
+// walks the tile list of its rows' union, a split pass its part of that list,
+// and a bit mask per tile says which of its keys have a page.
+template <typename T, int TPR, bool KV8, bool FULL, bool EXT>
+__global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split sp, int64_t row_blocks, Ext x) {
   constexpr int RPC = kThreads / TPR;  // rows per CTA
   extern __shared__ __align__(16) float smem[];
   float* Ks = smem;
@@ -66,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
   // Decode with append: every CTA of the range holding the new row writes it
   // (the same values) before the first barrier below, so its own staging
   // reads see it.
-  if (p.k_new) {
+  if (!EXT && p.k_new) {
     const int64_t row = append_target(p, b);
     if (row >= 0 && row / sp.split_len == split) append_row<T>(p, b, g, row);
   }
@@ -83,23 +88,62 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
   const int h = g * p.qpg + (valid ? (int)(r % p.qpg) : 0);
 
   int64_t lo = 0, hi = 0;
-  if (valid) {
+  Vis rv{0, 0, 0, 0}, uv{0, 0, 0, 0};
+  TileList tl{0, 0, 0, 0};
+  int tile0 = 0, tile1 = 0;
+  __shared__ int s_first[2];
+  __shared__ uint32_t s_paged;
+  if constexpr (EXT) {
+    if (valid) rv = row_vis(p, x.first, b, i);
+    if (threadIdx.x == 0) {
+      s_lo = s_first[0] = INT_MAX;
+      s_hi = s_first[1] = INT_MIN;
+    }
+    __syncthreads();
+    if (valid && lr == 0) {
+      if (rv.fe > rv.lo) {
+        atomicMin(&s_first[0], rv.lo);
+        atomicMax(&s_first[1], rv.fe);
+      }
+      if (rv.hi > rv.wl) {
+        atomicMin(&s_lo, rv.wl);
+        atomicMax(&s_hi, rv.hi);
+      }
+    }
+    __syncthreads();
+    // A row with a first part has a window part, so both parts are set or the first is empty.
+    if (s_hi > s_lo) {
+      uv = {s_lo, s_lo, s_lo, s_hi};
+      if (s_first[1] > s_first[0]) {
+        uv.lo = uv.fe = min(s_first[0], s_lo);
+        if (s_first[1] < s_lo) uv.fe = s_first[1];
+        else uv.wl = uv.lo;
+      }
+    }
+    tl = tile_list(uv, kTile);
+    tile1 = tl.n;
+    if (sp.part_o != nullptr) list_part(tl.n, split, sp.n_splits, tile0, tile1);
+  } else if (valid) {
     row_range(p, b, i, lo, hi);
     lo = max(lo, k0);
     hi = min(hi, k1);
     if (hi < lo) hi = lo;
   }
-  if (threadIdx.x == 0) {
+  if (!EXT && threadIdx.x == 0) {
     s_lo = INT_MAX;
     s_hi = INT_MIN;
   }
   __syncthreads();
-  if (valid && lr == 0 && hi > lo) {
+  if (!EXT && valid && lr == 0 && hi > lo) {
     atomicMin(&s_lo, (int)lo);
     atomicMax(&s_hi, (int)hi);
   }
   __syncthreads();
   const int u_lo = s_lo, u_hi = s_hi;  // union of the CTA's row ranges (empty: u_lo > u_hi)
+  if constexpr (!EXT) {
+    tile0 = u_lo / kTile;
+    tile1 = u_hi > u_lo ? (u_hi + kTile - 1) / kTile : tile0;
+  }
 
   const T* Q = static_cast<const T*>(p.Q);
   const T* K = static_cast<const T*>(p.K);
@@ -117,8 +161,20 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
   }
   float m = -INFINITY, l = 0.f;
 
-  for (int t0 = (u_lo / kTile) * kTile; t0 < u_hi; t0 += kTile) {
+  for (int ti = tile0; ti < tile1; ++ti) {
+    const int t0 = (EXT ? tl.tile(ti) : ti) * kTile;
     __syncthreads();
+    if constexpr (EXT) {
+      // Keys of the tile that the CTA reads: visible to some row, and in a page of the pool.
+      if (threadIdx.x < kTile) {
+        const int kk = t0 + threadIdx.x;
+        const bool here = visible(uv, kk) && (!x.page_size || page_of(x, b, kk) >= 0);
+        const uint32_t m = __ballot_sync(0xffffffffu, here);
+        if (threadIdx.x == 0) s_paged = m;
+      }
+      __syncthreads();
+    }
+    const uint32_t tile_keys = EXT ? s_paged : 0u;
     // Stage the tile; keys outside the CTA's union are zero (never read from
     // memory).  Each thread issues the loads of kBatch elements before it
     // stores any, so a tile costs about one memory latency, not kBatch.
@@ -132,14 +188,27 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
         const int kk = t0 + j;
         kv[u] = 0.f;
         vv[u] = 0.f;
-        if (e < kTile * D && kk >= u_lo && kk < u_hi) {
+        bool here = e < kTile * D;
+        int64_t ko = kb + (int64_t)kk * p.k.rs + d, vo = vb + (int64_t)kk * p.v.rs + d;
+        if constexpr (EXT) {
+          here = here && ((tile_keys >> j) & 1u);
+          if (here && x.page_size) {
+            const int64_t pg = page_of(x, b, kk);
+            const int r = kk % x.page_size;
+            ko = p.k.off + pg * p.k.bs + (int64_t)g * p.k.hs + (int64_t)r * p.k.rs + d;
+            vo = p.v.off + pg * p.v.bs + (int64_t)g * p.v.hs + (int64_t)r * p.v.rs + d;
+          }
+        } else {
+          here = here && kk >= u_lo && kk < u_hi;
+        }
+        if (here) {
           if constexpr (KV8) {
             const int si = p.kv_per_channel ? g * D + d : 0;
-            kv[u] = (float)reinterpret_cast<const int8_t*>(p.K)[kb + (int64_t)kk * p.k.rs + d] * p.k_scale[si];
-            vv[u] = (float)reinterpret_cast<const int8_t*>(p.V)[vb + (int64_t)kk * p.v.rs + d] * p.v_scale[si];
+            kv[u] = (float)reinterpret_cast<const int8_t*>(p.K)[ko] * p.k_scale[si];
+            vv[u] = (float)reinterpret_cast<const int8_t*>(p.V)[vo] * p.v_scale[si];
           } else {
-            kv[u] = to_f32(K[kb + (int64_t)kk * p.k.rs + d]);
-            vv[u] = to_f32(V[vb + (int64_t)kk * p.v.rs + d]);
+            kv[u] = to_f32(K[ko]);
+            vv[u] = to_f32(V[vo]);
           }
         }
       }
@@ -184,14 +253,14 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
 #pragma unroll
       for (int j = 0; j < kTile; ++j) {
         const int kk = t0 + j;
-        if (kk >= lo && kk < hi) sc[j] += p.M[mrow + kk];
+        if (EXT ? visible(rv, kk) : (kk >= lo && kk < hi)) sc[j] += p.M[mrow + kk];
       }
     }
     float mt = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
       const int kk = t0 + j;
-      const bool vis = valid && kk >= lo && kk < hi;
+      const bool vis = valid && (EXT ? ((tile_keys >> j) & 1u) && visible(rv, kk) : (kk >= lo && kk < hi));
       sc[j] = vis ? sc[j] : -INFINITY;
       mt = fmaxf(mt, sc[j]);
     }
@@ -263,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
   }
 }
 
-template <typename T, int TPR, bool KV8, bool FULL>
-cudaError_t launch_simt_f(const Problem& p, const Split& s, cudaStream_t st) {
+template <typename T, int TPR, bool KV8, bool FULL, bool EXT>
+cudaError_t launch_simt_f(const Problem& p, const Split& s, cudaStream_t st, const Ext& x) {
   constexpr int RPC = kThreads / TPR;
   const int64_t rows = (int64_t)p.Sq * p.qpg;
   const int64_t row_blocks = (rows + RPC - 1) / RPC;
@@ -272,32 +341,34 @@ cudaError_t launch_simt_f(const Problem& p, const Split& s, cudaStream_t st) {
   if (blocks <= 0) return cudaSuccess;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   const size_t smem = (size_t)2 * kTile * p.D * sizeof(float);
-  cudaError_t e = ensure_smem((const void*)simt_attn_kernel<T, TPR, KV8, FULL>, (int)smem);
+  cudaError_t e = ensure_smem((const void*)simt_attn_kernel<T, TPR, KV8, FULL, EXT>, (int)smem);
   if (e != cudaSuccess) return e;
-  simt_attn_kernel<T, TPR, KV8, FULL><<<(unsigned)blocks, kThreads, smem, st>>>(p, s, row_blocks);
+  simt_attn_kernel<T, TPR, KV8, FULL, EXT><<<(unsigned)blocks, kThreads, smem, st>>>(p, s, row_blocks, x);
   return cudaGetLastError();
 }
 
 // Threads per row from head_dim: 4 up to 32, 8 up to 64, 16 up to 128, else 32.
 // FULL requires head_dim == 8 * threads-per-row.
-template <typename T, bool KV8, bool FULL>
-cudaError_t launch_simt_k(const Problem& p, const Split& s, cudaStream_t st) {
-  if (p.D <= 32) return launch_simt_f<T, 4, KV8, FULL>(p, s, st);
-  if (p.D <= 64) return launch_simt_f<T, 8, KV8, FULL>(p, s, st);
-  if (p.D <= 128) return launch_simt_f<T, 16, KV8, FULL>(p, s, st);
-  return launch_simt_f<T, 32, KV8, FULL>(p, s, st);
+template <typename T, bool KV8, bool FULL, bool EXT>
+cudaError_t launch_simt_k(const Problem& p, const Split& s, cudaStream_t st, const Ext& x) {
+  if (p.D <= 32) return launch_simt_f<T, 4, KV8, FULL, EXT>(p, s, st, x);
+  if (p.D <= 64) return launch_simt_f<T, 8, KV8, FULL, EXT>(p, s, st, x);
+  if (p.D <= 128) return launch_simt_f<T, 16, KV8, FULL, EXT>(p, s, st, x);
+  return launch_simt_f<T, 32, KV8, FULL, EXT>(p, s, st, x);
 }
 
-template <bool FULL>
-cudaError_t launch_simt_all(const Problem& p, const Split& s, cudaStream_t st) {
+template <bool FULL, bool EXT>
+cudaError_t launch_simt_all(const Problem& p, const Split& s, cudaStream_t st, const Ext& x) {
   switch (p.dtype) {
     case ATTN_F32:
-      return p.kv_int8 ? launch_simt_k<float, true, FULL>(p, s, st) : launch_simt_k<float, false, FULL>(p, s, st);
+      return p.kv_int8 ? launch_simt_k<float, true, FULL, EXT>(p, s, st, x)
+                       : launch_simt_k<float, false, FULL, EXT>(p, s, st, x);
     case ATTN_F16:
-      return p.kv_int8 ? launch_simt_k<__half, true, FULL>(p, s, st) : launch_simt_k<__half, false, FULL>(p, s, st);
+      return p.kv_int8 ? launch_simt_k<__half, true, FULL, EXT>(p, s, st, x)
+                       : launch_simt_k<__half, false, FULL, EXT>(p, s, st, x);
     default:
-      return p.kv_int8 ? launch_simt_k<__nv_bfloat16, true, FULL>(p, s, st)
-                       : launch_simt_k<__nv_bfloat16, false, FULL>(p, s, st);
+      return p.kv_int8 ? launch_simt_k<__nv_bfloat16, true, FULL, EXT>(p, s, st, x)
+                       : launch_simt_k<__nv_bfloat16, false, FULL, EXT>(p, s, st, x);
   }
 }
 

@@ -1,0 +1,82 @@
+// visible.cuh -- key visibility of windows with first keys, and paged caches.
+//
+// A row's visible keys are [lo, fe) and [wl, hi): the first keys of its span
+// and the keys from its window's left end to its diagonal.  A kernel takes the
+// union over its rows, which has the same form, as a list of key tiles without
+// the tiles in the gap, and a split pass takes an equal part of that list.
+#pragma once
+
+#include "common.cuh"
+
+namespace attn {
+
+// First keys and page lists, passed by value next to a Problem.
+struct Ext {
+  int first;             // first keys visible behind the window
+  int page_size;         // 0: K and V are not paged
+  uint32_t n_pages;
+  const int32_t* table;
+  int64_t table_stride;
+};
+
+// Visible keys [lo, fe) and [wl, hi).  When the two meet, or one is empty,
+// fe = lo and [wl, hi) holds them all: a row has a first part only in front
+// of a gap with a window part behind it.
+struct Vis {
+  int lo, fe, wl, hi;
+};
+
+__device__ __forceinline__ Vis row_vis(const Problem& p, int first, int b, int i) {
+  int64_t kl = p.Sk;
+  if (p.klens) kl = clamp64((int64_t)p.klens[b] + p.klens_plus, 0, p.Sk);
+  int64_t hi = kl, lo = 0, wl = 0;
+  if (p.seg) lo = clamp64((int64_t)p.seg[(int64_t)b * p.seg_bs + i], 0, p.Sk);
+  if (p.causal) {
+    const int64_t diag = (int64_t)i + (p.align_klens ? kl - p.Sq : p.coff);
+    hi = min(hi, max(diag + 1, (int64_t)0));
+    if (p.window >= 0) wl = diag - p.window;
+  }
+  lo = min(lo, hi);
+  wl = clamp64(wl, lo, hi);
+  const int64_t fe = min(lo + first, hi);
+  if (fe > lo && wl >= hi) return {(int)lo, (int)lo, (int)lo, (int)fe};   // the window is empty
+  const bool gap = fe < wl && fe > lo;
+  return {(int)lo, (int)(gap ? fe : lo), (int)(fe >= wl ? lo : wl), (int)hi};
+}
+
+__device__ __forceinline__ bool visible(const Vis& v, int k) {
+  return (k >= v.wl && k < v.hi) || (k >= v.lo && k < v.fe);
+}
+
+// The union's tiles of `unit` keys, in key order, without those of the gap.
+struct TileList {
+  int ta, na, tb, n;   // na tiles from tile ta, then n - na tiles from tile tb
+  __device__ __forceinline__ int tile(int i) const { return i < na ? ta + i : tb + (i - na); }
+};
+
+__device__ __forceinline__ TileList tile_list(const Vis& u, int unit) {
+  TileList t;
+  t.ta = u.lo / unit;
+  const int ea = u.fe > u.lo ? (u.fe + unit - 1) / unit : t.ta;   // end of the first part's tiles
+  t.na = ea - t.ta;
+  t.tb = max(u.wl / unit, ea);
+  const int eb = (u.hi + unit - 1) / unit;
+  t.n = t.na + (u.hi > u.wl ? max(eb - t.tb, 0) : 0);
+  return t;
+}
+
+// Part `part` of `parts` of a list of n tiles: [begin, end).
+__device__ __forceinline__ void list_part(int n, int part, int parts, int& begin, int& end) {
+  begin = (int)((int64_t)n * part / parts);
+  end = (int)((int64_t)n * (part + 1) / parts);
+}
+
+// Page of key k of entry b, or -1 when the entry's list names no page of the pool there.
+__device__ __forceinline__ int page_of(const Ext& x, int b, int k) {
+  const int32_t pg = __ldg(x.table + (int64_t)b * x.table_stride + k / x.page_size);
+  return (uint32_t)pg < x.n_pages ? pg : -1;
+}
+
+cudaError_t launch_simt_ext(const Problem& p, const Ext& x, const Split& s, cudaStream_t st);
+
+}  // namespace attn

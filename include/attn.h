@@ -252,6 +252,120 @@ ATTN_API int attn_decode_append(const attn_problem* p, const void* q, const void
                                 void* k_cache, void* v_cache, void* o, const float* mask, const int32_t* k_lens,
                                 float* lse, void* workspace, size_t workspace_bytes, attn_stream stream);
 
+/* ---- Windows with first keys, paged caches, and the step before attention ----------------
+ *
+ * Sliding window with first keys ("com.microsoft.GroupQueryAttention",
+ * attribute local_window_size, extended).  A left window hides everything
+ * behind it; attn_fwd_window and attn_decode_paged also take first_keys: the
+ * first keys of a row's own span stay visible behind the window.  With
+ * s = clamp(seg[b, i], 0, k_len) (0 without seg), key k is visible to row
+ * (b, i) iff
+ *   - k < L_b and k <= i + off_b and k >= s, as above, and
+ *   - k >= i + off_b - window_left, or k < s + first_keys.
+ * Everything else (special values, score transforms, masks, masked rows, LSE)
+ * is as for attn_fwd. */
+
+/* Bytes of device workspace attn_fwd_window needs (0 when none).  The plan
+ * depends on the shape only: with fewer than 304 blocks of 256 query rows
+ * (128 for head_dim above 128), each block's list of visible key tiles is cut
+ * into ceil(304 / blocks) parts, at most 16 and at most one per 1024 keys of
+ * the longest list a block can have (min(k_len, window_left + first_keys +
+ * rows of a block)); p->key_splits >= 1 asks for a count (at most 16).
+ * Returns 0 for an invalid problem; attn_fwd_window then reports the error. */
+ATTN_API size_t attn_fwd_window_workspace_size(const attn_problem* p, int32_t first_keys);
+
+/* attn_fwd with first_keys (>= 0) keys of each row's span visible behind its
+ * window: p->causal must be 1 and p->window_left >= 0, first_keys <= 2^30,
+ * else ATTN_ERR_INVALID_ARG.  Key tiles between the first keys and the window
+ * are neither copied nor computed.  first_keys = 0 is attn_fwd.  Arguments,
+ * workspace rule and errors as for attn_fwd. */
+ATTN_API int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, const void* k, const void* v,
+                             void* o, const float* mask, const int32_t* seg, const int32_t* k_lens, float* lse,
+                             void* workspace, size_t workspace_bytes, attn_stream stream);
+
+/* A paged cache: fixed-size pages of a pool, and for every batch entry a list
+ * of the pages that hold its rows.  Row r of entry b is row r % page_size of
+ * page table[b * table_stride + r / page_size] (int32, DEVICE).  In the
+ * layouts of paged K and V the batch stride is the page stride: element
+ * (page, head, row, e) is at base[offset + page*batch_stride +
+ * head*head_stride + row*row_stride + e], so pools [pages, G, page_size, D]
+ * and [pages, page_size, G, D] are both described.  A table value outside
+ * [0, n_pages) holds no rows: its keys are hidden (a page freed behind a
+ * window, padding of the table) and rows written to it are dropped.  Two
+ * entries may share pages (a common prefix) that only attn_decode_paged
+ * reads. */
+typedef struct {
+  int32_t page_size;      /* rows of a page, >= 1 */
+  int32_t n_pages;        /* pages of the pool, >= 0 */
+  const int32_t* table;   /* [batch] lists of ceil(rows / page_size) values */
+  int64_t table_stride;   /* elements from one entry's list to the next, >= 0 */
+} attn_pages;
+
+/* Bytes of device workspace attn_decode_paged needs; from the shape alone
+ * (batch, heads, k_len, window).  0 for an invalid problem. */
+ATTN_API size_t attn_decode_paged_workspace_size(const attn_problem* p, const attn_pages* pages,
+                                                 int32_t first_keys);
+
+/* attn_decode over a paged cache: q_len must be 1; p->k_len is the number of
+ * rows an entry's list can hold (keys at k_len and behind are not visible;
+ * the list has ceil(k_len / page_size) values); k_pool / v_pool are laid out
+ * by p->k / p->v as above.  Visibility as for attn_fwd with first_keys (which
+ * must be 0 unless p->causal and p->window_left >= 0); seg is not taken.
+ * List values of pages without a visible key are not used.  The number of
+ * ranges the keys are cut into depends on the shape alone and their ends also
+ * on the entry's length: every range holds an equal share of the entry's own
+ * visible keys.  Types, int8 pools, score transforms, mask (columns are the
+ * entry's rows), masked rows and errors as for attn_decode.  Cache rows that
+ * are not visible are never read into the result. */
+ATTN_API int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t first_keys, const void* q,
+                               const void* k_pool, const void* v_pool, void* o, const float* mask,
+                               const int32_t* k_lens, float* lse, void* workspace, size_t workspace_bytes,
+                               attn_stream stream);
+
+/* The step before attention ("com.microsoft.GroupQueryAttention": rotary
+ * embedding with cos / sin caches, half-split or interleaved, and RMS norms
+ * of Q and K for each head), with the cache write in the same pass.  For every
+ * token (b, i) and every row x of head_dim values of Q (each query head) and
+ * K (each kv head):
+ *   y = x * weight / sqrt(mean(x^2) + eps)           with norm (weight 1 when NULL; y = x without norm)
+ *   (y[a], y[c]) <- (y[a] cos - y[c] sin, y[c] cos + y[a] sin)   for j < rot_dim / 2, where
+ *       cos, sin = cos[pos, j], sin[pos, j], and (a, c) = (j, j + rot_dim / 2), or (2j, 2j + 1) interleaved
+ * in float32, rounded once to dtype (or to int8 codes, below).  V is copied.
+ * pos = positions[b * pos_batch_stride + i], clamped to [0, max_pos).  Q goes
+ * to q_out at (b, head, i); K and V go to cache row
+ * r = rows[b * row_batch_stride + i] of entry b.  A row outside
+ * [0, cache_rows) (a padding token) writes no K and V; every other cache row
+ * is left as it was.  Two tokens of one call with the same cache row: which
+ * one the row holds afterwards is not defined. */
+typedef struct {
+  int32_t batch, seq_len;              /* tokens: [batch][seq_len] */
+  int32_t heads, kv_heads, head_dim;   /* head_dim 1..256, even for f16/bf16; heads % kv_heads == 0 */
+  int32_t rot_dim;                     /* rotated leading elements: even, 0..head_dim */
+  int32_t dtype;                       /* of Q, K, V, q_out, the weights and a float cache */
+  int32_t interleaved;                 /* 0: pairs (j, j + rot_dim / 2); 1: pairs (2j, 2j + 1) */
+  int32_t norm;                        /* 1: RMS norm */
+  float eps;                           /* finite, >= 0 */
+  int32_t max_pos;                     /* rows of cos and sin, >= 1 when rot_dim > 0 */
+  int32_t cache_rows;                  /* rows an entry's cache (or its page list) can hold, >= 0 */
+  attn_layout q, k, v;                 /* inputs [batch][head][token] (slices of a packed projection) */
+  attn_layout q_out;                   /* [batch][head][token]; q_out may be q itself */
+  attn_layout k_out, v_out;            /* caches [batch][kv head][row]; with pages [page][kv head][row] */
+  int64_t pos_batch_stride, row_batch_stride;
+  int32_t kv_dtype, kv_scale_kind;     /* ATTN_KV_INT8: codes x / scale, rounded and saturated as */
+  const float* k_scale;                /*   for attn_decode_append (scales are DEVICE float32) */
+  const float* v_scale;
+} attn_prep;
+
+/* positions and rows may be NULL (position i, row i); cos and sin are float32
+ * [max_pos][rot_dim / 2]; q_weight and k_weight are [head_dim] in dtype;
+ * pages is NULL for contiguous caches.  No workspace.  Inputs and outputs must
+ * not overlap except q_out = q with the same layout.  batch == 0 or
+ * seq_len == 0 is a no-op returning ATTN_OK. */
+ATTN_API int attn_qkv_prep(const attn_prep* p, const attn_pages* pages, const void* q, const void* k, const void* v,
+                           const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                           const int32_t* positions, const int32_t* rows, void* q_out, void* k_out, void* v_out,
+                           attn_stream stream);
+
 /* Size in bytes of the fixed scratch array attn_decode_noalloc uses. */
 ATTN_API size_t attn_decode_noalloc_max_scratch(void);
 
