@@ -507,7 +507,10 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   const Problem r = resolve(p, q, k, v, o, mask, seg, k_lens, lse, status);
   const Ext x{first_keys, 0, 0u, nullptr, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rc = from_cuda(launch_simt_ext(r, x, s, st));
+  int used = 0;
+  rc = prefill_tc_first_try(r, first_keys, s, st, &used);
+  if (rc) return rc;
+  if (!used) rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;
   return s.n_splits > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;
 }

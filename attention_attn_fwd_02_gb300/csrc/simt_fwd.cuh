@@ -111,15 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
       }
     }
     __syncthreads();
-    // A row with a first part has a window part, so both parts are set or the first is empty.
-    if (s_hi > s_lo) {
-      uv = {s_lo, s_lo, s_lo, s_hi};
-      if (s_first[1] > s_first[0]) {
-        uv.lo = uv.fe = min(s_first[0], s_lo);
-        if (s_first[1] < s_lo) uv.fe = s_first[1];
-        else uv.wl = uv.lo;
-      }
-    }
+    uv = vis_union(s_first[0], s_first[1], s_lo, s_hi);
     tl = tile_list(uv, kTile);
     tile1 = tl.n;
     if (sp.part_o != nullptr) list_part(tl.n, split, sp.n_splits, tile0, tile1);

@@ -19,9 +19,8 @@ struct Ext {
   int64_t table_stride;
 };
 
-// Visible keys [lo, fe) and [wl, hi).  When the two meet, or one is empty,
-// fe = lo and [wl, hi) holds them all: a row has a first part only in front
-// of a gap with a window part behind it.
+// Visible keys [lo, fe) and [wl, hi).  When the two meet, fe = lo and [wl, hi)
+// holds them all; a row whose window is behind every key has wl = hi = fe.
 struct Vis {
   int lo, fe, wl, hi;
 };
@@ -39,13 +38,28 @@ __device__ __forceinline__ Vis row_vis(const Problem& p, int first, int b, int i
   lo = min(lo, hi);
   wl = clamp64(wl, lo, hi);
   const int64_t fe = min(lo + first, hi);
-  if (fe > lo && wl >= hi) return {(int)lo, (int)lo, (int)lo, (int)fe};   // the window is empty
+  if (fe > lo && wl >= hi) return {(int)lo, (int)fe, (int)fe, (int)fe};   // the window is empty
   const bool gap = fe < wl && fe > lo;
   return {(int)lo, (int)(gap ? fe : lo), (int)(fe >= wl ? lo : wl), (int)hi};
 }
 
 __device__ __forceinline__ bool visible(const Vis& v, int k) {
   return (k >= v.wl && k < v.hi) || (k >= v.lo && k < v.fe);
+}
+
+// Whether every key of [a, z) is visible.
+__device__ __forceinline__ bool within(const Vis& v, int a, int z) {
+  return (a >= v.wl && z <= v.hi) || (a >= v.lo && z <= v.fe);
+}
+
+// The union of rows, from the ends over the rows that have one of first parts
+// [f_lo, f_hi) and window parts [w_lo, w_hi) (low ends at INT_MAX, high ends
+// negative where no row has one).
+__device__ __forceinline__ Vis vis_union(int f_lo, int f_hi, int w_lo, int w_hi) {
+  if (w_hi <= w_lo) return f_hi <= f_lo ? Vis{0, 0, 0, 0} : Vis{f_lo, f_hi, f_hi, f_hi};
+  if (f_hi <= f_lo) return {w_lo, w_lo, w_lo, w_hi};
+  const int lo = min(f_lo, w_lo);
+  return f_hi < w_lo ? Vis{lo, f_hi, w_lo, w_hi} : Vis{lo, lo, lo, w_hi};
 }
 
 // The union's tiles of `unit` keys, in key order, without those of the gap.
@@ -77,6 +91,10 @@ __device__ __forceinline__ int page_of(const Ext& x, int b, int k) {
   return (uint32_t)pg < x.n_pages ? pg : -1;
 }
 
+// The CUDA-core forward with first keys and paged caches.
 cudaError_t launch_simt_ext(const Problem& p, const Ext& x, const Split& s, cudaStream_t st);
+
+// The tensor-core forward with first keys: as prefill_tc_try.
+int prefill_tc_first_try(const Problem& p, int first, const Split& s, cudaStream_t st, int* used);
 
 }  // namespace attn

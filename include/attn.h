@@ -263,7 +263,8 @@ ATTN_API int attn_decode_append(const attn_problem* p, const void* q, const void
  *   - k < L_b and k <= i + off_b and k >= s, as above, and
  *   - k >= i + off_b - window_left, or k < s + first_keys.
  * Everything else (special values, score transforms, masks, masked rows, LSE)
- * is as for attn_fwd. */
+ * is as for attn_fwd.  With seg, keys between the first keys of two documents
+ * that share a query block count as seen by the block (their V is finite). */
 
 /* Bytes of device workspace attn_fwd_window needs (0 when none).  The plan
  * depends on the shape only: with fewer than 304 blocks of 256 query rows
