@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "prefill_tc.h"
 #include "decode.h"
+#include "paged.cuh"
 #include "visible.cuh"
 #include "prep.h"
 
@@ -372,7 +373,7 @@ int check_paged(const attn_problem* p, const attn_pages* pages, int32_t first_ke
   return check_pages(pages, p->k_len);
 }
 
-// attn_decode_paged's plan: ranges of each entry's own visible keys.
+// The CUDA-core pass's plan for a paged cache: ranges of each entry's own visible keys.
 int paged_plan(const attn_problem* p, int32_t first_keys) {
   int64_t span = p->k_len;
   if (p->causal && p->window_left >= 0) {
@@ -385,6 +386,14 @@ int paged_plan(const attn_problem* p, int32_t first_keys) {
   const int64_t tiles = (span + 127) / 128;
   n = n < tiles ? n : tiles;
   return n < 1 ? 1 : (int)n;
+}
+
+// Workspace of attn_decode_paged, whichever pass a call's alignment takes.
+size_t paged_bytes(const attn_problem* p, int32_t first_keys) {
+  int status = 0;
+  const Problem r = resolve(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, &status);
+  const size_t a = decode_ws_bytes(p, paged_plan(p, first_keys)), b = paged_ws_bytes(r);
+  return a > b ? a : b;
 }
 
 }  // namespace
@@ -517,7 +526,7 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
 
 size_t attn_decode_paged_workspace_size(const attn_problem* p, const attn_pages* pages, int32_t first_keys) {
   if (check_paged(p, pages, first_keys) != ATTN_OK) return 0;
-  return decode_ws_bytes(p, paged_plan(p, first_keys));
+  return paged_bytes(p, first_keys);
 }
 
 int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t first_keys, const void* q,
@@ -529,15 +538,18 @@ int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t fi
   rc = check_pointers(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse);
   if (rc) return rc;
   const int n = paged_plan(p, first_keys);
-  if (!workspace || workspace_bytes < decode_ws_bytes(p, n)) return ATTN_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < paged_bytes(p, first_keys)) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
   int* status = nullptr;
   rc = status_ptr(&status);
   if (rc) return rc;
   const Problem r = resolve(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse, status);
   const Ext x{first_keys, pages->page_size, (uint32_t)pages->n_pages, pages->table, pages->table_stride};
-  const Split s = split_in(workspace, (size_t)p->batch * p->heads, n, 0, p->head_dim);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int used = 0;
+  rc = paged_try(r, x, workspace, st, &used);
+  if (rc || used) return rc;
+  const Split s = split_in(workspace, (size_t)p->batch * p->heads, n, 0, p->head_dim);
   rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;
   return from_cuda(launch_combine(r, s, p->dtype, st));

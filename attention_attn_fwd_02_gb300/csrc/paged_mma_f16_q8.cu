@@ -1,0 +1,8 @@
+// paged_mma_f16_q8.cu -- instances of the tensor-core paged decode pass (paged_mma.cuh).
+#include "paged_mma.cuh"
+
+namespace attn {
+namespace paged {
+bool mma_f16_q8(Work& w, bool launch, cudaStream_t st, int* rc) { return pick<false, true>(w, launch, st, rc); }
+}  // namespace paged
+}  // namespace attn
