@@ -514,7 +514,7 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   rc = status_ptr(&status);
   if (rc) return rc;
   const Problem r = resolve(p, q, k, v, o, mask, seg, k_lens, lse, status);
-  const Ext x{first_keys, 0, 0u, nullptr, 0};
+  const Ext x = make_ext(first_keys, nullptr);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int used = 0;
   rc = prefill_tc_first_try(r, first_keys, s, st, &used);
@@ -544,7 +544,7 @@ int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t fi
   rc = status_ptr(&status);
   if (rc) return rc;
   const Problem r = resolve(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse, status);
-  const Ext x{first_keys, pages->page_size, (uint32_t)pages->n_pages, pages->table, pages->table_stride};
+  const Ext x = make_ext(first_keys, pages);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int used = 0;
   rc = paged_try(r, x, workspace, st, &used);

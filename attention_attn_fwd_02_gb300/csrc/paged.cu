@@ -11,6 +11,8 @@ bool mma_f16(Work& w, bool launch, cudaStream_t st, int* rc);
 bool mma_bf16(Work& w, bool launch, cudaStream_t st, int* rc);
 bool mma_f16_q8(Work& w, bool launch, cudaStream_t st, int* rc);
 bool mma_bf16_q8(Work& w, bool launch, cudaStream_t st, int* rc);
+// The CUDA-core pass over float32 caches (paged_f32.cu).
+bool cores_f32(Work& w, bool launch, cudaStream_t st, int* rc);
 
 namespace {
 
@@ -18,7 +20,7 @@ bool pass(Work& w, bool launch, cudaStream_t st, int* rc) {
   const Problem& p = w.p;
   if (p.dtype == ATTN_F16) return p.kv_int8 ? mma_f16_q8(w, launch, st, rc) : mma_f16(w, launch, st, rc);
   if (p.dtype == ATTN_BF16) return p.kv_int8 ? mma_bf16_q8(w, launch, st, rc) : mma_bf16(w, launch, st, rc);
-  return false;
+  return cores_f32(w, launch, st, rc);
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -32,7 +34,8 @@ size_t paged_ws_bytes(const Problem& p) {
   w.p = p;
   int rc = 0;
   if (p.B < 1 || !paged::pass(w, false, nullptr, &rc)) return 0;
-  return paged::round256(paged::rows_of(w) * p.D * 4) + paged::round256(paged::rows_of(w) * 4);
+  return paged::round256(paged::rows_of(w) * p.D * 4) + paged::round256(paged::rows_of(w) * 4) +
+         paged::round256(w.ctas * sizeof(paged::CutUnit));
 }
 
 int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, int* used) {
@@ -52,6 +55,8 @@ int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, 
   w.part_o = static_cast<float*>(workspace);
   w.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                         paged::round256(paged::rows_of(w) * p.D * sizeof(float)));
+  w.cuts = reinterpret_cast<paged::CutUnit*>(reinterpret_cast<char*>(w.part_lse) +
+                                             paged::round256(paged::rows_of(w) * sizeof(float)));
   *used = 1;
   paged::pass(w, true, st, &rc);
   if (rc) return rc;

@@ -26,6 +26,14 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kSlack = 8.0f;   // log2 units: how far a score may rise above the reference maximum
 constexpr unsigned kAll = 0xffffffffu;
 
+// A unit cut by shares, noted by the share that ends it: its fragments are the
+// last one of share c0 (slot 1 when that share began in front of the unit),
+// all of the shares between, and the first one of the noting share.
+struct CutUnit {
+  int b, u;   // b < 0: the share ends no cut unit
+  int c0, late;
+};
+
 struct Work {
   Problem p;
   Ext x;
@@ -35,6 +43,7 @@ struct Work {
   int ctas;        // shares
   float* part_o;   // [ctas][2][heads][D]
   float* part_lse; // [ctas][2][heads]
+  CutUnit* cuts;      // [ctas]
 };
 
 __device__ __forceinline__ int entry_tiles(const Work& w, int b) {
@@ -119,6 +128,107 @@ __device__ __forceinline__ void copy_wait() {
 }
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// The 16-byte unit u of row r of a stage, in bytes: swizzled so that the same
+// unit of 8 neighbouring rows lies in different banks.
+template <int UNITS>
+__device__ __forceinline__ uint32_t swz(int r, int u) {
+  return (uint32_t)(r * UNITS * 16 + ((u ^ (UNITS >= 8 ? r & 7 : (r >> 1) & 3)) << 4));
+}
+
+// A warp's ring of stages.  Each holds KEYS keys of a tile, rows of ROW bytes
+// (elements of ES): K rows, then V rows.  Rows are copied with cp.async from wherever the page
+// list puts them; rows that are hidden or have no page arrive as zeros, and
+// nothing is read for them.
+template <int ROW, int ES, int KEYS, int STAGES>
+struct Ring {
+  static constexpr int kUnits = ROW / 16;
+  static constexpr int kStage = 2 * KEYS * ROW;
+  static constexpr int kBytes = kWarps * STAGES * kStage;
+  static constexpr int kTile = kWarps * KEYS;
+  static constexpr uint32_t kAllKeys = KEYS == 32 ? 0xffffffffu : (1u << (KEYS & 31)) - 1u;
+  const Work& w;
+  Cursor in;               // the next tile to copy
+  const uint8_t *kbase, *vbase;
+  uint32_t ring;           // shared-memory address of this warp's stages
+  int* key;                // [STAGES] first key of a stage
+  uint32_t* vis;           // [STAGES] its visible keys, bit r = row r
+  int units, warp, lane, page;
+  bool one_page, same;
+
+  __device__ __forceinline__ Ring(const Work& work, const Cursor& at, int n_units, uint8_t* smem, int* keys,
+                                  uint32_t* masks)
+      : w(work), in(at), units(n_units), warp(threadIdx.x / 32), lane(threadIdx.x % 32) {
+    const Problem& p = w.p;
+    kbase = static_cast<const uint8_t*>(p.K) + p.k.off * ES;
+    vbase = static_cast<const uint8_t*>(p.V) + p.v.off * ES;
+    ring = smem_u32(smem) + warp * STAGES * kStage;
+    key = keys + warp * STAGES;
+    vis = masks + warp * STAGES;
+    one_page = w.x.page_size % KEYS == 0;   // a stage's keys share a page
+    same = p.k.bs == p.v.bs && p.k.hs == p.v.hs && p.k.rs == p.v.rs;
+    look_up();
+  }
+  // The page of row lane % KEYS of the next tile.
+  __device__ __forceinline__ void look_up() {
+    const int k = in.tl.tile(in.tile) * kTile + warp * KEYS + lane % KEYS;
+    page = visible(in.v, k) ? page_of(w.x, in.b, k) : -1;
+  }
+  // Copies the next tile into stage s; with `more` moves on and looks up the pages of the tile behind it.
+  __device__ __forceinline__ void issue(int s, bool more) {
+    const Problem& p = w.p;
+    const int k0 = in.tl.tile(in.tile) * kTile + warp * KEYS, kr = lane % KEYS;
+    const uint32_t mask = __ballot_sync(kAll, page >= 0);
+    const int g = in.u / w.n_hc, r = k0 + kr - page_index(w.x, k0 + kr) * w.x.page_size, pg = max(page, 0);
+    const int64_t ko = ((int64_t)pg * p.k.bs + (int64_t)g * p.k.hs + (int64_t)r * p.k.rs) * ES;
+    const int64_t vo = same ? ko : ((int64_t)pg * p.v.bs + (int64_t)g * p.v.hs + (int64_t)r * p.v.rs) * ES;
+    if (lane == 0) {
+      key[s] = k0;
+      vis[s] = mask;
+    }
+    const uint32_t dst = ring + s * kStage;
+    constexpr int kPasses = KEYS * kUnits / 32;
+    if constexpr (kUnits <= 32) {
+      // One pass of the lanes copies kRowsPer rows; its swizzle differs from the first pass's by a constant.
+      constexpr int kRowsPer = 32 / kUnits;
+      const int u = lane % kUnits, ru = lane / kUnits;
+      const uint32_t sw = swz<kUnits>(ru, u);
+      auto place = [&](int j) { return dst + (sw ^ (kUnits >= 8 ? ((j * kRowsPer) & 7) << 4 : 0)) + j * kRowsPer * ROW; };
+      if (one_page && (mask & kAllKeys) == kAllKeys) {
+        // Every row of one page: the addresses advance by the row stride.
+        const uint8_t* ks = kbase + __shfl_sync(kAll, ko, 0) + (int64_t)ru * p.k.rs * ES + u * 16;
+        const uint8_t* vs = vbase + __shfl_sync(kAll, vo, 0) + (int64_t)ru * p.v.rs * ES + u * 16;
+        const int64_t kst = (int64_t)kRowsPer * p.k.rs * ES, vst = (int64_t)kRowsPer * p.v.rs * ES;
+#pragma unroll
+        for (int j = 0; j < kPasses; ++j, ks += kst) copy16(place(j), ks, 16);
+#pragma unroll
+        for (int j = 0; j < kPasses; ++j, vs += vst) copy16(place(j) + KEYS * ROW, vs, 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPasses; ++j) {
+          const int row = j * kRowsPer + ru;
+          const int64_t a = __shfl_sync(kAll, ko, row), c = same ? a : __shfl_sync(kAll, vo, row);
+          const int sz = (mask >> row) & 1u ? 16 : 0;
+          copy16(place(j), kbase + a + u * 16, sz);
+          copy16(place(j) + KEYS * ROW, vbase + c + u * 16, sz);
+        }
+      }
+    } else {   // rows of 64 units: two passes a row
+#pragma unroll
+      for (int j = 0; j < kPasses; ++j) {
+        const int row = j / (kUnits / 32), u = j % (kUnits / 32) * 32 + lane;
+        const int64_t a = __shfl_sync(kAll, ko, row), c = same ? a : __shfl_sync(kAll, vo, row);
+        const int sz = (mask >> row) & 1u ? 16 : 0;
+        copy16(dst + swz<kUnits>(row, u), kbase + a + u * 16, sz);
+        copy16(dst + KEYS * ROW + swz<kUnits>(row, u), vbase + c + u * 16, sz);
+      }
+    }
+    if (more) {
+      in.next(w, units);
+      look_up();
+    }
+  }
+};
+
 // Where a row's finished fragment goes.  M: reference maximum in log2 units
 // (-inf: no visible key), L: sum relative to it, a: numerator of element d.
 template <typename T>
@@ -140,9 +250,57 @@ __device__ __forceinline__ void put_row(const Work& w, bool whole, int cta, int 
     p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs] = none ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-// Host: merges the fragments of the units that no single share holds, and
-// fills the rows of entries without a visible key.
+// What a row without a visible key returns, for all heads of entry b.  The
+// CTA's threads share it.
+template <typename T>
+__device__ __forceinline__ void fill_entry(const Work& w, int b) {
+  const Problem& p = w.p;
+  for (int x = threadIdx.x; x < p.H * p.D; x += kThreads) {
+    const int h = x / p.D, d = x - h * p.D;
+    float M = -INFINITY, L = 0.f;
+    if (p.sink_on) fold_sink<true>(M, L, sink_logit(p, h) * kLog2e);
+    const bool none = L == 0.f;
+    static_cast<T*>(p.O)[p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs + d] =
+        from_f32<T>(none ? (p.masked_zero ? 0.f : NAN) : 0.f / L);
+    if (p.lse && d == 0)
+      p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs] = none ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
+}
+
+// What every CTA of a pass does first: the fill of entries without a visible
+// key, and the mark of a share that ends no cut unit.
+template <typename T>
+__device__ __forceinline__ void begin_share(const Work& w, int cta) {
+  for (int b = cta; b < w.p.B; b += w.ctas)
+    if (entry_tiles(w, b) == 0) fill_entry<T>(w, b);
+  if (threadIdx.x == 0) w.cuts[cta].b = -1;
+}
+
+// Notes a cut unit that ends in share `cta` (whose first fragment it is), `first` tiles into its list.
+__device__ __forceinline__ void note_cut(const Work& w, int64_t total, int shares, int64_t t0, int cta,
+                                         const Cursor& c, int first) {
+  const int64_t at = t0 - first;
+  const int c0 = share_of(total, shares, at);
+  w.cuts[cta] = {c.b, c.u, c0, share_begin(total, shares, c0) < at ? 1 : 0};
+}
+
+// Lets the kernel behind this one in the stream start its prologue, and waits
+// in that kernel until everything in front of it is done and visible.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Host: merges the fragments of cut units.  Enqueued right behind the pass.
 cudaError_t launch_join(const Work& w, cudaStream_t st);
+
+// Host: shares of a pass with `ctas` CTAs an SM, never more than there can be tiles.
+inline void plan_shares(Work& w, int tile, int heads, int ctas) {
+  w.unit = tile;
+  w.heads = heads;
+  w.n_hc = (w.p.qpg + heads - 1) / heads;
+  const int64_t most = (int64_t)w.p.B * w.p.G * w.n_hc * (((int64_t)w.p.Sk + tile - 1) / tile);
+  const int64_t n = (int64_t)kSms * ctas;
+  w.ctas = (int)(most < 1 ? 1 : most < n ? most : n);
+}
 
 }  // namespace paged
 

@@ -90,31 +90,27 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t w, bool high) {
 template <bool BF16, bool KV8, int D, int NT>
 struct Cfg {
   static constexpr int kRow = D * (KV8 ? 1 : 2);                  // bytes of a cache row
-  static constexpr int kUnits = kRow / 16;                        // 16-byte units of a row
   static constexpr int kKeys = kRow <= 128 ? 32 : 16;             // keys of a warp's stage
-  static constexpr int kStage = 2 * kKeys * kRow;                 // bytes: K rows, then V rows
-  static constexpr int kStages = 3;
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kStages = 2 * kKeys * kRow > 8192 ? 3 : 2;
+  using Stages = Ring<kRow, KV8 ? 1 : 2, kKeys, kStages>;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRed = kWarps * kHeads * 64 * 4;           // merge buffer: 64 columns at a time
-  static constexpr int kSmem = kRing + kRed;
-  static constexpr int kCtas = kSmem <= 113 * 1024 ? 2 : 1;       // an SM
-  static constexpr int kTile = kWarps * kKeys;
+  static constexpr int kSmem = Stages::kBytes + kRed;
+  // CTAs an SM, by registers (three leave 168 a thread) and shared memory.
+  // More warps beat deeper rings: at head_dim 128 three CTAs of two stages
+  // against two of three, bf16 189.8 -> 183.9 us on the batch of 64 (8192
+  // rows at most), int8 190.6 -> 143.2 us.
+  static constexpr int kCtas = D == 256 ? (KV8 ? 2 : 1) : NT == 2 ? 2 : 3;
 };
-
-// The 16-byte unit u of row r in a stage: swizzled so that the 8 rows an
-// ldmatrix phase reads lie in different banks.
-template <int UNITS>
-__device__ __forceinline__ uint32_t swz(int r, int u) {
-  return (uint32_t)(r * UNITS * 16 + ((u ^ (UNITS >= 8 ? r & 7 : (r >> 1) & 3)) << 4));
-}
 
 // XF: scores under a softcap or an additive mask.
 template <bool BF16, bool KV8, int D, int NT, bool XF>
 __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_mma_kernel(const Work w) {
   using C = Cfg<BF16, KV8, D, NT>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr bool MB = BF16 && !KV8;   // MMA type bf16
+  constexpr bool MBF = BF16 && !KV8;   // MMA type bf16
+  // P and (int8) Q in two halves, except where one f16 value is already eight times finer than a bf16 result.
+  constexpr bool SPLIT = !(BF16 && KV8);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int st_key[kWarps][C::kStages];         // first key of a warp's stage
   __shared__ uint32_t st_vis[kWarps][C::kStages];    // which of its keys are visible
@@ -126,74 +122,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
   const int64_t total = tiles_before(w, p.B, lane) * units;
   const int shares = (int)min((int64_t)w.ctas, total);
   const int cta = blockIdx.x;
+  let_next_start();
+  begin_share<T>(w, cta);
   if (cta >= shares) return;
   const int64_t t0 = share_begin(total, shares, cta);
   const int my = (int)(share_begin(total, shares, cta + 1) - t0);   // tiles of this share
-  Cursor in = seek(w, t0, units, lane), out = in;
+  Cursor out = seek(w, t0, units, lane);   // the tile being computed
 
-  uint8_t* ring = smem + warp * C::kStages * C::kStage;
-  const uint32_t ring_a = smem_u32(ring);
-  constexpr int kEs = KV8 ? 1 : 2;
-  const uint8_t* kbase = static_cast<const uint8_t*>(p.K) + p.k.off * kEs;
-  const uint8_t* vbase = static_cast<const uint8_t*>(p.V) + p.v.off * kEs;
-  const bool one_page = w.x.page_size % C::kKeys == 0;   // a stage's keys share a page
-  const int kr = lane % C::kKeys;                        // the stage row whose page this lane looks up
-
-  // Page of this lane's row of the input cursor's tile.
-  auto look_up = [&]() {
-    const int key = in.tl.tile(in.tile) * C::kTile + warp * C::kKeys + kr;
-    return visible(in.v, key) ? page_of(w.x, in.b, key) : -1;
-  };
-  int page = look_up();
-  // Issues the input cursor's tile into a stage and moves on; `more`: another tile follows.
-  auto issue = [&](int s, bool more) {
-    const int k0 = in.tl.tile(in.tile) * C::kTile + warp * C::kKeys;
-    const uint32_t vis = __ballot_sync(kAll, page >= 0);   // (bit r = row r; 16-key stages repeat)
-    const int g = in.u / w.n_hc;
-    const int r = (k0 + kr) % w.x.page_size;
-    const int64_t ko = ((int64_t)max(page, 0) * p.k.bs + (int64_t)g * p.k.hs + (int64_t)r * p.k.rs) * kEs;
-    const int64_t vo = ((int64_t)max(page, 0) * p.v.bs + (int64_t)g * p.v.hs + (int64_t)r * p.v.rs) * kEs;
-    if (lane == 0) {
-      st_key[warp][s] = k0;
-      st_vis[warp][s] = vis;
-    }
-    const uint32_t dst = ring_a + s * C::kStage;
-    constexpr int kRowsPer = 32 / C::kUnits;   // rows of one pass over the lanes (C::kUnits <= 32)
-    const int u = lane % C::kUnits, ru = lane / C::kUnits;
-    if (one_page && (vis == kAll || (C::kKeys == 16 && (vis & 0xffffu) == 0xffffu))) {
-      // Every row of one page: the addresses advance by the row stride.
-      const uint8_t* ks = kbase + __shfl_sync(kAll, ko, 0) + (int64_t)ru * p.k.rs * kEs + u * 16;
-      const uint8_t* vs = vbase + __shfl_sync(kAll, vo, 0) + (int64_t)ru * p.v.rs * kEs + u * 16;
-      const int64_t kst = (int64_t)kRowsPer * p.k.rs * kEs, vst = (int64_t)kRowsPer * p.v.rs * kEs;
-#pragma unroll
-      for (int j = 0; j < C::kKeys / kRowsPer; ++j)
-        copy16(dst + swz<C::kUnits>(j * kRowsPer + ru, u), ks + j * kst, 16);
-#pragma unroll
-      for (int j = 0; j < C::kKeys / kRowsPer; ++j)
-        copy16(dst + C::kKeys * C::kRow + swz<C::kUnits>(j * kRowsPer + ru, u), vs + j * vst, 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < C::kKeys / kRowsPer; ++j) {
-        const int row = j * kRowsPer + ru;
-        const int64_t a = __shfl_sync(kAll, ko, row), c = __shfl_sync(kAll, vo, row);
-        const int sz = (vis >> row) & 1u ? 16 : 0;
-        copy16(dst + swz<C::kUnits>(row, u), kbase + a + u * 16, sz);
-        copy16(dst + C::kKeys * C::kRow + swz<C::kUnits>(row, u), vbase + c + u * 16, sz);
-      }
-    }
-    if (more) {   // look the next tile's pages up a tile ahead of their use
-      in.next(w, units);
-      page = look_up();
-    }
-  };
+  typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
 #pragma unroll
   for (int s = 0; s < C::kStages - 1; ++s) {
-    if (s < my) issue(s, s + 1 < my);
+    if (s < my) ring.issue(s, s + 1 < my);
     copy_commit();
   }
 
   // Q as the B operand (n = head, k = channels).
-  uint32_t qh[NT][D / 16][2], ql[KV8 ? NT : 1][D / 16][2];
+  uint32_t qh[NT][D / 16][2], ql[KV8 && SPLIT ? NT : 1][D / 16][2];
   float cs[NT][2];   // what a raw product is multiplied by, for the accumulator's two head columns
   auto load_q = [&]() {
     const int g = out.u / w.n_hc, h0 = g * p.qpg + (out.u % w.n_hc) * C::kHeads;
@@ -239,8 +183,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
             const int d = 16 * c + 4 * tig + e;
             v[e] = hh < nh ? to_f32(row[d]) * p.k_scale[p.kv_per_channel ? g * D + d : 0] * up : 0.f;
           }
-          qh[j][c][0] = pack_split<false>(v[0], v[2], ql[j][c][0]);
-          qh[j][c][1] = pack_split<false>(v[1], v[3], ql[j][c][1]);
+          uint32_t rest[2];
+          qh[j][c][0] = pack_split<false>(v[0], v[2], rest[0]);
+          qh[j][c][1] = pack_split<false>(v[1], v[3], rest[1]);
+          if constexpr (SPLIT) {
+            ql[j][c][0] = rest[0];
+            ql[j][c][1] = rest[1];
+          }
         }
         const float down = p.scale * kLog2e * ldexpf(1.f, -ex);
         cs[j][0] = __shfl_sync(kAll, down, 8 * tig);       // heads 2 tig and 2 tig + 1 of the column tile
@@ -271,133 +220,162 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
   const int lk_row = (lane & 7) + ((lane >> 3) & 1) * 8, lk_u = lane >> 4;
   const int lv_row = KV8 ? lk_row : (lane & 7) + (lane >> 4) * 8, lv_u = KV8 ? lane >> 4 : (lane >> 3) & 1;
 
+  // Offsets of their first blocks; block c of a row sits at the offset XOR its unit number (times 16).
+  const uint32_t lk = swz<C::Stages::kUnits>(lk_row, lk_u), lv = swz<C::Stages::kUnits>(lv_row, lv_u);
+
   int first_tile = out.tile, frag = 0;   // where the current fragment began in its unit; its number in this share
   for (int i = 0; i < my; ++i) {
     const int s = i % C::kStages;
-    if (i + C::kStages - 1 < my) issue((i + C::kStages - 1) % C::kStages, i + C::kStages < my);
+    if (i + C::kStages - 1 < my) ring.issue((i + C::kStages - 1) % C::kStages, i + C::kStages < my);
     copy_commit();
     copy_wait<C::kStages - 1>();
     __syncwarp();
-    const uint32_t ks = ring_a + s * C::kStage, vs = ks + C::kKeys * C::kRow;
+    const uint32_t ks = ring.ring + s * C::Stages::kStage, vs = ks + C::kKeys * C::kRow;
     const uint32_t vis = st_vis[warp][s];
+    constexpr int MB = C::kKeys / 16;   // 16-key blocks of a stage, in step: their chains of MMAs overlap
+    float sc[MB][NT][4];
 #pragma unroll
-    for (int mb = 0; mb < C::kKeys / 16; ++mb) {
-      const uint32_t vb = (vis >> (16 * mb)) & 0xffffu;
-      if (vb == 0) continue;
-      float sc[NT][4];
+    for (int mb = 0; mb < MB; ++mb) {
+      // Two accumulators a column tile (even and odd channel blocks): half the chain of dependent MMAs.
+      float sd[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[mb][j][e] = sd[j][e] = 0.f;
       if constexpr (!KV8) {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           uint32_t a[4];
-          ldsm4(ks + swz<C::kUnits>(16 * mb + lk_row, 2 * c + lk_u), a);
+          ldsm4(ks + (lk ^ (32 * c)) + 16 * mb * C::kRow, a);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma<MB>(sc[j], a, qh[j][c][0], qh[j][c][1]);
+          for (int j = 0; j < NT; ++j) mma<MBF>(c % 2 ? sd[j] : sc[mb][j], a, qh[j][c][0], qh[j][c][1]);
         }
       } else {
 #pragma unroll
         for (int c = 0; c < D / 16; c += 2) {   // two 16-channel blocks: keys 0-7 and 8-15 of each
           uint32_t kw[4];
-          ldsm4(ks + swz<C::kUnits>(16 * mb + lk_row, c + lk_u), kw);
+          ldsm4(ks + (lk ^ (16 * c)) + 16 * mb * C::kRow, kw);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const uint32_t a[4] = {half_pair(kw[2 * q], false), half_pair(kw[2 * q + 1], false),
                                    half_pair(kw[2 * q], true), half_pair(kw[2 * q + 1], true)};
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              mma<false>(sc[j], a, qh[j][c + q][0], qh[j][c + q][1]);
-              mma<false>(sc[j], a, ql[j][c + q][0], ql[j][c + q][1]);
+              mma<false>(q ? sd[j] : sc[mb][j], a, qh[j][c + q][0], qh[j][c + q][1]);
+              if constexpr (SPLIT) mma<false>(q ? sd[j] : sc[mb][j], a, ql[j][c + q][0], ql[j][c + q][1]);
             }
           }
         }
       }
-      // Scores in log2 units; hidden keys (rows gid and gid + 8 of the block) become -inf.
-      bool rise = false;
+      // Scores in log2 units.
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float x = sc[j][e] * cs[j][e & 1];
-          const int r = gid + 8 * (e >> 1);
+          float x = (sc[mb][j][e] + sd[j][e]) * cs[j][e & 1];
           if (XF) {
+            const int r = 16 * mb + gid + 8 * (e >> 1);
             if (capped) x = cap2 * tanh_exp2(x * cap_inv);
             const int hh = 8 * j + 2 * tig + (e & 1);
             const int in_kv = (out.u % w.n_hc) * C::kHeads + hh;
-            if (p.M && in_kv < p.qpg && ((vb >> r) & 1u))
+            if (p.M && in_kv < p.qpg && ((vis >> r) & 1u))
               x = fmaf(p.M[p.m.off + (int64_t)out.b * p.m.bs +
-                           (int64_t)(out.u / w.n_hc * p.qpg + in_kv) * p.m.hs + st_key[warp][s] + 16 * mb + r],
+                           (int64_t)(out.u / w.n_hc * p.qpg + in_kv) * p.m.hs + st_key[warp][s] + r],
                        kLog2e, x);
           }
-          sc[j][e] = (vb >> r) & 1u ? x : -INFINITY;
-          rise |= sc[j][e] > m_ref[j][e & 1] + kSlack;
+          sc[mb][j][e] = x;
         }
-      if (__any_sync(kAll, rise)) {
+    }
+    if ((vis & C::Stages::kAllKeys) != C::Stages::kAllKeys) {   // hidden keys
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {   // a column's keys are spread over the lanes of a tig
-            float mx = fmaxf(sc[j][q], sc[j][q + 2]);
-            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-            if (mx > m_ref[j][q] + kSlack) {
-              const float f = ex2_approx(m_ref[j][q] - mx);
-              l[j][q] *= f;
+          for (int e = 0; e < 4; ++e)
+            if (!((vis >> (16 * mb + gid + 8 * (e >> 1))) & 1u)) sc[mb][j][e] = -INFINITY;
+    }
+    // The reference maximum moves only when a score rises above it by more than the slack.
+    float top[NT][2];
+    bool rise = false;
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                o[c][j][q] *= f;
-                o[c][j][q + 2] *= f;
-              }
-              m_ref[j][q] = mx;
-            }
-          }
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        top[j][q] = fmaxf(sc[0][j][q], sc[0][j][q + 2]);
+#pragma unroll
+        for (int mb = 1; mb < MB; ++mb) top[j][q] = fmaxf(top[j][q], fmaxf(sc[mb][j][q], sc[mb][j][q + 2]));
+        rise |= top[j][q] > m_ref[j][q] + kSlack;
       }
-      uint32_t ph[NT][2], pl[NT][2];   // P^T: keys 2 tig, + 1 (then + 8) x head gid
+    if (__any_sync(kAll, rise)) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const float mu0 = m_ref[j][0] == -INFINITY ? 0.f : m_ref[j][0];
-        const float mu1 = m_ref[j][1] == -INFINITY ? 0.f : m_ref[j][1];
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {   // a column's keys are spread over the lanes of a tig
+          float mx = top[j][q];
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+          if (mx > m_ref[j][q] + kSlack) {
+            const float f = ex2_approx(m_ref[j][q] - mx);
+            l[j][q] *= f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[c][j][q] *= f;
+              o[c][j][q + 2] *= f;
+            }
+            m_ref[j][q] = mx;
+          }
+        }
+    }
+    uint32_t ph[MB][NT][2], pl[MB][NT][2];   // P^T: keys 2 tig, + 1 (then + 8) x head gid
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const float mu0 = m_ref[j][0] == -INFINITY ? 0.f : m_ref[j][0];
+      const float mu1 = m_ref[j][1] == -INFINITY ? 0.f : m_ref[j][1];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
         float e[4];
-        e[0] = ex2_approx(sc[j][0] - mu0);
-        e[1] = ex2_approx(sc[j][1] - mu1);
-        e[2] = ex2_approx(sc[j][2] - mu0);
-        e[3] = ex2_approx(sc[j][3] - mu1);
+        e[0] = ex2_approx(sc[mb][j][0] - mu0);
+        e[1] = ex2_approx(sc[mb][j][1] - mu1);
+        e[2] = ex2_approx(sc[mb][j][2] - mu0);
+        e[3] = ex2_approx(sc[mb][j][3] - mu1);
         l[j][0] += e[0] + e[2];
         l[j][1] += e[1] + e[3];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t rest;
-          ph[j][q] = movtrans(pack_split<MB>(e[2 * q], e[2 * q + 1], rest));
-          pl[j][q] = movtrans(rest);
+          ph[mb][j][q] = movtrans(pack_split<MBF>(e[2 * q], e[2 * q + 1], rest));
+          if constexpr (SPLIT) pl[mb][j][q] = movtrans(rest);
         }
       }
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
       if constexpr (!KV8) {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           uint32_t a[4];
-          ldsm4t(vs + swz<C::kUnits>(16 * mb + lv_row, 2 * c + lv_u), a);
+          ldsm4t(vs + (lv ^ (32 * c)) + 16 * mb * C::kRow, a);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            mma<MB>(o[c][j], a, ph[j][0], ph[j][1]);
-            mma<MB>(o[c][j], a, pl[j][0], pl[j][1]);
+            mma<MBF>(o[c][j], a, ph[mb][j][0], ph[mb][j][1]);
+            if constexpr (SPLIT) mma<MBF>(o[c][j], a, pl[mb][j][0], pl[mb][j][1]);
           }
         }
       } else {
 #pragma unroll
         for (int c = 0; c < D / 16; c += 2) {
           uint32_t vw[4];   // (block c, keys 0-7), (c, 8-15), (c + 1, 0-7), (c + 1, 8-15)
-          ldsm4t(vs + swz<C::kUnits>(16 * mb + lv_row, c + lv_u), vw);
+          ldsm4t(vs + (lv ^ (16 * c)) + 16 * mb * C::kRow, vw);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const uint32_t a[4] = {half_pair(vw[2 * q], false), half_pair(vw[2 * q], true),
                                    half_pair(vw[2 * q + 1], false), half_pair(vw[2 * q + 1], true)};
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              mma<false>(o[c + q][j], a, ph[j][0], ph[j][1]);
-              mma<false>(o[c + q][j], a, pl[j][0], pl[j][1]);
+              mma<false>(o[c + q][j], a, ph[mb][j][0], ph[mb][j][1]);
+              if constexpr (SPLIT) mma<false>(o[c + q][j], a, pl[mb][j][0], pl[mb][j][1]);
             }
           }
         }
@@ -425,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
             red_l[warp][8 * j + 2 * tig + q] = x;
           }
         }
-      float* red = reinterpret_cast<float*>(smem + C::kRing);   // [kWarps][kHeads][64]
+      float* red = reinterpret_cast<float*>(smem + C::Stages::kBytes);   // [kWarps][kHeads][64]
 #pragma unroll
       for (int part = 0; part < D / 64; ++part) {
 #pragma unroll
@@ -457,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
         }
         __syncthreads();
       }
+      if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {
@@ -480,16 +459,10 @@ int launch_cfg(Work& w, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Fills in the tile, the head chunks and the shares: two CTAs an SM (their
-// rings fill its shared memory), never more than there can be tiles.
 template <bool BF16, bool KV8, int D, int NT>
 int plan_cfg(Work& w, bool launch, cudaStream_t st) {
   using C = Cfg<BF16, KV8, D, NT>;
-  w.unit = C::kTile;
-  w.heads = C::kHeads;
-  w.n_hc = (w.p.qpg + C::kHeads - 1) / C::kHeads;
-  const int64_t most = (int64_t)w.p.B * w.p.G * w.n_hc * ((w.p.Sk + (int64_t)C::kTile - 1) / C::kTile);
-  w.ctas = (int)max((int64_t)1, min((int64_t)kSms * C::kCtas, most));
+  plan_shares(w, C::Stages::kTile, C::kHeads, C::kCtas);
   if (!launch) return ATTN_OK;
   const bool xf = w.p.softcap > 0.f || w.p.M != nullptr;
   return xf ? launch_cfg<BF16, KV8, D, NT, true>(w, st) : launch_cfg<BF16, KV8, D, NT, false>(w, st);

@@ -17,7 +17,28 @@ struct Ext {
   uint32_t n_pages;
   const int32_t* table;
   int64_t table_stride;
+  uint32_t div_mul;      // k / page_size = umulhi(k, div_mul) >> div_shift for 0 <= k < 2^31 (page_size > 1)
+  int div_shift;
 };
+
+inline Ext make_ext(int first, const attn_pages* pages) {
+  Ext x{first, 0, 0u, nullptr, 0, 0u, 0};
+  if (!pages) return x;
+  x.page_size = pages->page_size;
+  x.n_pages = (uint32_t)pages->n_pages;
+  x.table = pages->table;
+  x.table_stride = pages->table_stride;
+  // With 2^s < d <= 2^(s+1) and m = ceil(2^(32+s) / d) < 2^32: m d - 2^(32+s) < d <= 2^(s+1), so
+  // floor(k m / 2^(32+s)) is exact while k < 2^31.
+  const uint64_t d = (uint64_t)x.page_size;
+  while ((uint64_t)2 << x.div_shift < d) ++x.div_shift;
+  if (d > 1) x.div_mul = (uint32_t)((((uint64_t)1 << (32 + x.div_shift)) + d - 1) / d);
+  return x;
+}
+
+__device__ __forceinline__ int page_index(const Ext& x, int k) {
+  return x.page_size == 1 ? k : (int)(__umulhi((uint32_t)k, x.div_mul) >> x.div_shift);
+}
 
 // Visible keys [lo, fe) and [wl, hi).  When the two meet, fe = lo and [wl, hi)
 // holds them all; a row whose window is behind every key has wl = hi = fe.
@@ -87,7 +108,7 @@ __device__ __forceinline__ void list_part(int n, int part, int parts, int& begin
 
 // Page of key k of entry b, or -1 when the entry's list names no page of the pool there.
 __device__ __forceinline__ int page_of(const Ext& x, int b, int k) {
-  const int32_t pg = __ldg(x.table + (int64_t)b * x.table_stride + k / x.page_size);
+  const int32_t pg = __ldg(x.table + (int64_t)b * x.table_stride + page_index(x, k));
   return (uint32_t)pg < x.n_pages ? pg : -1;
 }
 
