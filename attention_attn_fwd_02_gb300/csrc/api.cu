@@ -350,20 +350,39 @@ int check_window(const attn_problem* p, int32_t first_keys) {
   return ATTN_OK;
 }
 
-// attn_fwd_window's plan: parts of each query block's list of key tiles, by
-// the rule of fwd_plan with the longest list a block can have for the keys.
+// attn_fwd_window's plan: how many parts each query block's list of key tiles
+// is cut into, from the shape alone.  Per count the model adds up, in us: waves
+// of one CTA an SM, each with its part of the longest list a block can have (a
+// 128-key tile of the tensor-core pass takes 1.5, and a CTA about three tiles
+// of fixed cost; the float32 pass takes 2.1 for 32 keys at head_dim 128, its
+// CTAs overlap), and the merge of the parts (its launch, and their float32
+// rows through HBM).
 int window_plan(const attn_problem* p, int32_t first_keys) {
   if (p->k_len <= 0 || p->q_len <= 0 || p->batch <= 0) return 1;
   if (p->key_splits > 0) return p->key_splits < kMaxRanges ? p->key_splits : kMaxRanges;
-  const int rows = p->head_dim <= 128 ? 256 : 128;
-  const int64_t blocks = (int64_t)((p->q_len + rows - 1) / rows) * p->heads * p->batch;
+  const bool cores = p->dtype == ATTN_F32;
+  const int rows = cores ? 32 : p->head_dim <= 128 ? 256 : 128;
+  const int keys = cores ? 32 : 128;
+  const int64_t lines = cores ? (int64_t)p->q_len * (p->heads / p->kv_heads) : p->q_len;   // a group's heads share tiles
+  const int64_t blocks = (lines + rows - 1) / rows * (cores ? p->kv_heads : p->heads) * p->batch;
   if (blocks >= kFillBlocks) return 1;
   int64_t span = (int64_t)p->window_left + first_keys + rows;
   span = span < p->k_len ? span : p->k_len;
-  int64_t n = (kFillBlocks + blocks - 1) / blocks;
-  n = n < kMaxRanges ? n : kMaxRanges;
-  n = n < span / 1024 ? n : span / 1024;
-  return n < 1 ? 1 : (int)n;
+  const int64_t tiles = (span + keys - 1) / keys + 1;
+  const double tile = cores ? 2.1 * p->head_dim / 128 : 1.5;   // us
+  int best = 1;
+  double least = 0;
+  for (int n = 1; n <= kMaxRanges && n <= tiles; ++n) {
+    const int64_t waves = (blocks * n + 151) / 152;
+    double cost = cores ? (double)(waves * ((tiles + n - 1) / n)) * tile
+                        : (double)(waves * ((tiles + n - 1) / n + 3)) * tile;
+    if (n > 1) cost += 4.0 + (double)(blocks * rows * n) * p->head_dim * 8 / 6.5e6;
+    if (n == 1 || cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
 }
 
 int check_paged(const attn_problem* p, const attn_pages* pages, int32_t first_keys) {
@@ -519,6 +538,10 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   int used = 0;
   rc = prefill_tc_first_try(r, first_keys, s, st, &used);
   if (rc) return rc;
+  if (!used) {
+    rc = window_f32_try(r, first_keys, s, st, &used);
+    if (rc) return rc;
+  }
   if (!used) rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;
   return s.n_splits > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;

@@ -12,6 +12,9 @@
 // unit in list order.  The cut depends on the lengths alone, so results are
 // deterministic.
 #pragma once
+#ifndef HINT
+#define HINT 2
+#endif
 
 #include "visible.cuh"
 
@@ -119,7 +122,13 @@ __device__ __forceinline__ Cursor seek(const Work& w, int64_t at, int units, int
 
 // Copies 16 bytes to shared memory without waiting; sz = 0 writes zeros and reads nothing.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int sz) {
+#if HINT == 0
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
+#elif HINT == 1
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
+#else
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
+#endif
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

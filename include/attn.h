@@ -266,13 +266,13 @@ ATTN_API int attn_decode_append(const attn_problem* p, const void* q, const void
  * is as for attn_fwd.  With seg, keys between the first keys of two documents
  * that share a query block count as seen by the block (their V is finite). */
 
-/* Bytes of device workspace attn_fwd_window needs (0 when none).  The plan
- * depends on the shape only: with fewer than 304 blocks of 256 query rows
- * (128 for head_dim above 128), each block's list of visible key tiles is cut
- * into ceil(304 / blocks) parts, at most 16 and at most one per 1024 keys of
- * the longest list a block can have (min(k_len, window_left + first_keys +
- * rows of a block)); p->key_splits >= 1 asks for a count (at most 16).
- * Returns 0 for an invalid problem; attn_fwd_window then reports the error. */
+/* Bytes of device workspace attn_fwd_window needs (0 when none).  With fewer
+ * than 304 blocks of 256 query rows (128 for head_dim above 128) each block's
+ * list of visible key tiles may be cut into up to 16 parts that are merged in
+ * order (float32 [B*H*q_len][parts][head_dim] and [B*H*q_len][parts], each
+ * 256-byte aligned); how many depends on the shape alone, and p->key_splits >=
+ * 1 asks for a count.  Returns 0 for an invalid problem; attn_fwd_window then
+ * reports the error. */
 ATTN_API size_t attn_fwd_window_workspace_size(const attn_problem* p, int32_t first_keys);
 
 /* attn_fwd with first_keys (>= 0) keys of each row's span visible behind its

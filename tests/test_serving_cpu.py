@@ -80,22 +80,32 @@ def _r256(x):
     return (x + 255) // 256 * 256
 
 
-def _parts(B, H, Sq, Sk, D, w, first, ks):
+def _parts(B, H, G, Sq, Sk, D, w, first, ks, f32):
+    """The cost model of the plan, restated: waves of one CTA an SM with their part of the tiles (and, on the
+    tensor cores, three tiles of fixed cost), and the merge."""
     if ks:
         return min(ks, 16)
-    rows = 256 if D <= 128 else 128
-    blocks = -(-Sq // rows) * H * B
+    rows, keys = (32, 32) if f32 else (256 if D <= 128 else 128, 128)
+    blocks = -(-Sq * H // G // rows) * G * B if f32 else -(-Sq // rows) * H * B
     if blocks >= 304:
         return 1
-    return max(1, min(-(-304 // blocks), 16, min(Sk, w + first + rows) // 1024))
+    tiles = -(-min(Sk, w + first + rows) // keys) + 1
+    tile = 2.1 * D / 128 if f32 else 1.5
+
+    def cost(n):
+        return -(-blocks * n // 152) * (-(-tiles // n) + (0 if f32 else 3)) * tile + \
+            (n > 1) * (4.0 + blocks * rows * n * D * 8 / 6.5e6)
+
+    return min(range(1, min(16, tiles) + 1), key=cost)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,H,Sq,Sk,D,w,first,ks", [
     (1, 4, 64, 20000, 128, 4095, 64, 0), (1, 4, 64, 20000, 128, 255, 4, 0), (2, 32, 4096, 4096, 128, 1023, 4, 0),
     (1, 2, 100, 5000, 256, 5000, 10, 0), (1, 2, 100, 500, 64, 63, 2, 5), (1, 1, 9, 900, 64, 63, 2, 40)])
-def test_window_workspace_follows_the_plan(B, H, Sq, Sk, D, w, first, ks):
-    p = window_problem(batch=B, heads=H, kv_heads=1, q_len=Sq, k_len=Sk, head_dim=D, window_left=w, key_splits=ks)
-    n = _parts(B, H, Sq, Sk, D, w, first, ks)
+def test_window_workspace_follows_the_plan(B, H, Sq, Sk, D, w, first, ks, dtype):
+    p = window_problem(dtype=dtype, batch=B, heads=H, kv_heads=1, q_len=Sq, k_len=Sk, head_dim=D, window_left=w, key_splits=ks)
+    n = _parts(B, H, 1, Sq, Sk, D, w, first, ks, dtype == "f32")
     rows = B * H * Sq
     assert attn.attn_fwd_window_workspace_size(p, first) == (0 if n == 1 else _r256(rows * n * D * 4) +
                                                              _r256(rows * n * 4))
