@@ -411,7 +411,7 @@ int paged_plan(const attn_problem* p, int32_t first_keys) {
 size_t paged_bytes(const attn_problem* p, int32_t first_keys) {
   int status = 0;
   const Problem r = resolve(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, &status);
-  const size_t a = decode_ws_bytes(p, paged_plan(p, first_keys)), b = paged_ws_bytes(r);
+  const size_t a = decode_ws_bytes(p, paged_plan(p, first_keys)), b = paged_ws_bytes(r, first_keys);
   return a > b ? a : b;
 }
 

@@ -29,11 +29,12 @@ size_t rows_of(const Work& w) { return (size_t)w.ctas * 2 * w.heads; }
 }  // namespace
 }  // namespace paged
 
-size_t paged_ws_bytes(const Problem& p) {
+size_t paged_ws_bytes(const Problem& p, int first) {
   paged::Work w{};
   w.p = p;
+  w.x.first = first;
   int rc = 0;
-  if (p.B < 1 || !paged::pass(w, false, nullptr, &rc)) return 0;
+  if (p.B < 1 || !paged::pass(w, false, nullptr, &rc) || w.cluster) return 0;
   return paged::round256(paged::rows_of(w) * p.D * 4) + paged::round256(paged::rows_of(w) * 4) +
          paged::round256(w.ctas * sizeof(paged::CutUnit));
 }
@@ -59,8 +60,7 @@ int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, 
                                              paged::round256(paged::rows_of(w) * sizeof(float)));
   *used = 1;
   paged::pass(w, true, st, &rc);
-  if (rc) return rc;
-  return paged::launch_join(w, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return rc;
 }
 
 }  // namespace attn

@@ -11,10 +11,11 @@
 // to two slots of the workspace, and the join kernel merges the fragments of a
 // unit in list order.  The cut depends on the lengths alone, so results are
 // deterministic.
+//
+// Small problems (few units of short lists) take no workspace and no join: a
+// thread-block cluster of up to 8 CTAs holds one unit, each CTA a part of its
+// list, and merges the parts through distributed shared memory.
 #pragma once
-#ifndef HINT
-#define HINT 2
-#endif
 
 #include "visible.cuh"
 
@@ -46,7 +47,8 @@ struct Work {
   int ctas;        // shares
   float* part_o;   // [ctas][2][heads][D]
   float* part_lse; // [ctas][2][heads]
-  CutUnit* cuts;      // [ctas]
+  CutUnit* cuts;   // [ctas]
+  int cluster;     // > 0: CTAs of the cluster that holds one unit (no shares)
 };
 
 __device__ __forceinline__ int entry_tiles(const Work& w, int b) {
@@ -122,13 +124,7 @@ __device__ __forceinline__ Cursor seek(const Work& w, int64_t at, int units, int
 
 // Copies 16 bytes to shared memory without waiting; sz = 0 writes zeros and reads nothing.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int sz) {
-#if HINT == 0
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
-#elif HINT == 1
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
-#else
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
-#endif
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -293,28 +289,119 @@ __device__ __forceinline__ void note_cut(const Work& w, int64_t total, int share
   w.cuts[cta] = {c.b, c.u, c0, share_begin(total, shares, c0) < at ? 1 : 0};
 }
 
+// ---- units held by a cluster ----
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at the same place of CTA `rank`'s shared memory.
+__device__ __forceinline__ float peer(const float* p, uint32_t rank) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+
+// A CTA's part of a unit in shared memory: numerators [heads][D], then
+// reference maxima [heads] and sums [heads].
+struct Part {
+  float *a, *m, *l;
+  __device__ __forceinline__ Part(void* base, int heads, int D)
+      : a(static_cast<float*>(base)), m(a + heads * D), l(m + heads) {}
+  __device__ __forceinline__ void put(int D, int hh, int d, float M, float L, float x) const {
+    a[hh * D + d] = x;
+    if (d == 0) {
+      m[hh] = M;
+      l[hh] = L;
+    }
+  }
+};
+
 // Lets the kernel behind this one in the stream start its prologue, and waits
 // in that kernel until everything in front of it is done and visible.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Merges the parts of the unit (b, heads h0 ..) that the cluster's CTAs hold; each CTA writes its share of the rows.
+template <typename T>
+__device__ __forceinline__ void cluster_join(const Work& w, const Part& part, int b, int h0, int nh) {
+  const int D = w.p.D, n = w.cluster;
+  cluster_sync();
+  for (int x = cluster_rank() * kThreads + threadIdx.x; x < nh * D; x += n * kThreads) {
+    const int hh = x / D, d = x - hh * D;
+    float m[8], l[8], a[8], M = -INFINITY, L = 0.f, A = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      m[q] = q < n ? peer(part.m + hh, q) : -INFINITY;
+      l[q] = q < n ? peer(part.l + hh, q) : 0.f;
+      a[q] = q < n ? peer(part.a + x, q) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) M = fmaxf(M, m[q]);
+    const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float f = ex2_approx(m[q] - mu);
+      L = fmaf(f, l[q], L);
+      A = fmaf(f, a[q], A);
+    }
+    put_row<T>(w, true, 0, 0, b, h0 + hh, hh, d, M, L, A);
+  }
+  cluster_sync();   // no CTA leaves while its part is being read
+}
+
 // Host: merges the fragments of cut units.  Enqueued right behind the pass.
 cudaError_t launch_join(const Work& w, cudaStream_t st);
 
-// Host: shares of a pass with `ctas` CTAs an SM, never more than there can be tiles.
-inline void plan_shares(Work& w, int tile, int heads, int ctas) {
+// Host: the work of a pass with `ctas` CTAs an SM: clusters when all units fit
+// the SMs at once, eight (or as many as the longest list has tiles) CTAs each
+// with at most eight tiles; else shares, never more than there can be tiles.
+// (One sequence of 700 rows, 8 kv heads: 11.3 us of device time in shares.)
+inline void plan_work(Work& w, int tile, int heads, int ctas) {
   w.unit = tile;
   w.heads = heads;
   w.n_hc = (w.p.qpg + heads - 1) / heads;
-  const int64_t most = (int64_t)w.p.B * w.p.G * w.n_hc * (((int64_t)w.p.Sk + tile - 1) / tile);
-  const int64_t n = (int64_t)kSms * ctas;
-  w.ctas = (int)(most < 1 ? 1 : most < n ? most : n);
+  const int64_t units = (int64_t)w.p.B * w.p.G * w.n_hc, n = (int64_t)kSms * ctas;
+  int64_t span = w.p.Sk;
+  if (w.p.causal && w.p.window >= 0) {
+    const int64_t seen = (int64_t)w.p.window + 1 + w.x.first + 2 * tile;   // both parts may end inside tiles
+    span = seen < span ? seen : span;
+  }
+  const int64_t list = (span + tile - 1) / tile, most = units * list;
+  const int64_t cluster = list < 8 ? (list < 1 ? 1 : list) : 8;
+  w.cluster = list <= 64 && units * cluster <= n ? (int)cluster : 0;
+  w.ctas = (int)(w.cluster ? units * cluster : most < 1 ? 1 : most < n ? most : n);
+}
+
+// Host: enqueues a pass, and the join behind shares.
+template <typename Kernel>
+int launch_pass(Kernel kern, const Work& w, int smem, cudaStream_t st) {
+  if (ensure_smem((const void*)kern, smem) != cudaSuccess) return ATTN_ERR_CUDA;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)w.cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)w.ctas);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = w.cluster ? 1 : 0;
+  if (cudaLaunchKernelEx(&c, kern, w) != cudaSuccess) return ATTN_ERR_CUDA;
+  return w.cluster || launch_join(w, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace paged
 
 // Fast passes: *used = 1 when one took the problem.  bytes: workspace they need.
-size_t paged_ws_bytes(const Problem& p);
+size_t paged_ws_bytes(const Problem& p, int first);
 int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, int* used);
 
 }  // namespace attn

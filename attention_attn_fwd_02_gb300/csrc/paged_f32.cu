@@ -48,15 +48,28 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int units = p.G * w.n_hc;
 
-  const int64_t total = tiles_before(w, p.B, lane) * units;
-  const int shares = (int)min((int64_t)w.ctas, total);
   const int cta = blockIdx.x;
-  let_next_start();
-  begin_share<float>(w, cta);
-  if (cta >= shares) return;
-  const int64_t t0 = share_begin(total, shares, cta);
-  const int my = (int)(share_begin(total, shares, cta + 1) - t0);
-  Cursor out = seek(w, t0, units, lane);
+  int64_t total = 0, t0 = 0;
+  int shares = 0, my;   // tiles of this CTA
+  Cursor out;           // the tile being computed
+  if (w.cluster) {
+    const int unit = cta / w.cluster;
+    out.b = unit / units;
+    out.u = unit % units;
+    out.load(w);
+    int end;
+    list_part(out.n, cta % w.cluster, w.cluster, out.tile, end);
+    my = end - out.tile;
+  } else {
+    total = tiles_before(w, p.B, lane) * units;
+    shares = (int)min((int64_t)w.ctas, total);
+    let_next_start();
+    begin_share<float>(w, cta);
+    if (cta >= shares) return;
+    t0 = share_begin(total, shares, cta);
+    my = (int)(share_begin(total, shares, cta + 1) - t0);
+    out = seek(w, t0, units, lane);
+  }
   typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
 #pragma unroll
   for (int s = 0; s < C::kStages - 1; ++s) {
@@ -93,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
   const int key = lane % KEYS, part = lane / KEYS;   // this lane's key of a stage and its share of the elements
   float* my_p = p_s + warp * KEYS * NH;
 
+  const Part mine(smem, NH, D);   // (cluster: over the stages, once they are done)
   int first_tile = out.tile, frag = 0;
   for (int i = 0; i < my; ++i) {
     const int s = i % C::kStages;
@@ -234,11 +248,12 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
             L = fmaf(f, red_l[v][hb + z], L);
             a = fmaf(f, red[(v * 4 + z) * D + d], a);
           }
-          put_row<float>(w, whole, cta, slot, out.b, h0 + hb + z, hb + z, d, M, L, a);
+          if (w.cluster) mine.put(D, hb + z, d, M, L, a);
+          else put_row<float>(w, whole, cta, slot, out.b, h0 + hb + z, hb + z, d, M, L, a);
         }
         __syncthreads();
       }
-      if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
+      if (!w.cluster && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {
@@ -251,27 +266,27 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
     }
   }
   copy_wait<0>();
-}
-
-template <int D, int NH, bool XF>
-int launch_cfg(const Work& w, cudaStream_t st) {
-  auto kern = paged_f32_kernel<D, NH, XF>;
-  if (ensure_smem((const void*)kern, CfgF32<D, NH>::kSmem) != cudaSuccess) return ATTN_ERR_CUDA;
-  kern<<<w.ctas, kThreads, CfgF32<D, NH>::kSmem, st>>>(w);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (w.cluster) {
+    const int g = out.u / w.n_hc, h0 = g * p.qpg + out.u % w.n_hc * NH;
+    const int nh = min(NH, (g + 1) * p.qpg - h0);
+    if (my == 0)
+      for (int x = threadIdx.x; x < nh * D; x += kThreads) mine.put(D, x / D, x % D, -INFINITY, 0.f, 0.f);
+    cluster_join<float>(w, mine, out.b, h0, nh);
+  }
 }
 
 template <int D, int NH>
-int plan_cfg(Work& w, bool launch, cudaStream_t st) {
+int pass_cfg(Work& w, bool launch, cudaStream_t st) {
   using C = CfgF32<D, NH>;
-  plan_shares(w, C::Stages::kTile, NH, C::kCtas);
+  plan_work(w, C::Stages::kTile, NH, C::kCtas);
   if (!launch) return ATTN_OK;
-  return w.p.softcap > 0.f || w.p.M ? launch_cfg<D, NH, true>(w, st) : launch_cfg<D, NH, false>(w, st);
+  return w.p.softcap > 0.f || w.p.M ? launch_pass(paged_f32_kernel<D, NH, true>, w, C::kSmem, st)
+                                    : launch_pass(paged_f32_kernel<D, NH, false>, w, C::kSmem, st);
 }
 
 template <int D>
-int plan_heads(Work& w, bool launch, cudaStream_t st) {
-  return w.p.qpg <= 4 ? plan_cfg<D, 4>(w, launch, st) : plan_cfg<D, 8>(w, launch, st);
+int pass_heads(Work& w, bool launch, cudaStream_t st) {
+  return w.p.qpg <= 4 ? pass_cfg<D, 4>(w, launch, st) : pass_cfg<D, 8>(w, launch, st);
 }
 
 }  // namespace
@@ -279,9 +294,9 @@ int plan_heads(Work& w, bool launch, cudaStream_t st) {
 bool cores_f32(Work& w, bool launch, cudaStream_t st, int* rc) {
   if (w.p.kv_int8) return false;
   switch (w.p.D) {
-    case 64: *rc = plan_heads<64>(w, launch, st); return true;
-    case 128: *rc = plan_heads<128>(w, launch, st); return true;
-    case 256: *rc = plan_heads<256>(w, launch, st); return true;
+    case 64: *rc = pass_heads<64>(w, launch, st); return true;
+    case 128: *rc = pass_heads<128>(w, launch, st); return true;
+    case 256: *rc = pass_heads<256>(w, launch, st); return true;
     default: return false;
   }
 }

@@ -119,16 +119,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gid = lane >> 2, tig = lane & 3;
   const int units = p.G * w.n_hc;
 
-  const int64_t total = tiles_before(w, p.B, lane) * units;
-  const int shares = (int)min((int64_t)w.ctas, total);
   const int cta = blockIdx.x;
-  let_next_start();
-  begin_share<T>(w, cta);
-  if (cta >= shares) return;
-  const int64_t t0 = share_begin(total, shares, cta);
-  const int my = (int)(share_begin(total, shares, cta + 1) - t0);   // tiles of this share
-  Cursor out = seek(w, t0, units, lane);   // the tile being computed
-
+  int64_t total = 0, t0 = 0;
+  int shares = 0, my;   // tiles of this CTA
+  Cursor out;           // the tile being computed
+  if (w.cluster) {
+    const int unit = cta / w.cluster;
+    out.b = unit / units;
+    out.u = unit % units;
+    out.load(w);
+    int end;
+    list_part(out.n, cta % w.cluster, w.cluster, out.tile, end);
+    my = end - out.tile;
+  } else {
+    total = tiles_before(w, p.B, lane) * units;
+    shares = (int)min((int64_t)w.ctas, total);
+    let_next_start();
+    begin_share<T>(w, cta);
+    if (cta >= shares) return;
+    t0 = share_begin(total, shares, cta);
+    my = (int)(share_begin(total, shares, cta + 1) - t0);
+    out = seek(w, t0, units, lane);
+  }
   typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
 #pragma unroll
   for (int s = 0; s < C::kStages - 1; ++s) {
@@ -223,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
   // Offsets of their first blocks; block c of a row sits at the offset XOR its unit number (times 16).
   const uint32_t lk = swz<C::Stages::kUnits>(lk_row, lk_u), lv = swz<C::Stages::kUnits>(lv_row, lv_u);
 
+  const Part mine(smem, C::kHeads, D);   // (cluster: over the stages, once they are done)
   int first_tile = out.tile, frag = 0;   // where the current fragment began in its unit; its number in this share
   for (int i = 0; i < my; ++i) {
     const int s = i % C::kStages;
@@ -431,11 +444,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
           }
           const int dd = 64 * part + d;
           if (KV8) a *= p.v_scale[p.kv_per_channel ? g * D + dd : 0];
-          put_row<T>(w, whole, cta, slot, out.b, h0 + hh, hh, dd, M, L, a);
+          if (w.cluster) mine.put(D, hh, dd, M, L, a);
+          else put_row<T>(w, whole, cta, slot, out.b, h0 + hh, hh, dd, M, L, a);
         }
         __syncthreads();
       }
-      if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
+      if (!w.cluster && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {
@@ -448,24 +462,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
     }
   }
   copy_wait<0>();
+  if (w.cluster) {
+    const int g = out.u / w.n_hc, h0 = g * p.qpg + (out.u % w.n_hc) * C::kHeads;
+    const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
+    if (my == 0)
+      for (int x = threadIdx.x; x < nh * D; x += kThreads) mine.put(D, x / D, x % D, -INFINITY, 0.f, 0.f);
+    cluster_join<T>(w, mine, out.b, h0, nh);
+  }
 }
 
-template <bool BF16, bool KV8, int D, int NT, bool XF>
-int launch_cfg(Work& w, cudaStream_t st) {
-  using C = Cfg<BF16, KV8, D, NT>;
-  auto kern = paged_mma_kernel<BF16, KV8, D, NT, XF>;
-  if (ensure_smem((const void*)kern, C::kSmem) != cudaSuccess) return ATTN_ERR_CUDA;
-  kern<<<w.ctas, kThreads, C::kSmem, st>>>(w);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-}
-
+// Plans the pass; with `launch` enqueues it.
 template <bool BF16, bool KV8, int D, int NT>
-int plan_cfg(Work& w, bool launch, cudaStream_t st) {
+int pass_cfg(Work& w, bool launch, cudaStream_t st) {
   using C = Cfg<BF16, KV8, D, NT>;
-  plan_shares(w, C::Stages::kTile, C::kHeads, C::kCtas);
+  plan_work(w, C::Stages::kTile, C::kHeads, C::kCtas);
   if (!launch) return ATTN_OK;
-  const bool xf = w.p.softcap > 0.f || w.p.M != nullptr;
-  return xf ? launch_cfg<BF16, KV8, D, NT, true>(w, st) : launch_cfg<BF16, KV8, D, NT, false>(w, st);
+  return w.p.softcap > 0.f || w.p.M ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true>, w, C::kSmem, st)
+                                    : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false>, w, C::kSmem, st);
 }
 
 // Two column tiles of heads a unit for more than eight heads a kv head (at
@@ -475,9 +488,9 @@ template <bool BF16, bool KV8>
 bool pick(Work& w, bool launch, cudaStream_t st, int* rc) {
   const bool two = w.p.qpg > 8;
   switch (w.p.D) {
-    case 64: *rc = two ? plan_cfg<BF16, KV8, 64, 2>(w, launch, st) : plan_cfg<BF16, KV8, 64, 1>(w, launch, st); return true;
-    case 128: *rc = two ? plan_cfg<BF16, KV8, 128, 2>(w, launch, st) : plan_cfg<BF16, KV8, 128, 1>(w, launch, st); return true;
-    case 256: *rc = plan_cfg<BF16, KV8, 256, 1>(w, launch, st); return true;
+    case 64: *rc = two ? pass_cfg<BF16, KV8, 64, 2>(w, launch, st) : pass_cfg<BF16, KV8, 64, 1>(w, launch, st); return true;
+    case 128: *rc = two ? pass_cfg<BF16, KV8, 128, 2>(w, launch, st) : pass_cfg<BF16, KV8, 128, 1>(w, launch, st); return true;
+    case 256: *rc = pass_cfg<BF16, KV8, 256, 1>(w, launch, st); return true;
     default: return false;
   }
 }

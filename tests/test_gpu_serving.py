@@ -171,6 +171,19 @@ PAGED = [
     ("f32", 128, 4, 2, 16, [200, 90], dict(slack=1)),
     ("bf16", 128, 4, 2, 16, [600, 90], dict(cap=500)),                       # lengths beyond max_rows
     ("bf16", 128, 2, 2, 16, [9000], {}),
+    # long lists and many units: shares that cut units, entries without keys among them
+    ("bf16", 128, 8, 2, 16, [9000, 0, 4321, 1], dict(nhd=True)),
+    ("f16", 64, 6, 2, 64, [6000, 4097, 17], dict(window=5000, first=200)),
+    ("f32", 64, 4, 2, 16, [5000, 0, 3], dict(sink=True)),
+    ("f32", 128, 6, 1, 32, [7000, 5000], {}),
+    ("bf16", 128, 4, 1, 32, [9000, 8191], dict(i8="channel")),
+    ("f16", 128, 20, 1, 16, [5000, 4500], dict(mask=True, zero=False)),
+    ("f16", 256, 2, 1, 16, [5000, 77], dict(smooth=True)),
+    ("bf16", 64, 8, 8, 16, [37 * i % 500 for i in range(70)], {}),
+    ("f32", 64, 8, 8, 8, [29 * i % 200 for i in range(70)], dict(bad=True)),
+    ("f16", 128, 8, 8, 16, [61 * i % 400 for i in range(65)], dict(window=50, first=3, sink=True)),
+    ("bf16", 128, 2, 1, 16, [0, 0, 0], dict(sink=True)),
+    ("f16", 128, 8, 8, 16, [0] * 60, dict(zero=False)),
 ]
 
 
