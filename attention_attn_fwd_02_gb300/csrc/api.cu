@@ -536,7 +536,7 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   const Ext x = make_ext(first_keys, nullptr);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int used = 0;
-  rc = prefill_tc_first_try(r, first_keys, s, st, &used);
+  rc = window_tc_try(r, first_keys, s, st, &used);
   if (rc) return rc;
   if (!used) {
     rc = window_f32_try(r, first_keys, s, st, &used);

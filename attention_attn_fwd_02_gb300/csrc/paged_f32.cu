@@ -30,7 +30,7 @@ struct CfgF32 {
   static constexpr int kCtas = kSmem <= 74 * 1024 ? 3 : 2;
 };
 
-template <int D, int NH, bool XF>
+template <int D, int NH, bool XF, bool CL>
 __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kernel(const Work w) {
   using C = CfgF32<D, NH>;
   constexpr int U = C::Stages::kUnits;              // 16-byte units of a row
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
   int64_t total = 0, t0 = 0;
   int shares = 0, my;   // tiles of this CTA
   Cursor out;           // the tile being computed
-  if (w.cluster) {
+  if constexpr (CL) {
     const int unit = cta / w.cluster;
     out.b = unit / units;
     out.u = unit % units;
@@ -248,12 +248,12 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
             L = fmaf(f, red_l[v][hb + z], L);
             a = fmaf(f, red[(v * 4 + z) * D + d], a);
           }
-          if (w.cluster) mine.put(D, hb + z, d, M, L, a);
+          if constexpr (CL) mine.put(D, hb + z, d, M, L, a);
           else put_row<float>(w, whole, cta, slot, out.b, h0 + hb + z, hb + z, d, M, L, a);
         }
         __syncthreads();
       }
-      if (!w.cluster && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
+      if (!CL && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
     }
   }
   copy_wait<0>();
-  if (w.cluster) {
+  if constexpr (CL) {
     const int g = out.u / w.n_hc, h0 = g * p.qpg + out.u % w.n_hc * NH;
     const int nh = min(NH, (g + 1) * p.qpg - h0);
     if (my == 0)
@@ -280,8 +280,12 @@ int pass_cfg(Work& w, bool launch, cudaStream_t st) {
   using C = CfgF32<D, NH>;
   plan_work(w, C::Stages::kTile, NH, C::kCtas);
   if (!launch) return ATTN_OK;
-  return w.p.softcap > 0.f || w.p.M ? launch_pass(paged_f32_kernel<D, NH, true>, w, C::kSmem, st)
-                                    : launch_pass(paged_f32_kernel<D, NH, false>, w, C::kSmem, st);
+  const bool xf = w.p.softcap > 0.f || w.p.M != nullptr;
+  if (w.cluster)
+    return xf ? launch_pass(paged_f32_kernel<D, NH, true, true>, w, C::kSmem, st)
+              : launch_pass(paged_f32_kernel<D, NH, false, true>, w, C::kSmem, st);
+  return xf ? launch_pass(paged_f32_kernel<D, NH, true, false>, w, C::kSmem, st)
+            : launch_pass(paged_f32_kernel<D, NH, false, false>, w, C::kSmem, st);
 }
 
 template <int D>

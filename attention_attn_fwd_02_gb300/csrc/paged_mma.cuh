@@ -103,8 +103,8 @@ struct Cfg {
   static constexpr int kCtas = D == 256 ? (KV8 ? 2 : 1) : NT == 2 ? 2 : 3;
 };
 
-// XF: scores under a softcap or an additive mask.
-template <bool BF16, bool KV8, int D, int NT, bool XF>
+// XF: scores under a softcap or an additive mask.  CL: units held by clusters.
+template <bool BF16, bool KV8, int D, int NT, bool XF, bool CL>
 __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_mma_kernel(const Work w) {
   using C = Cfg<BF16, KV8, D, NT>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
   int64_t total = 0, t0 = 0;
   int shares = 0, my;   // tiles of this CTA
   Cursor out;           // the tile being computed
-  if (w.cluster) {
+  if constexpr (CL) {
     const int unit = cta / w.cluster;
     out.b = unit / units;
     out.u = unit % units;
@@ -444,12 +444,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
           }
           const int dd = 64 * part + d;
           if (KV8) a *= p.v_scale[p.kv_per_channel ? g * D + dd : 0];
-          if (w.cluster) mine.put(D, hh, dd, M, L, a);
+          if constexpr (CL) mine.put(D, hh, dd, M, L, a);
           else put_row<T>(w, whole, cta, slot, out.b, h0 + hh, hh, dd, M, L, a);
         }
         __syncthreads();
       }
-      if (!w.cluster && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
+      if (!CL && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
     }
   }
   copy_wait<0>();
-  if (w.cluster) {
+  if constexpr (CL) {
     const int g = out.u / w.n_hc, h0 = g * p.qpg + (out.u % w.n_hc) * C::kHeads;
     const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
     if (my == 0)
@@ -477,8 +477,12 @@ int pass_cfg(Work& w, bool launch, cudaStream_t st) {
   using C = Cfg<BF16, KV8, D, NT>;
   plan_work(w, C::Stages::kTile, C::kHeads, C::kCtas);
   if (!launch) return ATTN_OK;
-  return w.p.softcap > 0.f || w.p.M ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true>, w, C::kSmem, st)
-                                    : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false>, w, C::kSmem, st);
+  const bool xf = w.p.softcap > 0.f || w.p.M != nullptr;
+  if (w.cluster)
+    return xf ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true, true>, w, C::kSmem, st)
+              : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false, true>, w, C::kSmem, st);
+  return xf ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true, false>, w, C::kSmem, st)
+            : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false, false>, w, C::kSmem, st);
 }
 
 // Two column tiles of heads a unit for more than eight heads a kv head (at

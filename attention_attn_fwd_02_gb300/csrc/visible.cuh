@@ -116,7 +116,7 @@ __device__ __forceinline__ int page_of(const Ext& x, int b, int k) {
 cudaError_t launch_simt_ext(const Problem& p, const Ext& x, const Split& s, cudaStream_t st);
 
 // The tensor-core and float32 forwards with first keys: as prefill_tc_try.
-int prefill_tc_first_try(const Problem& p, int first, const Split& s, cudaStream_t st, int* used);
+int window_tc_try(const Problem& p, int first, const Split& sp, cudaStream_t st, int* used);
 int window_f32_try(const Problem& p, int first, const Split& s, cudaStream_t st, int* used);
 
 }  // namespace attn

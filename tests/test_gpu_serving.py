@@ -112,6 +112,26 @@ def test_window(i, bshd):
     assert torch.equal(got.nan_to_num(7.0), again.nan_to_num(7.0)) and torch.equal(got_l, again_l)
 
 
+def test_window_many_items_a_cta():
+    """More query blocks than SMs: each CTA runs several items, with entries of no, few and all keys between."""
+    c = ("bf16", 64, 5, 8, 2, 1100, 1400, 200, 3, dict(lens=[1400, 0, 1100, 7, 1250]))
+    (q, k, v), kw, (o, lse, tol, tol_l) = window_case(c, 77, False)
+    got, got_l = attn.fwd(q, k, v, **kw)
+    ref.check(got, o, tol, "O")
+    ref.check(got_l, lse, tol_l, "LSE")
+
+
+def test_window_bounded_wait():
+    """A copy that never lands ends in a status; the next call is right."""
+    (q, k, v), kw, (o, lse, tol, tol_l) = window_case(WINDOW[0], 100, False)
+    attn.attn_test_inject(attn.ATTN_INJECT_DROP_FIRST_COPY)
+    attn.fwd(q, k, v, **kw)
+    assert attn.attn_device_status() == attn.ATTN_ERR_DEVICE_TIMEOUT
+    got, got_l = attn.fwd(q, k, v, **kw)
+    assert attn.attn_device_status() == attn.ATTN_OK
+    ref.check(got, o, tol, "O")
+
+
 def test_window_without_first_keys_is_attn_fwd():
     (q, k, v), kw, _ = window_case(WINDOW[0], 3, False)
     kw = dict(kw, first_keys=0)
