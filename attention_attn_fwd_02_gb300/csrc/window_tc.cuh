@@ -65,6 +65,7 @@ struct Item {
   int ta, na, tb, n;     // its tiles, as in TileList, from the part's first
   int n0;                // the tiles of query tile 0: the first n0
   int skip1;             // a tile that query tile 1 leaves out (-1: none)
+  int some1;             // query tile 1 has a row
   __device__ __forceinline__ int key(int i) const { return (i < na ? ta + i : tb + (i - na)) * BN; }
   // A tile of at most kShort first keys and nothing else: only its first kShort columns are computed.
   __device__ __forceinline__ bool is_short(int i) const {
@@ -190,8 +191,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int hi_0 = -1, w_lo1 = 0x7fffffff, f_hi1 = -1;                    // query tile 0's end; tile 1's starts
       for (int r = lane; r < 2 * BM; r += 32) {
         const int tt = r / BM, row = pair_heads ? r % BM : q0 + r;
-        Vis v{0, 0, 0, 0};
-        if (row < p.Sq && h + tt * ht_step < (g + 1) * p.qpg) v = row_vis(p, first, b, row);
+        // A row that does not exist hides nothing (its zero queries cost it no
+        // pass of its own; it is not written) and has no part in the union.
+        if (row >= p.Sq || h + tt * ht_step >= (g + 1) * p.qpg) {
+          row_v[buf][r] = {0, 0, 0, 0x7fffffff};
+          continue;
+        }
+        const Vis v = row_vis(p, first, b, row);
         row_v[buf][r] = v;
         if (v.hi > v.wl) {
           w_lo = min(w_lo, v.wl);
@@ -235,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.n0 = min(max(n0 - i0, 0), it.n);
         // The window's first tile, when it ends in front of query tile 1's windows and holds none of its first keys.
         const bool skip = tl.na < tl.n && (tl.tb + 1) * BN <= w_lo1 && tl.tb * BN >= f_hi1;
+        it.some1 = pair_heads ? h + 1 < (g + 1) * p.qpg : q0 + BM < p.Sq;
         it.skip1 = skip && tl.na >= i0 && tl.na < i1 ? tl.na - i0 : -1;
       }
       __syncwarp();
@@ -335,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = k & 1;
       if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
       const int n = items[buf].n, n0 = items[buf].n0, skip1 = items[buf].skip1;
+      const bool some1 = items[buf].some1 != 0;
       if (n > 0) {
         if (!(ok = wait_warp(&sb.q_full, (uint32_t)nq & 1u, &sb.abort, p.status))) break;
         ++nq;
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         issued = true;
         bool small = !XF && items[buf].is_short(0);
         if (n0 > 0) issue_qk(0, gt % C::kStages, small);
-        if (skip1 != 0) issue_qk(1, gt % C::kStages, small);
+        if (some1 && skip1 != 0) issue_qk(1, gt % C::kStages, small);
         mma_commit_w(&sb.k_empty[gt % C::kStages]);
         if (n == 1) mma_commit_w(&sb.q_empty);
         bool start0 = true, start1 = true;
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i, ++gt) {
           const int s = gt % C::kStages, s1 = (gt + 1) % C::kStages;
           const uint32_t ph = (uint32_t)(gt / C::kStages) & 1u, ph1 = (uint32_t)((gt + 1) / C::kStages) & 1u;
-          const bool more = i + 1 < n, has0 = i < n0, has1 = i != skip1;
+          const bool more = i + 1 < n, has0 = i < n0, has1 = some1 && i != skip1;
           const bool rp0 = !has0 || mbar_test(&sb.p_full[0], (uint32_t)c0 & 1u);
           if (!(ok = wait_ready(rv, &sb.v_full[s], ph, &sb.abort, p.status))) break;
           // Zero the V rows of keys no row of this item sees (they may hold
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit_w(&sb.v_empty[s]);
           if (more) {
-            if (i + 1 != skip1) issue_qk(1, s1, next_small);
+            if (some1 && i + 1 != skip1) issue_qk(1, s1, next_small);
             mma_commit_w(&sb.k_empty[s1]);
             if (i + 2 == n) mma_commit_w(&sb.q_empty);   // that was the item's last S
           }
@@ -435,10 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && k < my_items; ++k) {
       const int buf = k & 1;
       if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
-      const int n = items[buf].n, n_my = t ? n : items[buf].n0, skip = t ? items[buf].skip1 : -1;
+      const int n = items[buf].n, n_my = t ? (items[buf].some1 ? n : 0) : items[buf].n0;
+      const int skip = t ? items[buf].skip1 : -1;
       const int h = items[buf].h + t * ht_step, b = items[buf].b;
       const int qrow = items[buf].q0 + t * rt_step + r;
       const Vis* rv = &row_v[buf][t * BM + r];
+      const bool valid = qrow < p.Sq && h < (items[buf].g + 1) * p.qpg;
+      const bool idle = !__any_sync(0xffffffffu, valid);   // no row of this warp exists: its P is not used
       const float* mrow = nullptr;
       if (XF && p.M && qrow < p.Sq)
         mrow = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)h * p.m.hs + (int64_t)qrow * p.m.rs;
@@ -539,8 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < (N + 63) / 64; ++c) tmem_st32(s_tm + c * 32, x + c * 32);
         };
-        if (!XF && items[buf].is_short(i)) step(std::integral_constant<int, kShort>());
-        else step(std::integral_constant<int, BN>());
+        if (!idle) {
+          if (!XF && items[buf].is_short(i)) step(std::integral_constant<int, kShort>());
+          else step(std::integral_constant<int, BN>());
+        }
         if (__any_sync(0xffffffffu, rescale)) {
           // P V of the previous tile must have landed in O before it is scaled.
           if (!(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
@@ -566,7 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue: O / l, special rows, LSE ----
       if (done > 0 && !(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
       fence_after();
-      const bool valid = qrow < p.Sq && h < (items[buf].g + 1) * p.qpg;
       const bool split = sp.n_splits > 1;
       // The sink logit joins the denominator (and rescales the accumulated O); with parts the merge adds it once.
       const float o_mul = p.sink_on && !split ? fold_sink<true>(m_ref, l, sink_logit(p, h) * kLog2e) : 1.f;
