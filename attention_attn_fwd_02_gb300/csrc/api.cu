@@ -351,37 +351,48 @@ int check_window(const attn_problem* p, int32_t first_keys) {
 }
 
 // attn_fwd_window's plan: how many parts each query block's list of key tiles
-// is cut into, from the shape alone.  Per count the model adds up, in us: waves
-// of one CTA an SM, each with its part of the longest list a block can have (a
-// 128-key tile of the tensor-core pass takes 1.5, and a CTA about three tiles
-// of fixed cost; the float32 pass takes 2.1 for 32 keys at head_dim 128, its
-// CTAs overlap), and the merge of the parts (its launch, and their float32
-// rows through HBM).
-int window_plan(const attn_problem* p, int32_t first_keys) {
+// is cut into, from the shape alone; key_splits asks for a count.  Parts that
+// the plan chooses for f16/bf16 are the CTAs of a cluster and take no
+// workspace (*cluster = 1); the others are merged through it.
+//
+// Per count a model adds up, in us, what was measured on a GB300.  f16/bf16: a
+// CTA has 10 of fixed cost and 1.4 a 128-key tile, one CTA an SM; a cluster's
+// merge takes 2; the clusters must fit the SMs at once (a cluster lies within
+// one GPC, so larger ones leave some SMs out).  float32: 2.1 for 32 keys at
+// head_dim 128, CTAs overlap, and the merge takes its launch and its rows'
+// way through HBM.
+int window_plan(const attn_problem* p, int32_t first_keys, int* cluster) {
+  *cluster = 0;
   if (p->k_len <= 0 || p->q_len <= 0 || p->batch <= 0) return 1;
   if (p->key_splits > 0) return p->key_splits < kMaxRanges ? p->key_splits : kMaxRanges;
-  const bool cores = p->dtype == ATTN_F32;
-  const int rows = cores ? 32 : p->head_dim <= 128 ? 256 : 128;
-  const int keys = cores ? 32 : 128;
-  const int64_t lines = cores ? (int64_t)p->q_len * (p->heads / p->kv_heads) : p->q_len;   // a group's heads share tiles
-  const int64_t blocks = (lines + rows - 1) / rows * (cores ? p->kv_heads : p->heads) * p->batch;
+  const bool half = p->dtype != ATTN_F32;
+  if (half && p->head_dim != 64 && p->head_dim != 128) return 1;   // no pass that takes parts
+  const int64_t group = p->heads / p->kv_heads;
+  const int rows = half ? 256 : 32, keys = half ? 128 : 32;
+  int64_t blocks = (p->q_len + rows - 1) / rows * (int64_t)p->heads * p->batch;
+  if (half && p->q_len <= 128 && group > 1) blocks = (int64_t)p->batch * p->kv_heads * ((group + 1) / 2);
+  if (!half) blocks = (p->q_len * group + rows - 1) / rows * p->kv_heads * p->batch;   // a group's heads share tiles
   if (blocks >= kFillBlocks) return 1;
   int64_t span = (int64_t)p->window_left + first_keys + rows;
   span = span < p->k_len ? span : p->k_len;
   const int64_t tiles = (span + keys - 1) / keys + 1;
-  const double tile = cores ? 2.1 * p->head_dim / 128 : 1.5;   // us
   int best = 1;
   double least = 0;
-  for (int n = 1; n <= kMaxRanges && n <= tiles; ++n) {
-    const int64_t waves = (blocks * n + 151) / 152;
-    double cost = cores ? (double)(waves * ((tiles + n - 1) / n)) * tile
-                        : (double)(waves * ((tiles + n - 1) / n + 3)) * tile;
-    if (n > 1) cost += 4.0 + (double)(blocks * rows * n) * p->head_dim * 8 / 6.5e6;
+  for (int n = 1; n <= (half ? 8 : kMaxRanges) && n <= tiles; n = half ? 2 * n : n + 1) {
+    const int64_t part = (tiles + n - 1) / n, waves = (blocks * n + 151) / 152;
+    if (half && n > 1 && blocks * n > (n == 2 ? 152 : n == 4 ? 136 : 120)) break;
+    double cost;
+    if (half)
+      cost = waves * 10.0 + waves * part * 1.4 + (n > 1 ? 2.0 : 0.0);
+    else
+      cost = waves * part * 2.1 * p->head_dim / 128 +
+             (n > 1 ? 4.0 + (double)(blocks * rows * n) * p->head_dim * 8 / 6.5e6 : 0.0);
     if (n == 1 || cost < least) {
       least = cost;
       best = n;
     }
   }
+  *cluster = half && best > 1;
   return best;
 }
 
@@ -506,8 +517,9 @@ int attn_decode_append(const attn_problem* p, const void* q, const void* k_new, 
 size_t attn_fwd_window_workspace_size(const attn_problem* p, int32_t first_keys) {
   if (check_window(p, first_keys) != ATTN_OK) return 0;
   if (first_keys == 0) return attn_fwd_workspace_size(p);
-  const int n = window_plan(p, first_keys);
-  return n > 1 ? decode_ws_bytes(p, n) : 0;
+  int cluster = 0;
+  const int n = window_plan(p, first_keys, &cluster);
+  return n > 1 && !cluster ? decode_ws_bytes(p, n) : 0;
 }
 
 int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, const void* k, const void* v, void* o,
@@ -520,9 +532,10 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   if (p->batch == 0 || p->q_len == 0) return ATTN_OK;
   rc = check_pointers(p, q, k, v, o, mask, seg, k_lens, lse);
   if (rc) return rc;
-  const int n = window_plan(p, first_keys);
+  int cluster = 0;
+  const int n = window_plan(p, first_keys, &cluster);
   Split s{1, p->k_len > 0 ? p->k_len : 1, nullptr, nullptr};
-  if (n > 1) {
+  if (n > 1 && !cluster) {
     const bool enough = workspace && workspace_bytes >= decode_ws_bytes(p, n);
     if (enough && aligned(workspace, 256))
       s = split_in(workspace, (size_t)p->batch * p->heads * p->q_len, n, 0, p->head_dim);
@@ -536,7 +549,9 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   const Ext x = make_ext(first_keys, nullptr);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int used = 0;
-  rc = window_tc_try(r, first_keys, s, st, &used);
+  Split parts = s;
+  if (cluster) parts.n_splits = n;
+  rc = window_tc_try(r, first_keys, parts, st, &used);
   if (rc) return rc;
   if (!used) {
     rc = window_f32_try(r, first_keys, s, st, &used);

@@ -26,7 +26,12 @@
 // item's list; query tile 0 stops at its own last tile and query tile 1 leaves
 // out the window's first tile where only tile 0 sees it.
 //
-// Waits are bounded as in the prefill kernel.
+// Few query blocks: a cluster of 2, 4 or 8 CTAs takes one block, each CTA a part
+// of its list; the parts' O and row sums meet in distributed shared memory,
+// where every CTA merges and writes its share of the rows.
+//
+// Waits are bounded as in the prefill kernel (the cluster barriers at the end
+// are passed by every thread, also after a wait ran out).
 #pragma once
 
 #include <string.h>
@@ -108,12 +113,33 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
                : "memory");
 }
 
+// A float of CTA `rank`'s shared memory, at the address of this CTA's p.
+__device__ __forceinline__ float peer(const float* p, uint32_t rank) {
+  uint32_t r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 peer4(const float4* p, uint32_t rank) {
+  uint32_t r;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(r)
+               : "memory");
+  return v;
+}
+
 // XF: scores under a mask, a softcap or a scale that is not positive.
 template <int D, bool BF16, bool XF>
 __global__ void __launch_bounds__(kThreads, 1)
     window_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const Problem p, const int first,
-                     const int pair_heads, const int n_items, const int wide_rows, const int drop_first_copy, const Split sp) {
+                     const int pair_heads, const int n_items, const int wide_rows, const int clustered, const int drop_first_copy,
+                     const Split sp) {
   using C = Cfg<D>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -124,6 +150,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars sb;
   __shared__ Item items[2];
   __shared__ Vis row_v[2][2 * BM];
+  // clustered: each row's reference maximum and sum; its numerators lie over the stages, [D / 4][2 BM][4].
+  __shared__ float part_m[2 * BM], part_l[2 * BM];
+  float4* const part_a = reinterpret_cast<float4*>(k_s);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int my_items = (n_items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
@@ -164,6 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = sb.tmem_base;
 
+  // clustered: the three barriers of the merge, for the warps that take no part in it.
+  auto meet = [&]() {
+    if (clustered)
+      for (int i = 0; i < 3; ++i) cluster_sync();
+  };
   if (warp == 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // ---------------- items: rows, unions, tile lists ----------------
@@ -247,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_arrive(&sb.item_full[buf]);
     }
+    meet();
   } else if (warp == 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // ---------------- copies ----------------
@@ -304,6 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (k_only >= 0) drain_bar(&sb.k_full[k_only % C::kStages], (uint32_t)(k_only / C::kStages) & 1u, p.status);
     }
+    __syncwarp();
+    meet();
   } else if (warp == 9) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // ---------------- MMA issuer (warp-wide; one elected lane issues) ----------------
@@ -424,8 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) drain_bar(&sb.mma_done, 0, p.status);
     }
     __syncwarp();
+    meet();
   } else if (warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    meet();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------- softmax: one thread per query row ----------------
@@ -440,6 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t x[BN];
     int j = 0;   // key tiles so far
     bool ok = true;
+    float m_ref = -INFINITY, l = 0.f;
+    int done = 0;   // of them, this item's
     for (int k = 0; ok && k < my_items; ++k) {
       const int buf = k & 1;
       if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
@@ -453,8 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* mrow = nullptr;
       if (XF && p.M && qrow < p.Sq)
         mrow = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)h * p.m.hs + (int64_t)qrow * p.m.rs;
-      float m_ref = -INFINITY, l = 0.f;
-      int done = 0;
+      m_ref = -INFINITY;
+      l = 0.f;
+      done = 0;
       for (int i = 0; i < n_my; ++i) {
         if (i == skip) continue;
         if (!(ok = wait_warp(&sb.s_full[t], (uint32_t)j & 1u, &sb.abort, p.status))) break;
@@ -579,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue: O / l, special rows, LSE ----
       if (done > 0 && !(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
       fence_after();
+      if (clustered) break;   // (its only item)
       const bool split = sp.n_splits > 1;
       // The sink logit joins the denominator (and rescales the accumulated O); with parts the merge adds it once.
       const float o_mul = p.sink_on && !split ? fold_sink<true>(m_ref, l, sink_logit(p, h) * kLog2e) : 1.f;
@@ -634,6 +677,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_before();   // O's loads come before the next item's P, and so before its P V
       mbar_arrive(&sb.item_empty[buf]);
     }
+    if (clustered) {
+      cluster_sync();   // every P V is done with V's stages
+      const int row = t * BM + r;
+      part_m[row] = m_ref;
+      part_l[row] = l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (done > 0) {   // (warp-uniform)
+          tmem_ld32(o_tm + c * 32, o);
+          tmem_ld_wait_regs<1>(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          part_a[(c * 8 + e / 4) * 2 * BM + row] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                               __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+      }
+      cluster_sync();
+      // This CTA's rows: a thread takes 16 columns of a row from every part.
+      const int parts = sp.n_splits, rows = 2 * BM / parts;
+      const Item& it = items[0];
+      for (int u = threadIdx.x; u < rows * (D / 16); u += 2 * BM) {
+        const int mine = (int)cluster_rank() * rows + u % rows, col = u / rows * 16, tt = mine / BM;
+        const int i = it.q0 + (pair_heads ? mine % BM : mine), hh = it.h + tt * ht_step;
+        if (i >= p.Sq || hh >= (it.g + 1) * p.qpg) continue;
+        float M = -INFINITY, L = 0.f, a[16];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < parts) M = fmaxf(M, peer(part_m + mine, q));
+        const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) a[e] = 0.f;
+#pragma unroll 1
+        for (int q0 = 0; q0 < parts; q0 += 4) {   // the loads of up to four parts before their sums
+          float f[4], lq[4];
+          float4 y[4][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q0 + q >= parts) continue;
+            f[q] = peer(part_m + mine, q0 + q);
+            lq[q] = peer(part_l + mine, q0 + q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[q][e] = peer4(part_a + (col / 4 + e) * 2 * BM + mine, q0 + q);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q0 + q >= parts) continue;
+            f[q] = ex2(f[q] - mu);
+            L = fmaf(f[q], lq[q], L);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[4 * e] = fmaf(f[q], y[q][e].x, a[4 * e]);
+              a[4 * e + 1] = fmaf(f[q], y[q][e].y, a[4 * e + 1]);
+              a[4 * e + 2] = fmaf(f[q], y[q][e].z, a[4 * e + 2]);
+              a[4 * e + 3] = fmaf(f[q], y[q][e].w, a[4 * e + 3]);
+            }
+          }
+        }
+        const float o_mul = p.sink_on ? fold_sink<true>(M, L, sink_logit(p, hh) * kLog2e) : 1.f;
+        const bool hidden = L == 0.f;
+        const float inv = o_mul / L, fill = p.masked_zero ? 0.f : NAN;
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) w[e / 2] = pack2<BF16>(hidden ? fill : a[e] * inv, hidden ? fill : a[e + 1] * inv);
+        T* dst = static_cast<T*>(p.O) + p.o.off + (int64_t)it.b * p.o.bs + (int64_t)hh * p.o.hs + (int64_t)i * p.o.rs + col;
+        if (wide_rows) {
+          store32(dst, w);
+        } else {
+          reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        if (col == 0 && p.lse)
+          p.lse[(int64_t)it.b * p.lse_bs + (int64_t)hh * p.lse_hs + i] = hidden ? -INFINITY : (M + __log2f(L)) * kLn2;
+      }
+      cluster_sync();   // no CTA leaves while its part is being read
+    }
   }
 
   fence_before();
@@ -675,8 +797,22 @@ int launch(const Problem& p, int first, const Split& sp, cudaStream_t st) {
                        ? 1
                        : 0;
   const int drop = take_injection() == ATTN_INJECT_DROP_FIRST_COPY ? 1 : 0;
-  kern<<<(unsigned)(n < kSms ? n : kSms), kThreads, smem, st>>>(mq, mk, mv, p, first, pair, (int)n, wide, drop, sp);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  // Parts without a workspace are a cluster's CTAs.
+  const int clustered = sp.n_splits > 1 && !sp.part_o ? 1 : 0;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)sp.n_splits;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)(clustered || n < kSms ? n : kSms));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = clustered;
+  return cudaLaunchKernelEx(&c, kern, mq, mk, mv, p, first, pair, (int)n, wide, clustered, drop, sp) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 template <int D>

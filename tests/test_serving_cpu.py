@@ -80,21 +80,18 @@ def _r256(x):
     return (x + 255) // 256 * 256
 
 
-def _parts(B, H, G, Sq, Sk, D, w, first, ks, f32):
-    """The cost model of the plan, restated: waves of one CTA an SM with their part of the tiles (and, on the
-    tensor cores, three tiles of fixed cost), and the merge."""
+def _parts(B, H, G, Sq, Sk, D, w, first, ks):
+    """The float32 plan's cost model, restated: waves of one CTA an SM with their part of the tiles, and the merge.
+    (The half types' own parts are clusters, which take no workspace.)"""
     if ks:
         return min(ks, 16)
-    rows, keys = (32, 32) if f32 else (256 if D <= 128 else 128, 128)
-    blocks = -(-Sq * H // G // rows) * G * B if f32 else -(-Sq // rows) * H * B
+    blocks = -(-Sq * H // G // 32) * G * B
     if blocks >= 304:
         return 1
-    tiles = -(-min(Sk, w + first + rows) // keys) + 1
-    tile = 2.1 * D / 128 if f32 else 1.5
+    tiles = -(-min(Sk, w + first + 32) // 32) + 1
 
     def cost(n):
-        return -(-blocks * n // 152) * (-(-tiles // n) + (0 if f32 else 3)) * tile + \
-            (n > 1) * (4.0 + blocks * rows * n * D * 8 / 6.5e6)
+        return -(-blocks * n // 152) * -(-tiles // n) * 2.1 * D / 128 + (n > 1) * (4.0 + blocks * 32 * n * D * 8 / 6.5e6)
 
     return min(range(1, min(16, tiles) + 1), key=cost)
 
@@ -105,7 +102,7 @@ def _parts(B, H, G, Sq, Sk, D, w, first, ks, f32):
     (1, 2, 100, 5000, 256, 5000, 10, 0), (1, 2, 100, 500, 64, 63, 2, 5), (1, 1, 9, 900, 64, 63, 2, 40)])
 def test_window_workspace_follows_the_plan(B, H, Sq, Sk, D, w, first, ks, dtype):
     p = window_problem(dtype=dtype, batch=B, heads=H, kv_heads=1, q_len=Sq, k_len=Sk, head_dim=D, window_left=w, key_splits=ks)
-    n = _parts(B, H, 1, Sq, Sk, D, w, first, ks, dtype == "f32")
+    n = _parts(B, H, 1, Sq, Sk, D, w, first, ks) if dtype == "f32" or ks else 1
     rows = B * H * Sq
     assert attn.attn_fwd_window_workspace_size(p, first) == (0 if n == 1 else _r256(rows * n * D * 4) +
                                                              _r256(rows * n * 4))
