@@ -132,6 +132,74 @@ def test_window_bounded_wait():
     ref.check(got, o, tol, "O")
 
 
+@pytest.mark.parametrize("dt,lead,pad", [("bf16", 8, 8), ("f16", 16, 24), ("f32", 4, 4), ("f32", 1, 1), ("bf16", 1, 3),
+                                         ("bf16", 0, 8)])
+def test_window_strided_views(dt, lead, pad):
+    """Rows inside wider ones that start off 32, 16 or even 4 bytes; what lies between the rows of O stays."""
+    g = gen(31)
+    B, H, G, Sq, Sk, D = 2, 4, 2, 140, 300, 64
+
+    def view(h, n, fill=None):
+        flat = torch.full((lead + B * n * h * (D + pad),), 5.0) if fill else randn(g, lead + B * n * h * (D + pad))
+        return flat.to(DT[dt]).cuda()[lead:].view(B, n, h, D + pad)[..., :D]
+
+    q, k, v, out = view(H, Sq), view(G, Sk), view(G, Sk), view(H, Sq, True)
+    attn.fwd(q, k, v, layout="bshd", causal=True, window_left=33, first_keys=5, masked_rows="zero", out=out)
+    vis = ref.visible(Sq, Sk, [Sk] * B, window=33, first=5)
+    o, _, tol, _ = ref.attention(*(t.cpu().transpose(1, 2) for t in (q, k, v)), vis)
+    ref.check(out.transpose(1, 2), o, tol)
+    rest = out.as_strided(out.shape[:3] + (pad,), out.stride(), out.storage_offset() + D)
+    assert (rest[:, :-1] == 5).all()
+
+
+def test_window_int8_keys_and_values():
+    g = gen(33)
+    H, G, Sq, Sk, D = 4, 2, 70, 200, 64
+    q = randn(g, 1, H, Sq, D, dt=torch.bfloat16)
+    k, v = (torch.randint(-128, 128, (1, G, Sk, D), generator=g, dtype=torch.int8) for _ in range(2))
+    sc = [torch.rand(G * D, generator=g) * 0.015 + 0.005 for _ in range(2)]
+    vis = ref.visible(Sq, Sk, [Sk], window=20, first=6)
+    o, _, tol, _ = ref.attention(q, k, v, vis, kv_scales=sc)
+    qd, kd, vd, ks, vs = (t.cuda() for t in (q, k, v, *sc))
+    out = torch.empty_like(qd)
+    p = attn.make_problem(dict(
+        batch=1, heads=H, kv_heads=G, q_len=Sq, k_len=Sk, head_dim=D, dtype="bf16", causal=True, window_left=20,
+        kv_dtype="i8", kv_scale="channel", k_scale_ptr=ks.data_ptr(), v_scale_ptr=vs.data_ptr(),
+        **{f"{n}_layout": attn._layout4(t, 1) for n, t in (("q", qd), ("k", kd), ("v", vd), ("o", out))}))
+    assert attn.attn_fwd_window(p, 6, qd.data_ptr(), kd.data_ptr(), vd.data_ptr(), out.data_ptr(), None, None, None,
+                                None, None, 0, torch.cuda.current_stream().cuda_stream) == 0
+    ref.check(out, o, tol)
+
+
+def test_window_shared_workspace_and_graphs():
+    """Two captured calls that share a workspace of parts, replayed in turn, and an eager call between."""
+    cases = [window_case(WINDOW[i], 50 + i, False) for i in (4, 5)]
+    want = [attn.fwd(*t, **kw) for t, kw, _ in cases]
+    graphs, outs = [], []
+    ws = torch.empty(1 << 23, dtype=torch.uint8, device="cuda")
+    for (q, k, v), kw, _ in cases:
+        out = torch.empty_like(q)
+        p = attn.make_problem(dict(
+            batch=q.shape[0], heads=q.shape[1], kv_heads=k.shape[1], q_len=q.shape[2], k_len=k.shape[2],
+            head_dim=q.shape[3], dtype=attn._dtype_name(q), causal=True, causal_align="klens",
+            window_left=kw["window_left"], masked_rows="zero", key_splits=kw["key_splits"],
+            **{f"{n}_layout": attn._layout4(t, 1) for n, t in (("q", q), ("k", k), ("v", v), ("o", out))}))
+        assert 0 < attn.attn_fwd_window_workspace_size(p, kw["first_keys"]) <= ws.numel()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            assert attn.attn_fwd_window(p, kw["first_keys"], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                        None, None, kw["k_lens"].data_ptr(), None, ws.data_ptr(), ws.numel(),
+                                        torch.cuda.current_stream().cuda_stream) == 0
+        graphs.append(g)
+        outs.append(out)
+    for _ in range(3):
+        for g, out, (o, _) in zip(graphs, outs, want):
+            out.zero_()
+            ws.fill_(255)
+            g.replay()
+            assert torch.equal(out, o)
+
+
 def test_window_without_first_keys_is_attn_fwd():
     (q, k, v), kw, _ = window_case(WINDOW[0], 3, False)
     kw = dict(kw, first_keys=0)
@@ -592,6 +660,35 @@ def test_other_streams_and_offsets_of_views():
     k, _ = ref.gather(pool[:, 0].cpu(), table.cpu(), 16, 96, False)
     v, _ = ref.gather(pool[:, 1].cpu(), table.cpu(), 16, 96, False)
     o, _, tol, _ = ref.attention(q.cpu().transpose(1, 2), k, v, ref.visible(1, 96, [90, 33]))
+    ref.check(got.transpose(1, 2), o, tol)
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side, each with its own outputs and workspace, give what they give alone."""
+    jobs = [paged_case(PAGED[i], 400 + i) for i in (len(PAGED) - 10, 1)] + [paged_case(PAGED[0], 410)]
+    want = [attn.decode_paged(*a, **kw) for a, kw, _ in jobs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in jobs], [[] for _ in jobs]
+    for _ in range(10):
+        for st, (a, kw, _), g in zip(streams, jobs, got):
+            with torch.cuda.stream(st):
+                g.append(attn.decode_paged(*a, **kw))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w.nan_to_num(3.0), x.nan_to_num(3.0)) for x in g)
+
+
+def test_paged_many_entries():
+    """Thousands of short entries, most without a key."""
+    g = gen(41)
+    B, G, ps, D = 3500, 1, 8, 64
+    lens = torch.randint(-6, 4, (B,), generator=g).clamp(min=0)
+    k, v = randn(g, B, G, ps, D, dt=torch.float16), randn(g, B, G, ps, D, dt=torch.float16)
+    q = randn(g, B, 1, 2, D, dt=torch.float16)
+    table = torch.arange(B, dtype=torch.int32).view(B, 1)
+    got = attn.decode_paged(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.to(torch.int32).cuda(),
+                            masked_rows="zero")
+    o, _, tol, _ = ref.attention(q.transpose(1, 2), k, v, ref.visible(1, ps, lens))
     ref.check(got.transpose(1, 2), o, tol)
 
 
