@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
           fence_after();
           const float f = rescale ? corr : 1.f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(o_tm + c * 32, o);
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       T* orow = static_cast<T*>(p.O) + p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs + (int64_t)qrow * p.o.rs;
       const int64_t prow = ((int64_t)b * p.H + h) * p.Sq + qrow;
       float4* po = split ? reinterpret_cast<float4*>(sp.part_o + (prow * sp.n_splits + items[buf].part) * D) : nullptr;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (done > 0) {
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = t * BM + r;
       part_m[row] = m_ref;
       part_l[row] = l;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (done > 0) {   // (warp-uniform)
