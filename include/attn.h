@@ -266,20 +266,23 @@ ATTN_API int attn_decode_append(const attn_problem* p, const void* q, const void
  * is as for attn_fwd.  With seg, keys between the first keys of two documents
  * that share a query block count as seen by the block (their V is finite). */
 
-/* Bytes of device workspace attn_fwd_window needs (0 when none).  With fewer
- * than 304 blocks of 256 query rows (128 for head_dim above 128) each block's
- * list of visible key tiles may be cut into up to 16 parts that are merged in
- * order (float32 [B*H*q_len][parts][head_dim] and [B*H*q_len][parts], each
- * 256-byte aligned); how many depends on the shape alone, and p->key_splits >=
- * 1 asks for a count.  Returns 0 for an invalid problem; attn_fwd_window then
- * reports the error. */
+/* Bytes of device workspace attn_fwd_window needs (0 when none).  With few
+ * query blocks each block's list of visible key tiles may be cut into up to 16
+ * parts that are merged in order; how many depends on the shape alone, and
+ * p->key_splits >= 1 asks for a count.  float32 problems and asked-for counts
+ * take a workspace (float32 [B*H*q_len][parts][head_dim] and
+ * [B*H*q_len][parts], each 256-byte aligned); the parts the library chooses
+ * for f16/bf16 meet in shared memory.  Returns 0 for an invalid problem;
+ * attn_fwd_window then reports the error. */
 ATTN_API size_t attn_fwd_window_workspace_size(const attn_problem* p, int32_t first_keys);
 
 /* attn_fwd with first_keys (>= 0) keys of each row's span visible behind its
  * window: p->causal must be 1 and p->window_left >= 0, first_keys <= 2^30,
  * else ATTN_ERR_INVALID_ARG.  Key tiles between the first keys and the window
- * are neither copied nor computed.  first_keys = 0 is attn_fwd.  Arguments,
- * workspace rule and errors as for attn_fwd. */
+ * are neither copied nor computed.  first_keys = 0 is attn_fwd.  k_len and
+ * q_len are at most 2^30 (ATTN_ERR_UNSUPPORTED).  Arguments, workspace rule
+ * and errors as for attn_fwd.  f16/bf16 run on the tensor cores at head_dim
+ * 64 and 128. */
 ATTN_API int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, const void* k, const void* v,
                              void* o, const float* mask, const int32_t* seg, const int32_t* k_lens, float* lse,
                              void* workspace, size_t workspace_bytes, attn_stream stream);
@@ -312,10 +315,11 @@ ATTN_API size_t attn_decode_paged_workspace_size(const attn_problem* p, const at
  * the list has ceil(k_len / page_size) values); k_pool / v_pool are laid out
  * by p->k / p->v as above.  Visibility as for attn_fwd with first_keys (which
  * must be 0 unless p->causal and p->window_left >= 0); seg is not taken.
- * List values of pages without a visible key are not used.  The number of
- * ranges the keys are cut into depends on the shape alone and their ends also
- * on the entry's length: every range holds an equal share of the entry's own
- * visible keys.  Types, int8 pools, score transforms, mask (columns are the
+ * List values of pages without a visible key are not used.  Where an entry's
+ * keys are cut into ranges depends on the shape and on the lengths of all
+ * entries of the call (the visible keys of the whole batch are shared out
+ * equally), so an entry's last bits may change with its neighbours' lengths;
+ * two calls with the same lengths give the same bits.  Types, int8 pools, score transforms, mask (columns are the
  * entry's rows), masked rows and errors as for attn_decode.  Cache rows that
  * are not visible are never read into the result. */
 ATTN_API int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t first_keys, const void* q,

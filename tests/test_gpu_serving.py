@@ -132,6 +132,34 @@ def test_window_bounded_wait():
     ref.check(got, o, tol, "O")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("step,every", [(32, 20), (32, 130), (4, 7), (-32, 20), (64, 33)])
+def test_window_rising_scores(dt, step, every):
+    """Scores that climb (or fall) by `step` every few keys: running maxima move inside tiles and between them."""
+    g = gen(35)
+    Sq, Sk, D = 300, 400, 64
+    q, k = torch.zeros(1, 2, Sq, D, dtype=DT[dt]), torch.zeros(1, 1, Sk, D, dtype=DT[dt])
+    q[..., 0] = 1
+    k[0, 0, :, 0] = (torch.arange(Sk) // every * step).to(DT[dt])   # exact in every type
+    v = randn(g, 1, 1, Sk, D, dt=DT[dt])
+    vis = ref.visible(Sq, Sk, [Sk], window=200, first=40)
+    o, lse, tol, tol_l = ref.attention(q, k, v, vis, scale=1.0)
+    got, got_l = attn.fwd(q.cuda(), k.cuda(), v.cuda(), layout="bhsd", causal=True, window_left=200, first_keys=40,
+                          scale=1.0, return_lse=True)
+    ref.check(got, o, tol, "O")
+    ref.check(got_l, lse, tol_l, "LSE")
+    # and the same keys in pages
+    pool = [t[0].view(1, 25, 16, D).transpose(0, 1).contiguous().cuda() for t in (k, v)]
+    table = torch.arange(25, dtype=torch.int32).view(1, 25).cuda()
+    vis = ref.visible(1, Sk, [Sk], window=200, first=40)
+    o, lse, tol, tol_l = ref.attention(q[:, :, :1], k, v, vis, scale=1.0)
+    got, got_l = attn.decode_paged(q[:, :, :1].transpose(1, 2).contiguous().cuda(), *pool, table,
+                                   torch.tensor([Sk], dtype=torch.int32).cuda(), window_left=200, first_keys=40,
+                                   scale=1.0, return_lse=True)
+    ref.check(got.transpose(1, 2), o, tol, "paged O")
+    ref.check(got_l, lse, tol_l, "paged LSE")
+
+
 @pytest.mark.parametrize("dt,lead,pad", [("bf16", 8, 8), ("f16", 16, 24), ("f32", 4, 4), ("f32", 1, 1), ("bf16", 1, 3),
                                          ("bf16", 0, 8)])
 def test_window_strided_views(dt, lead, pad):
