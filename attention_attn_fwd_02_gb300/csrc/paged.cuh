@@ -12,9 +12,9 @@
 // unit in list order.  The cut depends on the lengths alone, so results are
 // deterministic.
 //
-// Small problems (few units of short lists) take no workspace and no join: a
-// thread-block cluster of up to 8 CTAs holds one unit, each CTA a part of its
-// list, and merges the parts through distributed shared memory.
+// Short lists take no workspace and no join: a unit is a CTA's, or a thread-block
+// cluster's of up to 8, each CTA with a part of its list, which merges the parts
+// through distributed shared memory.
 #pragma once
 
 #include "visible.cuh"
@@ -359,10 +359,13 @@ __device__ __forceinline__ void cluster_join(const Work& w, const Part& part, in
 // Host: merges the fragments of cut units.  Enqueued right behind the pass.
 cudaError_t launch_join(const Work& w, cudaStream_t st);
 
-// Host: the work of a pass with `ctas` CTAs an SM: clusters when all units fit
-// the SMs at once, eight (or as many as the longest list has tiles) CTAs each
-// with at most eight tiles; else shares, never more than there can be tiles.
-// (One sequence of 700 rows, 8 kv heads: 11.3 us of device time in shares.)
+// Host: the work of a pass with `ctas` CTAs an SM.  Short lists: a unit goes to
+// the largest cluster of 8, 4, 2 or 1 CTAs that lets all units run at once, if
+// that leaves a CTA at most eight tiles; lists of at most eight tiles run one
+// CTA a unit whatever their count.  Else shares, never more than there can be
+// tiles.  (Device time, bf16, 32/8 heads, head_dim 128, in shares: one sequence
+// of 700 rows 11.3 us, 30 of up to 500 rows 18.2, 60 of them 28.2, 90 of up to
+// 100 rows 20.7.)
 inline void plan_work(Work& w, int tile, int heads, int ctas) {
   w.unit = tile;
   w.heads = heads;
@@ -374,9 +377,13 @@ inline void plan_work(Work& w, int tile, int heads, int ctas) {
     span = seen < span ? seen : span;
   }
   const int64_t list = (span + tile - 1) / tile, most = units * list;
-  const int64_t cluster = list < 8 ? (list < 1 ? 1 : list) : 8;
-  w.cluster = list <= 64 && units * cluster <= n ? (int)cluster : 0;
-  w.ctas = (int)(w.cluster ? units * cluster : most < 1 ? 1 : most < n ? most : n);
+  w.cluster = list <= 8 && units <= (1 << 20) ? 1 : 0;
+  for (int c = 8; c >= 1; c /= 2)
+    if (units * c <= n && list <= 8 * c && (c == 1 || list >= c)) {
+      w.cluster = c;
+      break;
+    }
+  w.ctas = (int)(w.cluster ? units * w.cluster : most < 1 ? 1 : most < n ? most : n);
 }
 
 // Host: enqueues a pass, and the join behind shares.

@@ -171,14 +171,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
         cs[j][0] = cs[j][1] = p.scale * kLog2e;
       } else {
         // Channels 4t, 4t + 2 (then 4t + 1, 4t + 3) of a 16-channel block: the order in which the bytes arrive.
-        float top = 0.f;
+        float v[D / 16][4], top = 0.f;
+        const float* ks = p.k_scale + (p.kv_per_channel ? g * D : 0);
 #pragma unroll
-        for (int c = 0; c < D / 4; c += 4)
+        for (int c = 0; c < D / 16; ++c) {
+          const int d = 16 * c + 4 * tig;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = 4 * c + 4 * tig + e;
-            if (hh < nh) top = fmaxf(top, fabsf(to_f32(row[d]) * p.k_scale[p.kv_per_channel ? g * D + d : 0]));
-          }
+          for (int e = 0; e < 4; ++e)
+            v[c][e] = hh < nh ? to_f32(row[d + e]) * __ldg(ks + (p.kv_per_channel ? d + e : 0)) : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[c][e]));
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
         int ex = 0;
@@ -189,15 +194,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
         const float up = ldexpf(1.f, ex);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = 16 * c + 4 * tig + e;
-            v[e] = hh < nh ? to_f32(row[d]) * p.k_scale[p.kv_per_channel ? g * D + d : 0] * up : 0.f;
-          }
           uint32_t rest[2];
-          qh[j][c][0] = pack_split<false>(v[0], v[2], rest[0]);
-          qh[j][c][1] = pack_split<false>(v[1], v[3], rest[1]);
+          qh[j][c][0] = pack_split<false>(v[c][0] * up, v[c][2] * up, rest[0]);
+          qh[j][c][1] = pack_split<false>(v[c][1] * up, v[c][3] * up, rest[1]);
           if constexpr (SPLIT) {
             ql[j][c][0] = rest[0];
             ql[j][c][1] = rest[1];
