@@ -34,7 +34,7 @@ size_t paged_ws_bytes(const Problem& p, int first) {
   w.p = p;
   w.x.first = first;
   int rc = 0;
-  if (p.B < 1 || !paged::pass(w, false, nullptr, &rc) || w.cluster) return 0;
+  if (p.B < 1 || !paged::pass(w, false, nullptr, &rc) || w.cluster || w.stride) return 0;
   return paged::round256(paged::rows_of(w) * p.D * 4) + paged::round256(paged::rows_of(w) * 4) +
          paged::round256(w.ctas * sizeof(paged::CutUnit));
 }
@@ -53,11 +53,13 @@ int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, 
   w.x = x;
   int rc = 0;
   if (!paged::pass(w, false, st, &rc)) return ATTN_OK;
-  w.part_o = static_cast<float*>(workspace);
-  w.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        paged::round256(paged::rows_of(w) * p.D * sizeof(float)));
-  w.cuts = reinterpret_cast<paged::CutUnit*>(reinterpret_cast<char*>(w.part_lse) +
-                                             paged::round256(paged::rows_of(w) * sizeof(float)));
+  if (!w.cluster && !w.stride) {   // only shares have fragments
+    w.part_o = static_cast<float*>(workspace);
+    w.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                          paged::round256(paged::rows_of(w) * p.D * sizeof(float)));
+    w.cuts = reinterpret_cast<paged::CutUnit*>(reinterpret_cast<char*>(w.part_lse) +
+                                               paged::round256(paged::rows_of(w) * sizeof(float)));
+  }
   *used = 1;
   paged::pass(w, true, st, &rc);
   return rc;

@@ -12,9 +12,10 @@
 // unit in list order.  The cut depends on the lengths alone, so results are
 // deterministic.
 //
-// Short lists take no workspace and no join: a unit is a CTA's, or a thread-block
-// cluster's of up to 8, each CTA with a part of its list, which merges the parts
-// through distributed shared memory.
+// Short lists have no fragments and no join.  Few units: a unit is a thread-block
+// cluster's of 2, 4 or 8 CTAs, each with a part of its list, which merges the
+// parts through distributed shared memory.  Many: a CTA takes whole units, one
+// after the other.
 #pragma once
 
 #include "visible.cuh"
@@ -29,6 +30,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kSlack = 8.0f;   // log2 units: how far a score may rise above the reference maximum
 constexpr unsigned kAll = 0xffffffffu;
+
+// How a pass's CTAs divide the units: equal shares of all tiles, a cluster a
+// unit, or whole units in turn.
+enum { kShares = 0, kCluster = 1, kWhole = 2 };
 
 // A unit cut by shares, noted by the share that ends it: its fragments are the
 // last one of share c0 (slot 1 when that share began in front of the unit),
@@ -49,6 +54,7 @@ struct Work {
   float* part_lse; // [ctas][2][heads]
   CutUnit* cuts;   // [ctas]
   int cluster;     // > 0: CTAs of the cluster that holds one unit (no shares)
+  int stride;      // > 0: CTA c takes the units c, c + stride, ... (no shares)
 };
 
 __device__ __forceinline__ int entry_tiles(const Work& w, int b) {
@@ -81,10 +87,27 @@ struct Cursor {
     tl = tile_list(v, w.unit);
     n = tl.n;
   }
+  // To the first tile of unit `id`, or of the next one w.stride behind it that has tiles.  False: there is none.
+  __device__ __forceinline__ bool at_unit(const Work& w, int units, int64_t id) {
+    tile = 0;
+    for (; id < (int64_t)w.p.B * units; id += w.stride) {
+      b = (int)(id / units);
+      u = (int)(id - (int64_t)b * units);
+      load(w);
+      if (n > 0) return true;
+    }
+    return false;
+  }
   // To the next tile; the caller stays inside the total.
+  template <int MODE>
   __device__ __forceinline__ void next(const Work& w, int units) {
     if (++tile < n) return;
     tile = 0;
+    if constexpr (MODE == kCluster) return;   // (a cluster has one unit)
+    if constexpr (MODE == kWhole) {
+      at_unit(w, units, (int64_t)b * units + u + w.stride);
+      return;
+    }
     if (++u < units) return;
     u = 0;
     do ++b;
@@ -144,7 +167,7 @@ __device__ __forceinline__ uint32_t swz(int r, int u) {
 // (elements of ES): K rows, then V rows.  Rows are copied with cp.async from wherever the page
 // list puts them; rows that are hidden or have no page arrive as zeros, and
 // nothing is read for them.
-template <int ROW, int ES, int KEYS, int STAGES>
+template <int ROW, int ES, int KEYS, int STAGES, int MODE>
 struct Ring {
   static constexpr int kUnits = ROW / 16;
   static constexpr int kStage = 2 * KEYS * ROW;
@@ -228,7 +251,7 @@ struct Ring {
       }
     }
     if (more) {
-      in.next(w, units);
+      in.template next<MODE>(w, units);
       look_up();
     }
   }
@@ -272,13 +295,12 @@ __device__ __forceinline__ void fill_entry(const Work& w, int b) {
   }
 }
 
-// What every CTA of a pass does first: the fill of entries without a visible
-// key, and the mark of a share that ends no cut unit.
+// What every CTA of a pass without clusters does first: its entries without a
+// visible key.
 template <typename T>
-__device__ __forceinline__ void begin_share(const Work& w, int cta) {
+__device__ __forceinline__ void fill_entries(const Work& w, int cta) {
   for (int b = cta; b < w.p.B; b += w.ctas)
     if (entry_tiles(w, b) == 0) fill_entry<T>(w, b);
-  if (threadIdx.x == 0) w.cuts[cta].b = -1;
 }
 
 // Notes a cut unit that ends in share `cta` (whose first fragment it is), `first` tiles into its list.
@@ -359,13 +381,13 @@ __device__ __forceinline__ void cluster_join(const Work& w, const Part& part, in
 // Host: merges the fragments of cut units.  Enqueued right behind the pass.
 cudaError_t launch_join(const Work& w, cudaStream_t st);
 
-// Host: the work of a pass with `ctas` CTAs an SM.  Short lists: a unit goes to
-// the largest cluster of 8, 4, 2 or 1 CTAs that lets all units run at once, if
-// that leaves a CTA at most eight tiles; lists of at most eight tiles run one
-// CTA a unit whatever their count.  Else shares, never more than there can be
-// tiles.  (Device time, bf16, 32/8 heads, head_dim 128, in shares: one sequence
-// of 700 rows 11.3 us, 30 of up to 500 rows 18.2, 60 of them 28.2, 90 of up to
-// 100 rows 20.7.)
+// Host: the work of a pass with `ctas` CTAs an SM.  Short lists: clusters of 8,
+// 4 or 2 CTAs a unit if all units then run at once and a CTA has at most eight
+// tiles; else, for lists of at most eight tiles, whole units.  Other problems:
+// shares, never more than there can be tiles.  Device time, bf16, 32/8 heads,
+// head_dim 128, shares against these: one sequence of 700 rows 11.3 -> 6.3 us,
+// 30 of up to 500 rows 18.2 -> 12.6 (clusters); 60 of up to 500 rows 28.2 ->
+// 23.3, 90 of up to 100 rows 20.7 -> 13.3 (whole units).
 inline void plan_work(Work& w, int tile, int heads, int ctas) {
   w.unit = tile;
   w.heads = heads;
@@ -377,13 +399,11 @@ inline void plan_work(Work& w, int tile, int heads, int ctas) {
     span = seen < span ? seen : span;
   }
   const int64_t list = (span + tile - 1) / tile, most = units * list;
-  w.cluster = list <= 8 && units <= (1 << 20) ? 1 : 0;
-  for (int c = 8; c >= 1; c /= 2)
-    if (units * c <= n && list <= 8 * c && (c == 1 || list >= c)) {
-      w.cluster = c;
-      break;
-    }
+  w.cluster = w.stride = 0;
+  for (int c = 8; c > 1 && !w.cluster; c /= 2)
+    if (units * c <= n && list <= 8 * c && list >= c) w.cluster = c;
   w.ctas = (int)(w.cluster ? units * w.cluster : most < 1 ? 1 : most < n ? most : n);
+  if (!w.cluster && list <= 8) w.stride = w.ctas = (int)(units < 1 ? 1 : units < n ? units : n);
 }
 
 // Host: enqueues a pass, and the join behind shares.
@@ -402,7 +422,7 @@ int launch_pass(Kernel kern, const Work& w, int smem, cudaStream_t st) {
   c.attrs = &at;
   c.numAttrs = w.cluster ? 1 : 0;
   if (cudaLaunchKernelEx(&c, kern, w) != cudaSuccess) return ATTN_ERR_CUDA;
-  return w.cluster || launch_join(w, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return w.cluster || w.stride || launch_join(w, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace paged

@@ -11,18 +11,20 @@
 // What bounds it: HBM.  At 6 TB/s an SM takes an 8 KB stage every 200 ns; its
 // products are 8 x 1024 FMAs (of 128 a cycle) and about 100 shared-memory
 // wavefronts at 4 heads, a third of that time.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace attn {
 namespace paged {
 namespace {
 
-template <int D, int NH>
+template <int D, int NH, int MODE>
 struct CfgF32 {
   static constexpr int kKeys = 1024 / D;            // keys of a warp's stage: 4 KB of K, 4 KB of V
   static constexpr int kLanes = 32 / kKeys;         // lanes of a key
   static constexpr int kStages = 2;
-  using Stages = Ring<D * 4, 4, kKeys, kStages>;
+  using Stages = Ring<D * 4, 4, kKeys, kStages, MODE>;
   static constexpr int kQ = NH * D * 4;             // the unit's queries
   static constexpr int kP = kWarps * kKeys * NH * 4;
   static constexpr int kRed = kWarps * 4 * D * 4;   // merge buffer: 4 heads at a time
@@ -30,9 +32,9 @@ struct CfgF32 {
   static constexpr int kCtas = kSmem <= 74 * 1024 ? 3 : 2;
 };
 
-template <int D, int NH, bool XF, bool CL>
-__global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kernel(const Work w) {
-  using C = CfgF32<D, NH>;
+template <int D, int NH, bool XF, int MODE>
+__global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f32_kernel(const Work w) {
+  using C = CfgF32<D, NH, MODE>;
   constexpr int U = C::Stages::kUnits;              // 16-byte units of a row
   constexpr int KEYS = C::kKeys, LPK = C::kLanes;
   constexpr int VU = U >= 32 ? U / 32 : 1;          // units of a row a lane sums
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
   int64_t total = 0, t0 = 0;
   int shares = 0, my;   // tiles of this CTA
   Cursor out;           // the tile being computed
-  if constexpr (CL) {
+  if constexpr (MODE == kCluster) {
     const int unit = cta / w.cluster;
     out.b = unit / units;
     out.u = unit % units;
@@ -60,11 +62,19 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
     int end;
     list_part(out.n, cta % w.cluster, w.cluster, out.tile, end);
     my = end - out.tile;
+  } else if constexpr (MODE == kWhole) {
+    fill_entries<float>(w, cta);
+    if (!out.at_unit(w, units, cta)) return;
+    my = 0;
+    for (int64_t id = cta + (int64_t)lane * w.stride; id < (int64_t)p.B * units; id += 32 * (int64_t)w.stride)
+      my += entry_tiles(w, (int)(id / units));
+    my = __reduce_add_sync(kAll, my);
   } else {
     total = tiles_before(w, p.B, lane) * units;
     shares = (int)min((int64_t)w.ctas, total);
     let_next_start();
-    begin_share<float>(w, cta);
+    fill_entries<float>(w, cta);
+    if (threadIdx.x == 0) w.cuts[cta].b = -1;
     if (cta >= shares) return;
     t0 = share_begin(total, shares, cta);
     my = (int)(share_begin(total, shares, cta + 1) - t0);
@@ -248,16 +258,17 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
             L = fmaf(f, red_l[v][hb + z], L);
             a = fmaf(f, red[(v * 4 + z) * D + d], a);
           }
-          if constexpr (CL) mine.put(D, hb + z, d, M, L, a);
+          if constexpr (MODE == kCluster) mine.put(D, hb + z, d, M, L, a);
           else put_row<float>(w, whole, cta, slot, out.b, h0 + hb + z, hb + z, d, M, L, a);
         }
         __syncthreads();
       }
-      if (!CL && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
+      if constexpr (MODE == kShares)
+        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {
-      out.next(w, units);
+      out.template next<MODE>(w, units);
       if (unit_ends) {
         first_tile = 0;
         load_q();
@@ -266,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
     }
   }
   copy_wait<0>();
-  if constexpr (CL) {
+  if constexpr (MODE == kCluster) {
     const int g = out.u / w.n_hc, h0 = g * p.qpg + out.u % w.n_hc * NH;
     const int nh = min(NH, (g + 1) * p.qpg - h0);
     if (my == 0)
@@ -277,15 +288,18 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH>::kCtas) paged_f32_kern
 
 template <int D, int NH>
 int pass_cfg(Work& w, bool launch, cudaStream_t st) {
-  using C = CfgF32<D, NH>;
+  using C = CfgF32<D, NH, kShares>;   // (the same sizes for every mode)
   plan_work(w, C::Stages::kTile, NH, C::kCtas);
   if (!launch) return ATTN_OK;
   const bool xf = w.p.softcap > 0.f || w.p.M != nullptr;
-  if (w.cluster)
-    return xf ? launch_pass(paged_f32_kernel<D, NH, true, true>, w, C::kSmem, st)
-              : launch_pass(paged_f32_kernel<D, NH, false, true>, w, C::kSmem, st);
-  return xf ? launch_pass(paged_f32_kernel<D, NH, true, false>, w, C::kSmem, st)
-            : launch_pass(paged_f32_kernel<D, NH, false, false>, w, C::kSmem, st);
+  auto go = [&](auto mode) {
+    constexpr int M = decltype(mode)::value;
+    return xf ? launch_pass(paged_f32_kernel<D, NH, true, M>, w, C::kSmem, st)
+              : launch_pass(paged_f32_kernel<D, NH, false, M>, w, C::kSmem, st);
+  };
+  return w.cluster  ? go(std::integral_constant<int, kCluster>())
+         : w.stride ? go(std::integral_constant<int, kWhole>())
+                    : go(std::integral_constant<int, kShares>());
 }
 
 template <int D>

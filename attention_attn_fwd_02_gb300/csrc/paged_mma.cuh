@@ -87,12 +87,12 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t w, bool high) {
 }
 
 // KV8: int8 cache (MMAs in f16).  NT: column tiles of 8 query heads.
-template <bool BF16, bool KV8, int D, int NT>
+template <bool BF16, bool KV8, int D, int NT, int MODE>
 struct Cfg {
   static constexpr int kRow = D * (KV8 ? 1 : 2);                  // bytes of a cache row
   static constexpr int kKeys = kRow <= 128 ? 32 : 16;             // keys of a warp's stage
   static constexpr int kStages = 2 * kKeys * kRow > 8192 ? 3 : 2;
-  using Stages = Ring<kRow, KV8 ? 1 : 2, kKeys, kStages>;
+  using Stages = Ring<kRow, KV8 ? 1 : 2, kKeys, kStages, MODE>;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRed = kWarps * kHeads * 64 * 4;           // merge buffer: 64 columns at a time
   static constexpr int kSmem = Stages::kBytes + kRed;
@@ -103,10 +103,10 @@ struct Cfg {
   static constexpr int kCtas = D == 256 ? (KV8 ? 2 : 1) : NT == 2 ? 2 : 3;
 };
 
-// XF: scores under a softcap or an additive mask.  CL: units held by clusters.
-template <bool BF16, bool KV8, int D, int NT, bool XF, bool CL>
-__global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_mma_kernel(const Work w) {
-  using C = Cfg<BF16, KV8, D, NT>;
+// XF: scores under a softcap or an additive mask.  MODE: how the units are divided.
+template <bool BF16, bool KV8, int D, int NT, bool XF, int MODE>
+__global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) paged_mma_kernel(const Work w) {
+  using C = Cfg<BF16, KV8, D, NT, MODE>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr bool MBF = BF16 && !KV8;   // MMA type bf16
   // P and (int8) Q in two halves, except where one f16 value is already eight times finer than a bf16 result.
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
   int64_t total = 0, t0 = 0;
   int shares = 0, my;   // tiles of this CTA
   Cursor out;           // the tile being computed
-  if constexpr (CL) {
+  if constexpr (MODE == kCluster) {
     const int unit = cta / w.cluster;
     out.b = unit / units;
     out.u = unit % units;
@@ -131,11 +131,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
     int end;
     list_part(out.n, cta % w.cluster, w.cluster, out.tile, end);
     my = end - out.tile;
+  } else if constexpr (MODE == kWhole) {
+    fill_entries<T>(w, cta);
+    if (!out.at_unit(w, units, cta)) return;
+    my = 0;
+    for (int64_t id = cta + (int64_t)lane * w.stride; id < (int64_t)p.B * units; id += 32 * (int64_t)w.stride)
+      my += entry_tiles(w, (int)(id / units));
+    my = __reduce_add_sync(kAll, my);
   } else {
     total = tiles_before(w, p.B, lane) * units;
     shares = (int)min((int64_t)w.ctas, total);
     let_next_start();
-    begin_share<T>(w, cta);
+    fill_entries<T>(w, cta);
+    if (threadIdx.x == 0) w.cuts[cta].b = -1;
     if (cta >= shares) return;
     t0 = share_begin(total, shares, cta);
     my = (int)(share_begin(total, shares, cta + 1) - t0);
@@ -443,16 +451,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
           }
           const int dd = 64 * part + d;
           if (KV8) a *= p.v_scale[p.kv_per_channel ? g * D + dd : 0];
-          if constexpr (CL) mine.put(D, hh, dd, M, L, a);
+          if constexpr (MODE == kCluster) mine.put(D, hh, dd, M, L, a);
           else put_row<T>(w, whole, cta, slot, out.b, h0 + hh, hh, dd, M, L, a);
         }
         __syncthreads();
       }
-      if (!CL && unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
+      if constexpr (MODE == kShares)
+        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {
-      out.next(w, units);
+      out.template next<MODE>(w, units);
       if (unit_ends) {
         first_tile = 0;
         load_q();
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
     }
   }
   copy_wait<0>();
-  if constexpr (CL) {
+  if constexpr (MODE == kCluster) {
     const int g = out.u / w.n_hc, h0 = g * p.qpg + (out.u % w.n_hc) * C::kHeads;
     const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
     if (my == 0)
@@ -473,15 +482,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT>::kCtas) paged_
 // Plans the pass; with `launch` enqueues it.
 template <bool BF16, bool KV8, int D, int NT>
 int pass_cfg(Work& w, bool launch, cudaStream_t st) {
-  using C = Cfg<BF16, KV8, D, NT>;
+  using C = Cfg<BF16, KV8, D, NT, kShares>;   // (the same sizes for every mode)
   plan_work(w, C::Stages::kTile, C::kHeads, C::kCtas);
   if (!launch) return ATTN_OK;
   const bool xf = w.p.softcap > 0.f || w.p.M != nullptr;
-  if (w.cluster)
-    return xf ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true, true>, w, C::kSmem, st)
-              : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false, true>, w, C::kSmem, st);
-  return xf ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true, false>, w, C::kSmem, st)
-            : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false, false>, w, C::kSmem, st);
+  auto go = [&](auto mode) {
+    constexpr int M = decltype(mode)::value;
+    return xf ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true, M>, w, C::kSmem, st)
+              : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false, M>, w, C::kSmem, st);
+  };
+  return w.cluster  ? go(std::integral_constant<int, kCluster>())
+         : w.stride ? go(std::integral_constant<int, kWhole>())
+                    : go(std::integral_constant<int, kShares>());
 }
 
 // Two column tiles of heads a unit for more than eight heads a kv head (at

@@ -384,6 +384,45 @@ def test_paged(i):
     assert attn.attn_device_status() == attn.ATTN_OK
 
 
+@pytest.mark.parametrize("dt,i8", [("bf16", False), ("f32", False), ("f16", True)])
+@pytest.mark.parametrize("B,G,lens,window", [(1, 2, 700, None), (90, 8, 100, None), (70, 8, 500, None), (3, 2, 6000, None),
+                                             (40, 4, 900, 70)])
+def test_paged_writes_nothing_outside(dt, i8, B, G, lens, window):
+    """The workspace the query asks for, the outputs, and not a byte beside them; every way of dividing the work."""
+    g = gen(43)
+    H, D, ps, guard = 2 * G, 64, 16, 4096
+    n = torch.randint(0, lens + 1, (B,), generator=g).to(torch.int32)
+    n[0] = lens
+    width = -(-lens // ps)
+    table = torch.randint(0, 50, (B, width), generator=g).to(torch.int32)
+    if i8:
+        k, v = (torch.randint(-128, 128, (50, G, ps, D), generator=g, dtype=torch.int8) for _ in range(2))
+    else:
+        k, v = randn(g, 50, G, ps, D, dt=DT[dt]), randn(g, 50, G, ps, D, dt=DT[dt])
+    sc = [torch.rand(G * D, generator=g) * 0.015 + 0.005 for _ in range(2)]
+    q = randn(g, B, 1, H, D, dt=DT[dt])
+    qd, kd, vd, td, nd, ks, vs = (t.cuda() for t in (q, k, v, table, n, *sc))
+    buf = torch.full((B * H * D + 2 * guard,), 7.0, dtype=DT[dt], device="cuda")
+    out = buf[guard:-guard].view(B, 1, H, D)
+    d = dict(batch=B, heads=H, kv_heads=G, q_len=1, k_len=lens, head_dim=D, dtype=dt, causal=window is not None,
+             causal_align="klens", window_left=window, masked_rows="zero", k_layout=attn._layout4(kd, 1),
+             v_layout=attn._layout4(vd, 1), q_layout=attn._layout4(qd, 2), o_layout=attn._layout4(out, 2))
+    if i8:
+        d.update(kv_dtype="i8", kv_scale="channel", k_scale_ptr=ks.data_ptr(), v_scale_ptr=vs.data_ptr())
+    p, pages = attn.make_problem(d), attn.make_pages(ps, 50, td.data_ptr(), td.stride(0))
+    size = attn.attn_decode_paged_workspace_size(p, pages, 0)
+    ws = torch.full((size + 2 * guard * 64,), 171, dtype=torch.uint8, device="cuda")
+    assert attn.attn_decode_paged(p, pages, 0, qd.data_ptr(), kd.data_ptr(), vd.data_ptr(), out.data_ptr(), None,
+                                  nd.data_ptr(), None, ws.data_ptr() + guard * 64, size,
+                                  torch.cuda.current_stream().cuda_stream) == 0
+    rk, rv = ref.gather(k, table, ps, lens, False)[0], ref.gather(v, table, ps, lens, False)[0]
+    vis = ref.visible(1, lens, n, window=-1 if window is None else window)
+    o, _, tol, _ = ref.attention(q.transpose(1, 2), rk, rv, vis, kv_scales=sc if i8 else None, half_q=i8)
+    ref.check(out.transpose(1, 2), o, tol)
+    assert (buf[:guard] == 7).all() and (buf[-guard:] == 7).all()
+    assert (ws[:guard * 64] == 171).all() and (ws[guard * 64 + size:] == 171).all()
+
+
 def test_paged_matches_the_contiguous_decode_and_shares_pages():
     """The rows of one entry as pages of a pool, two entries naming the same pages."""
     g = gen(5)
