@@ -3,9 +3,9 @@
 // The visible keys of a batch entry are a list of key tiles (visible.cuh).
 // Every (batch entry, kv head, chunk of its query heads) -- a unit -- walks its
 // entry's list, and the lists of all units, laid end to end, are cut into
-// equal shares, one a CTA: every SM streams the same number of cache bytes
-// whatever the entries' lengths, one launch fits short and long caches, and a
-// CTA's fixed cost is paid once.  A share's piece of a unit is a fragment.  A
+// shares of equal cost, one a CTA (a unit's end costs about what a tile does):
+// every SM streams as long as the others whatever the entries' lengths, one
+// launch fits short and long caches, and a CTA's fixed cost is paid once.  A share's piece of a unit is a fragment.  A
 // fragment that holds its unit's whole list writes the unit's rows of O; a CTA
 // has at most two others (its first and its last), whose partial results go
 // to two slots of the workspace, and the join kernel merges the fragments of a
@@ -61,19 +61,15 @@ __device__ __forceinline__ int entry_tiles(const Work& w, int b) {
   return tile_list(row_vis(w.p, w.x.first, b, 0), w.unit).n;
 }
 
-// Tiles of one unit of every entry in front of entry b (b = B: of all).  Warp-wide.
-__device__ __forceinline__ int64_t tiles_before(const Work& w, int b, int lane) {
-  int64_t n = 0;
-  for (int i = lane; i < b; i += 32) n += entry_tiles(w, i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
-  return n;
-}
+// What a unit with n tiles costs, in tiles: its end (merge, output, the next unit's queries) counts as kEnd more.
+// (3 against 1: 256 entries of up to 1000 rows, cut into shares, 106 -> 98 us, the batch of 64 181.0 -> 180.5.)
+constexpr int kEnd = 3;
+__device__ __forceinline__ int unit_cost(int n) { return n > 0 ? n + kEnd : 0; }
 
-// Shares: CTA c of n takes tiles [c * total / n, (c + 1) * total / n).
+// Shares: CTA c of n takes what lies in [c * total / n, (c + 1) * total / n) of the costs.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int share_of(int64_t total, int n, int64_t tile) {
-  return (int)(((tile + 1) * n - 1) / total);
+__device__ __forceinline__ int share_of(int64_t total, int n, int64_t at) {
+  return (int)(((at + 1) * n - 1) / total);
 }
 
 // A place in the list of all units: unit u of entry b, tile `tile` of its n.
@@ -116,33 +112,63 @@ struct Cursor {
   }
 };
 
-// The cursor at tile `at` of the whole list (at < total).  Warp-wide.
-__device__ __forceinline__ Cursor seek(const Work& w, int64_t at, int units, int lane) {
-  Cursor c;
-  int64_t before = 0;
-  c.b = 0;
-  for (int base = 0; base < w.p.B; base += 32) {
-    const int n = base + lane < w.p.B ? entry_tiles(w, base + lane) : 0;
-    int64_t incl = n;
+// A share: the total of the costs, the number of shares and where this one begins.
+struct Share {
+  int64_t total, t0;
+  int shares;
+};
+// CTA cta's share, its first tile and how many it has.  Warp-wide: the lanes
+// hold 32 entries at a time (their costs add up to less than 2^31).
+__device__ __forceinline__ int find_share(const Work& w, int units, int cta, int lane, Share& s, Cursor& out) {
+  const int n0 = lane < w.p.B ? entry_tiles(w, lane) : 0;
+  int64_t all = __reduce_add_sync(kAll, unit_cost(n0));
+  for (int base = 32; base < w.p.B; base += 32)
+    all += __reduce_add_sync(kAll, base + lane < w.p.B ? unit_cost(entry_tiles(w, base + lane)) : 0);
+  s.total = all * units;
+  s.shares = (int)min((int64_t)w.ctas, s.total);
+  if (cta >= s.shares) return 0;
+  s.t0 = share_begin(s.total, s.shares, cta);
+  const int64_t t1 = share_begin(s.total, s.shares, cta + 1);
+  int64_t before = 0, filled = 0;    // costs and entries with tiles of the chunks so far
+  int64_t from = -1, to = -1;        // tiles in front of t0 and t1
+  for (int base = 0; to < 0 && base < w.p.B; base += 32) {
+    const int n = base == 0 ? n0 : base + lane < w.p.B ? entry_tiles(w, base + lane) : 0;
+    const unsigned some = __ballot_sync(kAll, n > 0);
+    int cost = unit_cost(n);   // inclusive sum
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, incl, o);
-      if (lane >= o) incl += y;
+      const int y = __shfl_up_sync(kAll, cost, o);
+      if (lane >= o) cost += y;
     }
-    const unsigned hit = __ballot_sync(kAll, (before + incl) * units > at);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      c.b = base + l;
-      before += __shfl_sync(kAll, incl - n, l);
-      break;
+    // The entry of this chunk that holds place t: its lane; u and tile there.
+    auto place = [&](int64_t t, int l, int& u, int& tile) {
+      const int own = __shfl_sync(kAll, n, l), c = unit_cost(own);
+      const int64_t front = before + __shfl_sync(kAll, cost, l) - c, rem = t - front * units;
+      u = (int)(rem / c);
+      tile = (int)(rem - (int64_t)u * c);
+      return (front - kEnd * (filled + __popc(some & ((1u << l) - 1u)))) * units + (int64_t)u * own + min(tile, own);
+    };
+    int u, tile;
+    const unsigned h0 = __ballot_sync(kAll, (before + cost) * units > s.t0);
+    if (from < 0 && h0) {
+      out.b = base + __ffs(h0) - 1;
+      from = place(s.t0, __ffs(h0) - 1, out.u, out.tile);
     }
-    before += __shfl_sync(kAll, incl, 31);
+    const unsigned h1 = __ballot_sync(kAll, (before + cost) * units > t1 - 1);
+    if (h1) {   // tiles up to and with place t1 - 1
+      to = place(t1 - 1, __ffs(h1) - 1, u, tile);
+      to += tile < __shfl_sync(kAll, n, __ffs(h1) - 1);
+    }
+    before += __shfl_sync(kAll, cost, 31);
+    filled += __popc(some);
   }
-  c.load(w);
-  const int64_t rem = at - before * units;
-  c.u = (int)(rem / c.n);
-  c.tile = (int)(rem % c.n);
-  return c;
+  if (to <= from) return 0;
+  out.load(w);
+  if (out.tile >= out.n) {   // t0 is at a unit's end
+    out.tile = out.n - 1;
+    out.template next<kShares>(w, units);
+  }
+  return (int)(to - from);
 }
 
 // Copies 16 bytes to shared memory without waiting; sz = 0 writes zeros and reads nothing.
@@ -295,8 +321,8 @@ __device__ __forceinline__ void fill_entry(const Work& w, int b) {
   }
 }
 
-// What every CTA of a pass without clusters does first: its entries without a
-// visible key.
+// What every CTA of a pass without clusters does beside its units: its entries
+// without a visible key.
 template <typename T>
 __device__ __forceinline__ void fill_entries(const Work& w, int cta) {
   for (int b = cta; b < w.p.B; b += w.ctas)
@@ -304,11 +330,11 @@ __device__ __forceinline__ void fill_entries(const Work& w, int cta) {
 }
 
 // Notes a cut unit that ends in share `cta` (whose first fragment it is), `first` tiles into its list.
-__device__ __forceinline__ void note_cut(const Work& w, int64_t total, int shares, int64_t t0, int cta,
-                                         const Cursor& c, int first) {
-  const int64_t at = t0 - first;
-  const int c0 = share_of(total, shares, at);
-  w.cuts[cta] = {c.b, c.u, c0, share_begin(total, shares, c0) < at ? 1 : 0};
+__device__ __forceinline__ void note_cut(const Work& w, const Share& s, int cta, const Cursor& c, int first) {
+  const int64_t at = s.t0 - first;
+  const int c0 = share_of(s.total, s.shares, at);
+  // (Share c0 has a fragment in front of it if it begins in front of the last unit's end.)
+  w.cuts[cta] = {c.b, c.u, c0, share_begin(s.total, s.shares, c0) < at - kEnd ? 1 : 0};
 }
 
 // ---- units held by a cluster ----
@@ -381,13 +407,18 @@ __device__ __forceinline__ void cluster_join(const Work& w, const Part& part, in
 // Host: merges the fragments of cut units.  Enqueued right behind the pass.
 cudaError_t launch_join(const Work& w, cudaStream_t st);
 
-// Host: the work of a pass with `ctas` CTAs an SM.  Short lists: clusters of 8,
-// 4 or 2 CTAs a unit if all units then run at once and a CTA has at most eight
-// tiles; else, for lists of at most eight tiles, whole units.  Other problems:
-// shares, never more than there can be tiles.  Device time, bf16, 32/8 heads,
-// head_dim 128, shares against these: one sequence of 700 rows 11.3 -> 6.3 us,
-// 30 of up to 500 rows 18.2 -> 12.6 (clusters); 60 of up to 500 rows 28.2 ->
-// 23.3, 90 of up to 100 rows 20.7 -> 13.3 (whole units).
+// Host: the work of a pass with `ctas` CTAs an SM.  A cluster a unit, of the most
+// CTAs (8 to 2) with which all units run at once, if a CTA has at most 16 tiles,
+// or 24 when the units fill half of the machine or are no more than four (whose
+// many fragments a join would read in turn); else whole units, if a unit has at
+// most 24 tiles and the rounds of units are no more than 12 tiles longer than
+// equal shares; else shares, never more than there can be tiles.  Shares cost about 10
+// us more (finding the place, fragments, the join), the others' CTAs wait for the
+// longest list.  Device time, bf16, 32/8 heads, head_dim 128, shares against
+// these: one sequence of 700 rows 10.9 -> 6.4 us, 25 of up to 1500 rows 26.9 ->
+// 21.0, 12 of up to 6000 rows 41.8 -> 32.7 (clusters); 57 of 900 to 1000 rows
+// 48.9 -> 38.6, 90 of up to 100 rows 19.9 -> 12.6 (whole units); the other way
+// round, 8/8 heads: one sequence of 12000 rows 16.1 against 21.0 in clusters.
 inline void plan_work(Work& w, int tile, int heads, int ctas) {
   w.unit = tile;
   w.heads = heads;
@@ -398,12 +429,13 @@ inline void plan_work(Work& w, int tile, int heads, int ctas) {
     const int64_t seen = (int64_t)w.p.window + 1 + w.x.first + 2 * tile;   // both parts may end inside tiles
     span = seen < span ? seen : span;
   }
-  const int64_t list = (span + tile - 1) / tile, most = units * list;
+  const int64_t list = (span + tile - 1) / tile, most = units * list, rounds = (units + n - 1) / n;
   w.cluster = w.stride = 0;
-  for (int c = 8; c > 1 && !w.cluster; c /= 2)
-    if (units * c <= n && list <= 8 * c && list >= c) w.cluster = c;
+  for (int c = 8; c > 1 && !w.cluster; --c)
+    if (units * c <= n && list >= c && list <= (2 * units * c >= n || units <= 4 ? 24 : 16) * c) w.cluster = c;
   w.ctas = (int)(w.cluster ? units * w.cluster : most < 1 ? 1 : most < n ? most : n);
-  if (!w.cluster && list <= 8) w.stride = w.ctas = (int)(units < 1 ? 1 : units < n ? units : n);
+  if (!w.cluster && list <= 24 && (rounds < 2 || rounds * n * list <= most + 12 * n))
+    w.stride = w.ctas = (int)(units < 1 ? 1 : units < n ? units : n);
 }
 
 // Host: enqueues a pass, and the join behind shares.

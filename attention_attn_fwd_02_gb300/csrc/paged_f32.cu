@@ -51,9 +51,9 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
   const int units = p.G * w.n_hc;
 
   const int cta = blockIdx.x;
-  int64_t total = 0, t0 = 0;
-  int shares = 0, my;   // tiles of this CTA
-  Cursor out;           // the tile being computed
+  int my;       // tiles of this CTA
+  Cursor out;   // the tile being computed
+  __shared__ Share share;   // (thread 0's, for its notes of cut units)
   if constexpr (MODE == kCluster) {
     const int unit = cta / w.cluster;
     out.b = unit / units;
@@ -63,22 +63,21 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
     list_part(out.n, cta % w.cluster, w.cluster, out.tile, end);
     my = end - out.tile;
   } else if constexpr (MODE == kWhole) {
-    fill_entries<float>(w, cta);
-    if (!out.at_unit(w, units, cta)) return;
     my = 0;
     for (int64_t id = cta + (int64_t)lane * w.stride; id < (int64_t)p.B * units; id += 32 * (int64_t)w.stride)
       my += entry_tiles(w, (int)(id / units));
     my = __reduce_add_sync(kAll, my);
+    if (my) out.at_unit(w, units, cta);
   } else {
-    total = tiles_before(w, p.B, lane) * units;
-    shares = (int)min((int64_t)w.ctas, total);
     let_next_start();
-    fill_entries<float>(w, cta);
     if (threadIdx.x == 0) w.cuts[cta].b = -1;
-    if (cta >= shares) return;
-    t0 = share_begin(total, shares, cta);
-    my = (int)(share_begin(total, shares, cta + 1) - t0);
-    out = seek(w, t0, units, lane);
+    Share s;
+    my = find_share(w, units, cta, lane, s, out);
+    if (threadIdx.x == 0) share = s;
+  }
+  if (MODE != kCluster && my == 0) {
+    fill_entries<float>(w, cta);
+    return;
   }
   typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
 #pragma unroll
@@ -113,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
     }
   };
   reset();
+  if constexpr (MODE != kCluster) fill_entries<float>(w, cta);   // (while the first copies are under way)
   const int key = lane % KEYS, part = lane / KEYS;   // this lane's key of a stage and its share of the elements
   float* my_p = p_s + warp * KEYS * NH;
 
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
         __syncthreads();
       }
       if constexpr (MODE == kShares)
-        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
+        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, share, cta, out, first_tile);
       ++frag;
     }
     if (i + 1 < my) {

@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
   const int units = p.G * w.n_hc;
 
   const int cta = blockIdx.x;
-  int64_t total = 0, t0 = 0;
-  int shares = 0, my;   // tiles of this CTA
-  Cursor out;           // the tile being computed
+  int my;       // tiles of this CTA
+  Cursor out;   // the tile being computed
+  __shared__ Share share;   // (thread 0's, for its notes of cut units)
   if constexpr (MODE == kCluster) {
     const int unit = cta / w.cluster;
     out.b = unit / units;
@@ -132,22 +132,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     list_part(out.n, cta % w.cluster, w.cluster, out.tile, end);
     my = end - out.tile;
   } else if constexpr (MODE == kWhole) {
-    fill_entries<T>(w, cta);
-    if (!out.at_unit(w, units, cta)) return;
     my = 0;
     for (int64_t id = cta + (int64_t)lane * w.stride; id < (int64_t)p.B * units; id += 32 * (int64_t)w.stride)
       my += entry_tiles(w, (int)(id / units));
     my = __reduce_add_sync(kAll, my);
+    if (my) out.at_unit(w, units, cta);
   } else {
-    total = tiles_before(w, p.B, lane) * units;
-    shares = (int)min((int64_t)w.ctas, total);
     let_next_start();
-    fill_entries<T>(w, cta);
     if (threadIdx.x == 0) w.cuts[cta].b = -1;
-    if (cta >= shares) return;
-    t0 = share_begin(total, shares, cta);
-    my = (int)(share_begin(total, shares, cta + 1) - t0);
-    out = seek(w, t0, units, lane);
+    Share s;
+    my = find_share(w, units, cta, lane, s, out);
+    if (threadIdx.x == 0) share = s;
+  }
+  if (MODE != kCluster && my == 0) {
+    fill_entries<T>(w, cta);
+    return;
   }
   typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
 #pragma unroll
@@ -233,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     }
   };
   reset();
+  if constexpr (MODE != kCluster) fill_entries<T>(w, cta);   // (while the first copies are under way)
   const bool capped = XF && p.softcap > 0.f;
   const float cap2 = p.softcap * kLog2e, cap_inv = capped ? 1.f / cap2 : 0.f;
   // ldmatrix source rows and unit offsets of this lane (K: keys x channels; V transposed).
@@ -407,9 +407,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     if (unit_ends || i + 1 == my) {
       // The fragment ends: the four warps' results, merged in warp order, 64 columns at a time.
       const bool whole = unit_ends && first_tile == 0;
-      const int slot = frag == 0 ? 0 : 1;
+      const int slot = frag == 0 ? 0 : 1, b = out.b;
       const int g = out.u / w.n_hc, h0 = g * p.qpg + (out.u % w.n_hc) * C::kHeads;
       const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
+      if constexpr (MODE == kShares)
+        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, share, cta, out, first_tile);
+      if (i + 1 < my) {   // the next unit's queries arrive during the merge
+        out.template next<MODE>(w, units);
+        load_q();
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -452,21 +458,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           const int dd = 64 * part + d;
           if (KV8) a *= p.v_scale[p.kv_per_channel ? g * D + dd : 0];
           if constexpr (MODE == kCluster) mine.put(D, hh, dd, M, L, a);
-          else put_row<T>(w, whole, cta, slot, out.b, h0 + hh, hh, dd, M, L, a);
+          else put_row<T>(w, whole, cta, slot, b, h0 + hh, hh, dd, M, L, a);
         }
         __syncthreads();
       }
-      if constexpr (MODE == kShares)
-        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, total, shares, t0, cta, out, first_tile);
       ++frag;
-    }
-    if (i + 1 < my) {
-      out.template next<MODE>(w, units);
-      if (unit_ends) {
-        first_tile = 0;
-        load_q();
-        reset();
-      }
+      first_tile = 0;
+      reset();
+    } else {
+      ++out.tile;
     }
   }
   copy_wait<0>();

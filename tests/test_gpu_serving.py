@@ -385,8 +385,8 @@ def test_paged(i):
 
 
 @pytest.mark.parametrize("dt,i8", [("bf16", False), ("f32", False), ("f16", True)])
-@pytest.mark.parametrize("B,G,lens,window", [(1, 2, 700, None), (90, 8, 100, None), (70, 8, 500, None), (3, 2, 6000, None),
-                                             (40, 4, 900, 70)])
+@pytest.mark.parametrize("B,G,lens,window", [(1, 2, 700, None), (90, 8, 100, None), (70, 8, 500, None),
+                                             (58, 8, 1900, None), (40, 4, 900, 70)])
 def test_paged_writes_nothing_outside(dt, i8, B, G, lens, window):
     """The workspace the query asks for, the outputs, and not a byte beside them; every way of dividing the work."""
     g = gen(43)
@@ -757,6 +757,52 @@ def test_paged_many_entries():
                             masked_rows="zero")
     o, _, tol, _ = ref.attention(q.transpose(1, 2), k, v, ref.visible(1, ps, lens))
     ref.check(got.transpose(1, 2), o, tol)
+
+
+@pytest.mark.parametrize("dt,i8,D,H,G,B,rows,opt", [
+    ("f16", None, 64, 8, 8, 58, 1800, dict(zero=False)),
+    ("bf16", None, 128, 16, 8, 58, 900, dict(sink=True)),
+    ("bf16", "channel", 128, 16, 8, 58, 1700, {}),
+    ("f16", "tensor", 64, 24, 8, 59, 1800, dict(sink=True)),
+    ("f32", None, 64, 16, 8, 58, 900, dict(softcap=15.0)),
+    ("f32", None, 128, 64, 8, 39, 500, dict(sink=True)),
+    ("bf16", None, 256, 16, 8, 20, 900, dict(zero=False)),
+    ("bf16", None, 128, 72, 4, 39, 900, {}),
+    ("f16", None, 64, 8, 8, 60, 2500, dict(window=1500, first=5)),
+])
+def test_paged_shares(dt, i8, D, H, G, B, rows, opt):
+    """Lists too many and too long for clusters and whole units: cut anywhere, ends and empty entries among them."""
+    g = gen(47)
+    ps, w, first, zero = 16, opt.get("window", -1), opt.get("first", 0), opt.get("zero", True)
+    long = torch.rand(B, generator=g) < 0.4
+    n = torch.where(long, torch.randint(0, rows + 1, (B,), generator=g), torch.randint(0, 70, (B,), generator=g))
+    n[torch.rand(B, generator=g) < 0.1] = 0
+    n[B // 2] = rows
+    width = -(-rows // ps)
+    table = torch.randint(0, 60, (B, width), generator=g).to(torch.int32)
+    if i8:
+        k, v = (torch.randint(-128, 128, (60, G, ps, D), generator=g, dtype=torch.int8) for _ in range(2))
+        sc = [torch.rand(G * D if i8 == "channel" else 1, generator=g) * 0.015 + 0.005 for _ in range(2)]
+    else:
+        k, v, sc = randn(g, 60, G, ps, D, dt=DT[dt]), randn(g, 60, G, ps, D, dt=DT[dt]), None
+    q = randn(g, B, 1, H, D, dt=DT[dt])
+    sink = randn(g, H) if opt.get("sink") else None
+    kw = dict(masked_rows="zero" if zero else "nan", softcap=opt.get("softcap", 0.0), max_rows=rows,
+              window_left=None if w < 0 else w, first_keys=first, head_sink=None if sink is None else sink.cuda())
+    if i8:
+        kw.update(k_scale=sc[0].cuda(), v_scale=sc[1].cuda())
+    args = [t.cuda() for t in (q, k, v, table, n.to(torch.int32))]
+    got, lse = attn.decode_paged(*args, return_lse=True, **kw)
+    again = attn.decode_paged(*args, workspace=torch.full((1 << 22,), math.nan, device="cuda").view(torch.uint8), **kw)
+    assert torch.equal(got.nan_to_num(7.0), again.nan_to_num(7.0))
+    for b in range(B):
+        m = max(int(n[b]), 1)
+        rk, rv = (ref.gather(t, table[b:b + 1], ps, m, False)[0] for t in (k, v))
+        vis = ref.visible(1, m, n[b:b + 1], window=w, first=first)
+        o, l, tol, tol_l = ref.attention(q[b:b + 1].transpose(1, 2), rk, rv, vis, softcap=opt.get("softcap", 0.0),
+                                         sink=sink, zero=zero, kv_scales=sc, half_q=bool(i8) and dt != "f32")
+        ref.check(got[b:b + 1].transpose(1, 2), o, tol, f"O of entry {b}")
+        ref.check(lse[b:b + 1], l, tol_l, f"LSE of entry {b}")
 
 
 def test_python_entry_points_refuse():
