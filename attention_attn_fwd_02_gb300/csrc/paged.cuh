@@ -117,13 +117,16 @@ struct Share {
   int64_t total, t0;
   int shares;
 };
-// CTA cta's share, its first tile and how many it has.  Warp-wide: the lanes
-// hold 32 entries at a time (their costs add up to less than 2^31).
+// The sum over a warp's lanes of x >= 0, in 64 bits.
+__device__ __forceinline__ int64_t warp_sum(int x) {
+  return __reduce_add_sync(kAll, x & 0xffff) + ((int64_t)__reduce_add_sync(kAll, x >> 16) << 16);
+}
+// CTA cta's share, its first tile and how many it has.  Warp-wide: the lanes hold 32 entries at a time.
 __device__ __forceinline__ int find_share(const Work& w, int units, int cta, int lane, Share& s, Cursor& out) {
   const int n0 = lane < w.p.B ? entry_tiles(w, lane) : 0;
-  int64_t all = __reduce_add_sync(kAll, unit_cost(n0));
+  int64_t all = warp_sum(unit_cost(n0));
   for (int base = 32; base < w.p.B; base += 32)
-    all += __reduce_add_sync(kAll, base + lane < w.p.B ? unit_cost(entry_tiles(w, base + lane)) : 0);
+    all += warp_sum(base + lane < w.p.B ? unit_cost(entry_tiles(w, base + lane)) : 0);
   s.total = all * units;
   s.shares = (int)min((int64_t)w.ctas, s.total);
   if (cta >= s.shares) return 0;
@@ -134,10 +137,10 @@ __device__ __forceinline__ int find_share(const Work& w, int units, int cta, int
   for (int base = 0; to < 0 && base < w.p.B; base += 32) {
     const int n = base == 0 ? n0 : base + lane < w.p.B ? entry_tiles(w, base + lane) : 0;
     const unsigned some = __ballot_sync(kAll, n > 0);
-    int cost = unit_cost(n);   // inclusive sum
+    int64_t cost = unit_cost(n);   // inclusive sum
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, cost, o);
+      const int64_t y = __shfl_up_sync(kAll, cost, o);
       if (lane >= o) cost += y;
     }
     // The entry of this chunk that holds place t: its lane; u and tile there.
