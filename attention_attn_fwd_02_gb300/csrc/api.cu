@@ -328,14 +328,20 @@ int decode_impl(const attn_problem* p, const void* q, const void* k_cache, const
   }
   return from_cuda(launch_combine(r, s, p->dtype, st));
 }
+// Workspace of ranges whose maxima and sums are kept apart (Split::part_l).
+size_t sums_ws_bytes(const attn_problem* p, int n_splits) {
+  return decode_ws_bytes(p, n_splits) + round256((size_t)p->batch * p->heads * p->q_len * n_splits * sizeof(float));
+}
+
 // The partial-result arrays of a split pass over `rows` rows in a workspace.
-Split split_in(void* workspace, size_t rows, int n_splits, int split_len, int D) {
+Split split_in(void* workspace, size_t rows, int n_splits, int split_len, int D, bool sums) {
   Split s;
   s.n_splits = n_splits;
   s.split_len = split_len;
   s.part_o = static_cast<float*>(workspace);
   s.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                         round256(rows * n_splits * D * sizeof(float)));
+  if (sums) s.part_l = s.part_lse + round256(rows * n_splits * sizeof(float)) / sizeof(float);
   return s;
 }
 
@@ -422,7 +428,7 @@ int paged_plan(const attn_problem* p, int32_t first_keys) {
 size_t paged_bytes(const attn_problem* p, int32_t first_keys) {
   int status = 0;
   const Problem r = resolve(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, &status);
-  const size_t a = decode_ws_bytes(p, paged_plan(p, first_keys)), b = paged_ws_bytes(r, first_keys);
+  const size_t a = sums_ws_bytes(p, paged_plan(p, first_keys)), b = paged_ws_bytes(r, first_keys);
   return a > b ? a : b;
 }
 
@@ -537,9 +543,13 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   Split s{1, p->k_len > 0 ? p->k_len : 1, nullptr, nullptr};
   if (n > 1 && !cluster) {
     const bool enough = workspace && workspace_bytes >= decode_ws_bytes(p, n);
-    if (enough && aligned(workspace, 256))
-      s = split_in(workspace, (size_t)p->batch * p->heads * p->q_len, n, 0, p->head_dim);
-    else if (p->key_splits > 1)
+    if (enough && aligned(workspace, 256)) {
+      // Under a mask the parts' sums take the room of a part.
+      int parts = n;
+      while (mask && parts > 1 && sums_ws_bytes(p, parts) > decode_ws_bytes(p, n)) --parts;
+      if (parts > 1)
+        s = split_in(workspace, (size_t)p->batch * p->heads * p->q_len, parts, 0, p->head_dim, mask != nullptr);
+    } else if (p->key_splits > 1)
       return enough ? ATTN_ERR_ALIGNMENT : ATTN_ERR_WORKSPACE;
   }
   int* status = nullptr;
@@ -587,7 +597,7 @@ int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t fi
   int used = 0;
   rc = paged_try(r, x, workspace, st, &used);
   if (rc || used) return rc;
-  const Split s = split_in(workspace, (size_t)p->batch * p->heads, n, 0, p->head_dim);
+  const Split s = split_in(workspace, (size_t)p->batch * p->heads, n, 0, p->head_dim, true);
   rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;
   return from_cuda(launch_combine(r, s, p->dtype, st));

@@ -56,6 +56,9 @@ struct Split {
   int split_len;     // keys per range (multiple of 32)
   float* part_o;     // [rows][n_splits][D], rows = B*H*Sq in (b, h, i) order
   float* part_lse;   // [rows][n_splits]
+  // Not null: part_lse holds the ranges' maxima and part_l their sums (0: empty).  A mask near the lowest float32
+  // leaves no room for the logarithm of a sum in an LSE, and the merge would weigh the ranges alike.
+  float* part_l = nullptr;
 };
 
 __device__ __forceinline__ float to_f32(float x) { return x; }

@@ -25,6 +25,7 @@ bool pass(Work& w, bool launch, cudaStream_t st, int* rc) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 size_t rows_of(const Work& w) { return (size_t)w.ctas * 2 * w.heads; }
+size_t sums_bytes(const Work& w) { return round256(rows_of(w) * 2 * sizeof(float)); }   // part_m and part_l
 
 }  // namespace
 }  // namespace paged
@@ -35,7 +36,7 @@ size_t paged_ws_bytes(const Problem& p, int first) {
   w.x.first = first;
   int rc = 0;
   if (p.B < 1 || !paged::pass(w, false, nullptr, &rc) || w.cluster || w.stride) return 0;
-  return paged::round256(paged::rows_of(w) * p.D * 4) + paged::round256(paged::rows_of(w) * 4) +
+  return paged::round256(paged::rows_of(w) * p.D * sizeof(float)) + paged::sums_bytes(w) +
          paged::round256(w.ctas * sizeof(paged::CutUnit));
 }
 
@@ -55,10 +56,10 @@ int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, 
   if (!paged::pass(w, false, st, &rc)) return ATTN_OK;
   if (!w.cluster && !w.stride) {   // only shares have fragments
     w.part_o = static_cast<float*>(workspace);
-    w.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                          paged::round256(paged::rows_of(w) * p.D * sizeof(float)));
-    w.cuts = reinterpret_cast<paged::CutUnit*>(reinterpret_cast<char*>(w.part_lse) +
-                                               paged::round256(paged::rows_of(w) * sizeof(float)));
+    w.part_m = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        paged::round256(paged::rows_of(w) * p.D * sizeof(float)));
+    w.part_l = w.part_m + paged::rows_of(w);
+    w.cuts = reinterpret_cast<paged::CutUnit*>(reinterpret_cast<char*>(w.part_m) + paged::sums_bytes(w));
   }
   *used = 1;
   paged::pass(w, true, st, &rc);

@@ -51,7 +51,8 @@ struct Work {
   int n_hc;        // chunks of a kv head's query heads
   int ctas;        // shares
   float* part_o;   // [ctas][2][heads][D]
-  float* part_lse; // [ctas][2][heads]
+  float* part_m;   // [ctas][2][heads]  natural maxima (-inf: no visible key)
+  float* part_l;   // [ctas][2][heads]  sums (maxima apart: Split::part_l says why)
   CutUnit* cuts;   // [ctas]
   int cluster;     // > 0: CTAs of the cluster that holds one unit (no shares)
   int stride;      // > 0: CTA c takes the units c, c + stride, ... (no shares)
@@ -286,25 +287,29 @@ struct Ring {
   }
 };
 
-// Where a row's finished fragment goes.  M: reference maximum in log2 units
-// (-inf: no visible key), L: sum relative to it, a: numerator of element d.
-template <typename T>
+// Where a row's finished fragment goes.  M: reference maximum in the units of
+// Scores<NAT> (-inf: no visible key), L: sum relative to it, a: numerator of element d.
+template <typename T, bool NAT>
 __device__ __forceinline__ void put_row(const Work& w, bool whole, int cta, int slot, int b, int h, int hh, int d,
                                         float M, float L, float a) {
   const Problem& p = w.p;
+  M = Scores<NAT>::natural(M);
   if (!whole) {
     const int64_t at = ((int64_t)cta * 2 + slot) * w.heads + hh;
     const bool none = L == 0.f;
     w.part_o[at * p.D + d] = none ? 0.f : a / L;
-    if (d == 0) w.part_lse[at] = none ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (d == 0) {
+      w.part_m[at] = none ? -INFINITY : M;
+      w.part_l[at] = L;
+    }
     return;
   }
-  if (p.sink_on) a *= fold_sink<true>(M, L, sink_logit(p, h) * kLog2e);
+  if (p.sink_on) a *= fold_sink<false>(M, L, sink_logit(p, h));
   const bool none = L == 0.f;
   static_cast<T*>(p.O)[p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs + d] =
       from_f32<T>(none ? (p.masked_zero ? 0.f : NAN) : a / L);
   if (p.lse && d == 0)
-    p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs] = none ? -INFINITY : (M + log2f(L)) * kLn2;
+    p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs] = none ? -INFINITY : Scores<NAT>::lse(M, log2f(L));
 }
 
 // What a row without a visible key returns, for all heads of entry b.  The
@@ -315,12 +320,12 @@ __device__ __forceinline__ void fill_entry(const Work& w, int b) {
   for (int x = threadIdx.x; x < p.H * p.D; x += kThreads) {
     const int h = x / p.D, d = x - h * p.D;
     float M = -INFINITY, L = 0.f;
-    if (p.sink_on) fold_sink<true>(M, L, sink_logit(p, h) * kLog2e);
+    if (p.sink_on) fold_sink<false>(M, L, sink_logit(p, h));
     const bool none = L == 0.f;
     static_cast<T*>(p.O)[p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs + d] =
         from_f32<T>(none ? (p.masked_zero ? 0.f : NAN) : 0.f / L);
     if (p.lse && d == 0)
-      p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs] = none ? -INFINITY : (M + log2f(L)) * kLn2;
+      p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs] = none ? -INFINITY : M + logf(L);
   }
 }
 
@@ -380,7 +385,7 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Merges the parts of the unit (b, heads h0 ..) that the cluster's CTAs hold; each CTA writes its share of the rows.
-template <typename T>
+template <typename T, bool NAT>
 __device__ __forceinline__ void cluster_join(const Work& w, const Part& part, int b, int h0, int nh) {
   const int D = w.p.D, n = w.cluster;
   cluster_sync();
@@ -398,11 +403,11 @@ __device__ __forceinline__ void cluster_join(const Work& w, const Part& part, in
     const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float f = ex2_approx(m[q] - mu);
+      const float f = Scores<NAT>::weight(m[q], mu);
       L = fmaf(f, l[q], L);
       A = fmaf(f, a[q], A);
     }
-    put_row<T>(w, true, 0, 0, b, h0 + hh, hh, d, M, L, A);
+    put_row<T, NAT>(w, true, 0, 0, b, h0 + hh, hh, d, M, L, A);
   }
   cluster_sync();   // no CTA leaves while its part is being read
 }

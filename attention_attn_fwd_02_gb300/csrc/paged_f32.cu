@@ -85,9 +85,10 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
     if (s < my) ring.issue(s, s + 1 < my);
     copy_commit();
   }
-  // The unit's queries, scaled to log2 units (a softcap wants them in natural units).
+  using S = Scores<XF>;   // (masks come with XF)
   const bool capped = XF && p.softcap > 0.f;
-  const float qscale = capped ? p.scale : p.scale * kLog2e;
+  const float qscale = p.scale * S::kUnit;
+  constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
   auto load_q = [&]() {
     const int g = out.u / w.n_hc, c0 = out.u % w.n_hc * NH;
     for (int x = threadIdx.x; x < NH * D; x += kThreads) {
@@ -148,15 +149,14 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
         for (int x = KEYS; x < 32; x <<= 1) sc[h] += __shfl_xor_sync(kAll, sc[h], x);
         float v = sc[h] * qscale;
         if (XF) {
-          if (capped) v = p.softcap * tanhf(v / p.softcap) * kLog2e;
+          if (capped) v = p.softcap * tanhf(v / p.softcap);
           const int in_kv = out.u % w.n_hc * NH + h;
           if (p.M && seen && in_kv < p.qpg)
-            v = fmaf(p.M[p.m.off + (int64_t)out.b * p.m.bs + (int64_t)(out.u / w.n_hc * p.qpg + in_kv) * p.m.hs +
-                         st_key[warp][s] + key],
-                     kLog2e, v);
+            v += p.M[p.m.off + (int64_t)out.b * p.m.bs + (int64_t)(out.u / w.n_hc * p.qpg + in_kv) * p.m.hs +
+                     st_key[warp][s] + key];
         }
         sc[h] = seen ? v : -INFINITY;
-        rise |= sc[h] > m_ref[h] + kSlack;
+        rise |= sc[h] > m_ref[h] + kRise;
       }
       if (__any_sync(kAll, rise)) {
 #pragma unroll
@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
           float mx = sc[h];
 #pragma unroll
           for (int x = 1; x < KEYS; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, x));
-          if (mx > m_ref[h] + kSlack) {
-            const float f = ex2_approx(m_ref[h] - mx);
+          if (mx > m_ref[h] + kRise) {
+            const float f = S::weight(m_ref[h], mx);
             l[h] *= f;
 #pragma unroll
             for (int v = 0; v < VU; ++v)
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        sc[h] = ex2_approx(sc[h] - (m_ref[h] == -INFINITY ? 0.f : m_ref[h]));
+        sc[h] = S::weight(sc[h], m_ref[h] == -INFINITY ? 0.f : m_ref[h]);
         l[h] += sc[h];   // (the lanes of a key hold the same value: one of them is counted at the end)
       }
       if (part == 0) {
@@ -254,12 +254,12 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
           float L = 0.f, a = 0.f;
 #pragma unroll
           for (int v = 0; v < kWarps; ++v) {
-            const float f = ex2_approx(red_m[v][hb + z] - mu);
+            const float f = S::weight(red_m[v][hb + z], mu);
             L = fmaf(f, red_l[v][hb + z], L);
             a = fmaf(f, red[(v * 4 + z) * D + d], a);
           }
           if constexpr (MODE == kCluster) mine.put(D, hb + z, d, M, L, a);
-          else put_row<float>(w, whole, cta, slot, out.b, h0 + hb + z, hb + z, d, M, L, a);
+          else put_row<float, XF>(w, whole, cta, slot, out.b, h0 + hb + z, hb + z, d, M, L, a);
         }
         __syncthreads();
       }
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
     const int nh = min(NH, (g + 1) * p.qpg - h0);
     if (my == 0)
       for (int x = threadIdx.x; x < nh * D; x += kThreads) mine.put(D, x / D, x % D, -INFINITY, 0.f, 0.f);
-    cluster_join<float>(w, mine, out.b, h0, nh);
+    cluster_join<float, XF>(w, mine, out.b, h0, nh);
   }
 }
 

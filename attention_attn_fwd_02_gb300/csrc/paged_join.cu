@@ -2,7 +2,7 @@
 //
 // A unit is cut when its tile list crosses the end of a share; the share that
 // ends it has noted where it began, and the CTA of that share's number merges
-// the unit: O = sum_f exp(lse_f - M) O_f / sum_f exp(lse_f - M), in an order
+// the unit: O = sum_f l_f exp(m_f - M) O_f / sum_f l_f exp(m_f - M), in an order
 // fixed by the cut, with the sink's logit as one more term of the denominator.
 // The kernel is launched as the pass's programmatic dependent: its CTAs are in
 // place when the pass ends.  Its time is the latency of the fragments' loads,
@@ -37,8 +37,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
     bool bad = isnan(sg) || sg == INFINITY;
     float M = bad ? -INFINITY : sg;
     for (int f = lane; f < count; f += 32) {
-      const float x = w.part_lse[slot_row(f, hh)];
-      if (isnan(x) || x == INFINITY) bad = true;
+      const int64_t at = slot_row(f, hh);
+      const float x = w.part_m[at];
+      if (x == INFINITY || isnan(w.part_l[at])) bad = true;
       else M = fmaxf(M, x);
     }
     bad = __any_sync(kAll, bad);
@@ -47,8 +48,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
     float sum = 0.f;
     if (!bad && M != -INFINITY) {
       for (int f = lane; f < count; f += 32) {
-        const float x = w.part_lse[slot_row(f, hh)];
-        sum += x == -INFINITY ? 0.f : expf(x - M);
+        const int64_t at = slot_row(f, hh);
+        const float x = w.part_m[at];
+        sum += x == -INFINITY ? 0.f : w.part_l[at] * expf(x - M);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
     const bool normal = M == M && M != -INFINITY;
     if (normal) {
       for (int f0 = groups > 1 ? group : 0; f0 < count; f0 += 8 * groups) {
-        float x[8];
+        float x[8], l[8];
         float4 v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -82,14 +84,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
           x[q] = -INFINITY;
           if (f < count) {
             const int64_t at = slot_row(f, hh);
-            x[q] = w.part_lse[at];
+            x[q] = w.part_m[at];
+            l[q] = w.part_l[at];
             v[q] = *reinterpret_cast<const float4*>(w.part_o + at * D + d);
           }
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           if (x[q] == -INFINITY) continue;   // an empty fragment
-          const float k = expf(x[q] - M);
+          const float k = l[q] * expf(x[q] - M);
           acc.x = fmaf(k, v[q].x, acc.x);
           acc.y = fmaf(k, v[q].y, acc.y);
           acc.z = fmaf(k, v[q].z, acc.z);

@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
   constexpr bool MBF = BF16 && !KV8;   // MMA type bf16
   // P and (int8) Q in two halves, except where one f16 value is already eight times finer than a bf16 result.
   constexpr bool SPLIT = !(BF16 && KV8);
+  using S = Scores<XF>;   // (masks come with XF)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int st_key[kWarps][C::kStages];         // first key of a warp's stage
   __shared__ uint32_t st_vis[kWarps][C::kStages];    // which of its keys are visible
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
             const uint16_t* src = reinterpret_cast<const uint16_t*>(row + d);
             qh[j][c][e] = hh < nh ? (uint32_t)src[0] | ((uint32_t)src[1] << 16) : 0u;
           }
-        cs[j][0] = cs[j][1] = p.scale * kLog2e;
+        cs[j][0] = cs[j][1] = p.scale * S::kUnit;
       } else {
         // Channels 4t, 4t + 2 (then 4t + 1, 4t + 3) of a 16-channel block: the order in which the bytes arrive.
         float v[D / 16][4], top = 0.f;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
             ql[j][c][1] = rest[1];
           }
         }
-        const float down = p.scale * kLog2e * ldexpf(1.f, -ex);
+        const float down = p.scale * S::kUnit * ldexpf(1.f, -ex);
         cs[j][0] = __shfl_sync(kAll, down, 8 * tig);       // heads 2 tig and 2 tig + 1 of the column tile
         cs[j][1] = __shfl_sync(kAll, down, 8 * tig + 4);
       }
@@ -234,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
   reset();
   if constexpr (MODE != kCluster) fill_entries<T>(w, cta);   // (while the first copies are under way)
   const bool capped = XF && p.softcap > 0.f;
-  const float cap2 = p.softcap * kLog2e, cap_inv = capped ? 1.f / cap2 : 0.f;
+  const float cap_inv = capped ? 1.f / p.softcap : 0.f;
+  constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
   // ldmatrix source rows and unit offsets of this lane (K: keys x channels; V transposed).
   const int lk_row = (lane & 7) + ((lane >> 3) & 1) * 8, lk_u = lane >> 4;
   const int lv_row = KV8 ? lk_row : (lane & 7) + (lane >> 4) * 8, lv_u = KV8 ? lane >> 4 : (lane >> 3) & 1;
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           }
         }
       }
-      // Scores in log2 units.
+      // Scores.
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -295,13 +297,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           float x = (sc[mb][j][e] + sd[j][e]) * cs[j][e & 1];
           if (XF) {
             const int r = 16 * mb + gid + 8 * (e >> 1);
-            if (capped) x = cap2 * tanh_exp2(x * cap_inv);
+            if (capped) x = p.softcap * tanh_exp2(x * cap_inv);
             const int hh = 8 * j + 2 * tig + (e & 1);
             const int in_kv = (out.u % w.n_hc) * C::kHeads + hh;
             if (p.M && in_kv < p.qpg && ((vis >> r) & 1u))
-              x = fmaf(p.M[p.m.off + (int64_t)out.b * p.m.bs +
-                           (int64_t)(out.u / w.n_hc * p.qpg + in_kv) * p.m.hs + st_key[warp][s] + r],
-                       kLog2e, x);
+              x += p.M[p.m.off + (int64_t)out.b * p.m.bs + (int64_t)(out.u / w.n_hc * p.qpg + in_kv) * p.m.hs +
+                       st_key[warp][s] + r];
           }
           sc[mb][j][e] = x;
         }
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
         top[j][q] = fmaxf(sc[0][j][q], sc[0][j][q + 2]);
 #pragma unroll
         for (int mb = 1; mb < MB; ++mb) top[j][q] = fmaxf(top[j][q], fmaxf(sc[mb][j][q], sc[mb][j][q + 2]));
-        rise |= top[j][q] > m_ref[j][q] + kSlack;
+        rise |= top[j][q] > m_ref[j][q] + kRise;
       }
     if (__any_sync(kAll, rise)) {
 #pragma unroll
@@ -336,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-          if (mx > m_ref[j][q] + kSlack) {
-            const float f = ex2_approx(m_ref[j][q] - mx);
+          if (mx > m_ref[j][q] + kRise) {
+            const float f = S::weight(m_ref[j][q], mx);
             l[j][q] *= f;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -356,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         float e[4];
-        e[0] = ex2_approx(sc[mb][j][0] - mu0);
-        e[1] = ex2_approx(sc[mb][j][1] - mu1);
-        e[2] = ex2_approx(sc[mb][j][2] - mu0);
-        e[3] = ex2_approx(sc[mb][j][3] - mu1);
+        e[0] = S::weight(sc[mb][j][0], mu0);
+        e[1] = S::weight(sc[mb][j][1], mu1);
+        e[2] = S::weight(sc[mb][j][2], mu0);
+        e[3] = S::weight(sc[mb][j][3], mu1);
         l[j][0] += e[0] + e[2];
         l[j][1] += e[1] + e[3];
 #pragma unroll
@@ -451,14 +452,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           float L = 0.f, a = 0.f;
 #pragma unroll
           for (int v = 0; v < kWarps; ++v) {
-            const float f = ex2_approx(red_m[v][hh] - mu);
+            const float f = S::weight(red_m[v][hh], mu);
             L = fmaf(f, red_l[v][hh], L);
             a = fmaf(f, red[(v * C::kHeads + hh) * 64 + d], a);
           }
           const int dd = 64 * part + d;
           if (KV8) a *= p.v_scale[p.kv_per_channel ? g * D + dd : 0];
           if constexpr (MODE == kCluster) mine.put(D, hh, dd, M, L, a);
-          else put_row<T>(w, whole, cta, slot, b, h0 + hh, hh, dd, M, L, a);
+          else put_row<T, XF>(w, whole, cta, slot, b, h0 + hh, hh, dd, M, L, a);
         }
         __syncthreads();
       }
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
     if (my == 0)
       for (int x = threadIdx.x; x < nh * D; x += kThreads) mine.put(D, x / D, x % D, -INFINITY, 0.f, 0.f);
-    cluster_join<T>(w, mine, out.b, h0, nh);
+    cluster_join<T, XF>(w, mine, out.b, h0, nh);
   }
 }
 

@@ -17,10 +17,11 @@ namespace {
 // and broadcast the weights; the partial rows of four ranges are loaded
 // before they are summed, so the loads overlap instead of queueing behind one
 // another.  Ranges with weight 0 (empty, or underflowed) are left out of the
-// sum by a select, so an unwritten partial never reaches it.
+// sum by a select, so an unwritten partial never reaches it.  With part_l the
+// ranges give maxima and sums in place of LSEs (Split).
 template <typename T>
 __global__ void __launch_bounds__(128) combine_kernel(int n_splits, int64_t rows, int D, const float* part_o,
-                                                      const float* part_lse, T* O, Layout ol, int H, int Sq,
+                                                      const float* part_lse, const float* part_l, T* O, Layout ol, int H, int Sq,
                                                       float* lse, int64_t lse_bs, int64_t lse_hs,
                                                       int64_t lse_rs, int masked_zero, int sink_on,
                                                       const float* sink) {
@@ -29,6 +30,7 @@ __global__ void __launch_bounds__(128) combine_kernel(int n_splits, int64_t rows
   const int lane = threadIdx.x % 32;
   if (row >= rows) return;
   const float* pl = part_lse + row * n_splits;
+  const float* sums = part_l ? part_l + row * n_splits : nullptr;
   const int i = (int)(row % Sq);
   const int h = (int)((row / Sq) % H);
   const float sg = sink_on ? (sink ? sink[h] : 0.f) : -INFINITY;
@@ -36,7 +38,7 @@ __global__ void __launch_bounds__(128) combine_kernel(int n_splits, int64_t rows
   float M = bad ? -INFINITY : sg;
   for (int r = lane; r < n_splits; r += 32) {
     const float x = pl[r];
-    if (isnan(x) || x == INFINITY) bad = true;
+    if (isnan(x) || x == INFINITY || (sums && isnan(sums[r]))) bad = true;
     else M = fmaxf(M, x);
   }
   bad = __any_sync(kAll, bad);
@@ -53,7 +55,8 @@ __global__ void __launch_bounds__(128) combine_kernel(int n_splits, int64_t rows
     for (int base = 0; base < n_splits; base += 32) {
       const int r = base + lane;
       const float x = r < n_splits ? pl[r] : -INFINITY;
-      const float wr = x == -INFINITY ? 0.f : expf(x - M);
+      float wr = x == -INFINITY ? 0.f : expf(x - M);
+      if (sums && wr != 0.f) wr *= sums[r];
       ws += wr;
       const int nr = min(32, n_splits - base);
       for (int k = 0; k < nr; k += 4) {
@@ -90,29 +93,30 @@ __global__ void __launch_bounds__(128) combine_kernel(int n_splits, int64_t rows
 }
 
 template <typename T>
-cudaError_t launch_combine_t(int n_splits, int64_t rows, int D, const float* po, const float* pl, void* o,
+cudaError_t launch_combine_t(int n_splits, int64_t rows, int D, const float* po, const float* pl, const float* sums,
+                             void* o,
                              Layout ol, int H, int Sq, float* lse, int64_t lbs, int64_t lhs, int64_t lrs,
                              int masked_zero, int sink_on, const float* sink, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   const int64_t blocks = (rows + 3) / 4;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  combine_kernel<T><<<(unsigned)blocks, 128, 0, st>>>(n_splits, rows, D, po, pl, static_cast<T*>(o), ol, H, Sq,
+  combine_kernel<T><<<(unsigned)blocks, 128, 0, st>>>(n_splits, rows, D, po, pl, sums, static_cast<T*>(o), ol, H, Sq,
                                                       lse, lbs, lhs, lrs, masked_zero, sink_on, sink);
   return cudaGetLastError();
 }
 
 cudaError_t combine_dispatch(int32_t dt, int n_splits, int64_t rows, int D, const float* po, const float* pl,
-                             void* o, Layout ol, int H, int Sq, float* lse, int64_t lbs, int64_t lhs,
+                             const float* sums, void* o, Layout ol, int H, int Sq, float* lse, int64_t lbs, int64_t lhs,
                              int64_t lrs, int masked_zero, int sink_on, const float* sink, cudaStream_t st) {
   switch (dt) {
     case ATTN_F32:
-      return launch_combine_t<float>(n_splits, rows, D, po, pl, o, ol, H, Sq, lse, lbs, lhs, lrs, masked_zero,
+      return launch_combine_t<float>(n_splits, rows, D, po, pl, sums, o, ol, H, Sq, lse, lbs, lhs, lrs, masked_zero,
                                      sink_on, sink, st);
     case ATTN_F16:
-      return launch_combine_t<__half>(n_splits, rows, D, po, pl, o, ol, H, Sq, lse, lbs, lhs, lrs, masked_zero,
+      return launch_combine_t<__half>(n_splits, rows, D, po, pl, sums, o, ol, H, Sq, lse, lbs, lhs, lrs, masked_zero,
                                       sink_on, sink, st);
     default:
-      return launch_combine_t<__nv_bfloat16>(n_splits, rows, D, po, pl, o, ol, H, Sq, lse, lbs, lhs, lrs,
+      return launch_combine_t<__nv_bfloat16>(n_splits, rows, D, po, pl, sums, o, ol, H, Sq, lse, lbs, lhs, lrs,
                                              masked_zero, sink_on, sink, st);
   }
 }
@@ -126,15 +130,15 @@ cudaError_t launch_simt(const Problem& p, const Split& s, cudaStream_t st) {
 
 cudaError_t launch_combine(const Problem& p, const Split& s, int32_t out_dtype, cudaStream_t st) {
   const int64_t rows = (int64_t)p.B * p.H * p.Sq;
-  return combine_dispatch(out_dtype, s.n_splits, rows, p.D, s.part_o, s.part_lse, p.O, p.o, p.H, p.Sq, p.lse,
-                          p.lse_bs, p.lse_hs, 1, p.masked_zero, p.sink_on, p.sink, st);
+  return combine_dispatch(out_dtype, s.n_splits, rows, p.D, s.part_o, s.part_lse, s.part_l, p.O, p.o, p.H, p.Sq,
+                          p.lse, p.lse_bs, p.lse_hs, 1, p.masked_zero, p.sink_on, p.sink, st);
 }
 
 cudaError_t launch_combine_flat(int n_splits, int rows, int D, const float* part_o, const float* part_lse,
                                 int32_t out_dtype, void* o, int64_t o_row_stride, float* lse, int masked_zero,
                                 cudaStream_t st) {
   Layout ol{0, 0, 0, o_row_stride};
-  return combine_dispatch(out_dtype, n_splits, rows, D, part_o, part_lse, o, ol, 1, rows, lse, 0, 0, 1,
+  return combine_dispatch(out_dtype, n_splits, rows, D, part_o, part_lse, nullptr, o, ol, 1, rows, lse, 0, 0, 1,
                           masked_zero, 0, nullptr, st);
 }
 

@@ -320,7 +320,11 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
 #pragma unroll
     for (int s = 0; s < kSlots; ++s)
       if (has(s)) po[dim_of(s)] = hidden ? 0.f : acc[s] / l;
-    if (lr == 0) sp.part_lse[row * sp.n_splits + split] = hidden ? -INFINITY : m + logf(l);
+    if (lr == 0) {
+      const bool sums = EXT && sp.part_l;
+      sp.part_lse[row * sp.n_splits + split] = hidden ? -INFINITY : sums ? m : m + logf(l);
+      if (sums) sp.part_l[row * sp.n_splits + split] = l;
+    }
   }
 }
 

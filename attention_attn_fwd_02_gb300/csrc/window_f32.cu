@@ -32,8 +32,7 @@ using paged::smem_u32;
 
 constexpr int kThreads = 128;
 constexpr int BN = 32;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994531f;
+using S = Scores<true>;   // (one instance with and without a mask: a product more for each D of a score)
 
 template <int D, int TM>
 struct Cfg {
@@ -130,7 +129,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[r][c][e] = 0.f;
   }
-  const float sc = p.scale * kLog2e;
   for (int ti = t0; ti < t1; ++ti) {
     const int k0 = tl.tile(ti) * BN;
     copy_wait<1>();
@@ -157,24 +155,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
     __syncthreads();   // K's tile is free
     if (ti + 1 < t1) load(k_s, PITCH, K, p.k.rs, ti + 1);
     copy_commit();
-    // Scores in log2 units, hidden ones -inf, and the online softmax of each row (8 lanes a row).
+    // Scores, hidden ones -inf, and the online softmax of each row (8 lanes a row).
 #pragma unroll
     for (int r = 0; r < TM; ++r) {
       const int row = ty + 16 * r;
       const Vis v = row_v[row];
       if (p.softcap > 0.f) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[r][c] = p.softcap * tanhf(s[r][c] * p.scale / p.softcap) * kLog2e;
+        for (int c = 0; c < 4; ++c) s[r][c] = p.softcap * tanhf(s[r][c] * p.scale / p.softcap);
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[r][c] *= sc;
+        for (int c = 0; c < 4; ++c) s[r][c] *= p.scale;
       }
       if (p.M && valid(row)) {
         const float* mr = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)head_of(row) * p.m.hs +
                           (int64_t)query_of(row) * p.m.rs + k0 + tx;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (visible(v, k0 + tx + 8 * c)) s[r][c] = fmaf(mr[8 * c], kLog2e, s[r][c]);
+          if (visible(v, k0 + tx + 8 * c)) s[r][c] += mr[8 * c];
       }
       if (!within(v, k0, k0 + BN)) {
 #pragma unroll
@@ -185,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
 #pragma unroll
       for (int x = 1; x < 8; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
       if (mt > m[r]) {
-        const float f = ex2_approx(m[r] - mt);
+        const float f = S::weight(m[r], mt);
         m[r] = mt;
         l[r] *= f;
 #pragma unroll
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
       const float mu = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        s[r][c] = ex2_approx(s[r][c] - mu);
+        s[r][c] = S::weight(s[r][c], mu);
         l[r] += s[r][c];
       }
     }
@@ -238,10 +236,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
     for (int x = 1; x < 8; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
     if (!valid(row)) continue;
     const int i = query_of(row), h = head_of(row);
-    float f = 1.f;
-    if (!sp.part_o && p.sink_on) f = fold_sink<true>(m[r], l[r], sink_logit(p, h) * kLog2e);
+    float f = 1.f, M = S::natural(m[r]);
+    if (!sp.part_o && p.sink_on) f = fold_sink<false>(M, l[r], sink_logit(p, h));
     const bool hidden = l[r] == 0.f;
-    const float lse = hidden ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+    const float lse = hidden ? -INFINITY : S::lse(M, log2f(l[r]));
     const float fill = sp.part_o || p.masked_zero ? 0.f : NAN;
     const int64_t at = ((int64_t)b * p.H + h) * p.Sq + i;
     float* dst = sp.part_o ? sp.part_o + (at * sp.n_splits + split) * D
@@ -255,8 +253,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
       *reinterpret_cast<float4*>(dst + c * 32 + tx * 4) = y;
     }
     if (tx == 0) {
-      if (sp.part_o) sp.part_lse[at * sp.n_splits + split] = lse;
-      else if (p.lse) p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + i] = lse;
+      if (sp.part_o) sp.part_lse[at * sp.n_splits + split] = sp.part_l && !hidden ? M : lse;
+      if (sp.part_l) sp.part_l[at * sp.n_splits + split] = l[r];
+      if (!sp.part_o && p.lse) p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + i] = lse;
     }
   }
 }
@@ -291,7 +290,7 @@ int window_f32_try(const Problem& p, int first, const Split& sp, cudaStream_t st
   if (!tma_layout_ok_es(p.Q, p.q, p.Sq, p.H, p.B, 4) || !tma_layout_ok_es(p.K, p.k, p.Sk, p.G, p.B, 4) ||
       !tma_layout_ok_es(p.V, p.v, p.Sk, p.G, p.B, 4) || !tma_layout_ok_es(p.O, p.o, p.Sq, p.H, p.B, 4))
     return ATTN_OK;   // 16-byte loads and stores of rows
-  const float sc = p.scale * kLog2e;
+  const float sc = p.scale * S::kLog2;
   if (!(sc == sc) || isinf(sc)) return ATTN_OK;
   int rc = -1;
   switch (p.D) {

@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float part_m[2 * BM], part_l[2 * BM];
   float4* const part_a = reinterpret_cast<float4*>(k_s);
 
+  using S = Scores<XF>;   // (masks come with XF)
+  constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int my_items = (n_items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   // The two query tiles are rows [q0, q0 + 256) of one head, or with
@@ -474,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_tm = tmem + lane_off + (t ? C::kO1 : C::kO0);
     const float sc = p.scale * kLog2e;
     const bool capped = XF && p.softcap > 0.f;
-    const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * kLog2e;
-    const float c_eff = XF ? 1.f : sc;
+    const float kinv = capped ? p.scale / p.softcap : 0.f;
+    const float c_eff = XF ? 1.f : sc;   // of a value in x, to the units of m_ref
     uint32_t x[BN];
     int j = 0;   // key tiles so far
     bool ok = true;
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int pass = 0; pass < 2; ++pass) {
             if constexpr (XF) {
-              // Scores in log2 units, one 32-column chunk at a time.
+              // Scores, one 32-column chunk at a time.
 #pragma unroll
               for (int c = 0; c < N / 32; ++c) {
                 const uint32_t seen = seen_bits(*rv, k0 + c * 32);
@@ -526,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   float v = -INFINITY;
                   if ((seen >> (e % 32)) & 1u) {
                     const float s = __uint_as_float(x[e]);
-                    v = capped ? cap2 * tanh_exp2(s * kinv) : s * sc;
-                    if (mrow) v = fmaf(mrow[k0 + e], kLog2e, v);
+                    v = capped ? p.softcap * tanh_exp2(s * kinv) : s * p.scale;
+                    if (mrow) v += mrow[k0 + e];
                   }
                   x[e] = __float_as_uint(v);
                   if ((e & 7) == 7) asm volatile("" ::: "memory");  // at most 8 mask loads in flight
@@ -556,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx1 = max3(mx1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
               }
               const float mt = fmaxf(mx0, mx1) * c_eff;
-              const bool raise = mt > m_ref + kSlack;     // also true for the first tile with a visible key
-              if (raise) corr = ex2(m_ref - mt);          // 0 when m_ref = -inf
+              const bool raise = mt > m_ref + kRise;      // also true for the first tile with a visible key
+              if (raise) corr = S::weight(m_ref, mt);     // 0 when m_ref = -inf
               rescale = raise && m_ref > -INFINITY;       // O holds earlier tiles' sums
               if (raise) {
                 l *= corr;
@@ -572,6 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               float a0, a1, b0, b1;
               fma2(a0, a1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]), c2, n2);
               fma2(b0, b1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), c2, n2);
+              if constexpr (XF) {   // natural differences
+                fma2(a0, a1, a0, a1, f2u(kLog2e, kLog2e), 0);
+                fma2(b0, b1, b0, b1, f2u(kLog2e, kLog2e), 0);
+              }
               a0 = ex2(a0);
               a1 = ex2(a1);
               b0 = ex2(b0);
@@ -624,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (clustered) break;   // (its only item)
       const bool split = sp.n_splits > 1;
       // The sink logit joins the denominator (and rescales the accumulated O); with parts the merge adds it once.
-      const float o_mul = p.sink_on && !split ? fold_sink<true>(m_ref, l, sink_logit(p, h) * kLog2e) : 1.f;
+      float M = S::natural(m_ref);
+      const float o_mul = p.sink_on && !split ? fold_sink<false>(M, l, sink_logit(p, h)) : 1.f;
       const bool hidden_row = (l == 0.f);         // no visible key; a NaN l stays a NaN row
       const float inv = o_mul / l;
       const float fill = p.masked_zero ? 0.f : NAN;
@@ -670,9 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (valid) {
-        const float lse = hidden_row ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
-        if (split) sp.part_lse[prow * sp.n_splits + items[buf].part] = lse;
-        else if (p.lse) p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + qrow] = lse;
+        const float lse = hidden_row ? -INFINITY : S::lse(M, __log2f(l));
+        if (split) {
+          const int64_t at = prow * sp.n_splits + items[buf].part;
+          sp.part_lse[at] = XF && sp.part_l && !hidden_row ? M : lse;
+          if (XF && sp.part_l) sp.part_l[at] = l;
+        } else if (p.lse) {
+          p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + qrow] = lse;
+        }
       }
       fence_before();   // O's loads come before the next item's P, and so before its P V
       mbar_arrive(&sb.item_empty[buf]);
@@ -727,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (q0 + q >= parts) continue;
-            f[q] = ex2(f[q] - mu);
+            f[q] = S::weight(f[q], mu);
             L = fmaf(f[q], lq[q], L);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -738,7 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float o_mul = p.sink_on ? fold_sink<true>(M, L, sink_logit(p, hh) * kLog2e) : 1.f;
+        M = S::natural(M);
+        const float o_mul = p.sink_on ? fold_sink<false>(M, L, sink_logit(p, hh)) : 1.f;
         const bool hidden = L == 0.f;
         const float inv = o_mul / L, fill = p.masked_zero ? 0.f : NAN;
         uint32_t w[8];
@@ -752,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
         if (col == 0 && p.lse)
-          p.lse[(int64_t)it.b * p.lse_bs + (int64_t)hh * p.lse_hs + i] = hidden ? -INFINITY : (M + __log2f(L)) * kLn2;
+          p.lse[(int64_t)it.b * p.lse_bs + (int64_t)hh * p.lse_hs + i] = hidden ? -INFINITY : S::lse(M, __log2f(L));
       }
       cluster_sync();   // no CTA leaves while its part is being read
     }
