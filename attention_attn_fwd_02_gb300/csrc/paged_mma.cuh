@@ -236,7 +236,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
   if constexpr (MODE != kCluster) fill_entries<T>(w, cta);   // (while the first copies are under way)
   const bool capped = XF && p.softcap > 0.f;
   const float cap_inv = capped ? 1.f / p.softcap : 0.f;
-  constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
+  // A row's reference is its maximum, less a lead where P is f16: there p = 2^(x - m_ref) is 2^11 at the maximum
+  // the reference was taken from and at most 2^15 when it moves, and what f16 cannot hold (2^-25) is 2^-36 of the
+  // row's largest probability: all keys together lose n 2^-36, under a quarter of f16's half step up to 2^23 rows.
+  constexpr float kLead = (MBF ? 0.f : 11.f) * (XF ? kLn2 : 1.f);   // in the units of the scores
+  constexpr float kRise = (MBF ? kSlack : 15.f) * (XF ? kLn2 : 1.f);
   // ldmatrix source rows and unit offsets of this lane (K: keys x channels; V transposed).
   const int lk_row = (lane & 7) + ((lane >> 3) & 1) * 8, lk_u = lane >> 4;
   const int lv_row = KV8 ? lk_row : (lane & 7) + (lane >> 4) * 8, lv_u = KV8 ? lane >> 4 : (lane >> 3) & 1;
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           for (int e = 0; e < 4; ++e)
             if (!((vis >> (16 * mb + gid + 8 * (e >> 1))) & 1u)) sc[mb][j][e] = -INFINITY;
     }
-    // The reference maximum moves only when a score rises above it by more than the slack.
+    // The reference moves only when a score rises above it by more than kRise.
     float top[NT][2];
     bool rise = false;
 #pragma unroll
@@ -338,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
           if (mx > m_ref[j][q] + kRise) {
+            mx -= kLead;
             const float f = S::weight(m_ref[j][q], mx);
             l[j][q] *= f;
 #pragma unroll

@@ -156,6 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   using S = Scores<XF>;   // (masks come with XF)
   constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
+  // A row's reference is a maximum, less a lead where P is f16: p is 2^7 at that maximum (a tile of 128 such keys
+  // sums to 2^14 and causes no scan), and what f16 cannot hold (2^-25) is 2^-32 of the row's largest probability,
+  // for all keys together n 2^-32: under a quarter of f16's half step up to 2^19 keys of window.
+  constexpr float kLead = (BF16 ? 0.f : 7.f) * (XF ? kLn2 : 1.f);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int my_items = (n_items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   // The two query tiles are rows [q0, q0 + 256) of one head, or with
@@ -557,8 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx0 = max3(mx0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                 mx1 = max3(mx1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
               }
-              const float mt = fmaxf(mx0, mx1) * c_eff;
+              float mt = fmaxf(mx0, mx1) * c_eff;
               const bool raise = mt > m_ref + kRise;      // also true for the first tile with a visible key
+              mt -= kLead;
               if (raise) corr = S::weight(m_ref, mt);     // 0 when m_ref = -inf
               rescale = raise && m_ref > -INFINITY;       // O holds earlier tiles' sums
               if (raise) {

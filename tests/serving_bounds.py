@@ -29,7 +29,7 @@ def p_error(dt, how):
     if dt == torch.float32:
         return 0.0, 0.0
     if how == "f16":
-        return 2.0 ** -11, 2.0 ** -24
+        return 2.0 ** -11, 2.0 ** -35
     if how == "single":
         return HALF[dt], 0.0 if dt == torch.bfloat16 else 2.0 ** -32
     return (2.0 ** -15, 0.0) if dt == torch.bfloat16 else (2.0 ** -20, 2.0 ** -34)
