@@ -19,9 +19,11 @@
 // The contractions use mma.sync m16n8k16 with the keys on the 16 rows and the
 // query heads on the 8 columns (few heads share a kv head): S^T = K Q^T with K
 // from ldmatrix, O^T += V^T P^T with V from ldmatrix.trans and P^T from the
-// S^T accumulator through movmatrix.  P enters as the sum of two rounded
-// halves (p rounded, and the rest rounded), so that the result carries the
-// output's rounding only; the extra MMAs are free under the HBM time.
+// S^T accumulator through movmatrix.  P enters as the sum of two halves (p
+// cut, and the rest rounded), so that the result carries the output's rounding
+// only; the extra MMAs are free under the HBM time.  Over float caches both
+// halves of a p > 0 are above zero, so that an infinite V gives an infinite
+// result, as in the formula, and not the NaN of infinity times zero or less.
 //
 // int8 caches enter the MMAs as exact f16 integers (0x6400 | (x ^ 0x80) is
 // 1152 + x, minus 1152).  The scales leave the loop: Q is scaled by k_scale,
@@ -77,6 +79,28 @@ __device__ __forceinline__ uint32_t pack_split(float a, float b, uint32_t& rest)
     const __half2 r = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
     rest = *reinterpret_cast<const uint32_t*>(&r);
     return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+// Two probabilities (>= 0) as sums of two values of the MMA type, both above zero where the probability is.  The
+// first is cut a little below its value: p is off by 2^-15.6 of itself in bf16 (2^-9 of a rest that is at most 2^-7
+// + 2^-9 of p), in f16 by 2^-21, or by 2^-23 in all where it is small and the halves are lifted to f16's least value.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_above_zero(float a, float b, uint32_t& rest) {
+  if constexpr (BF16) {
+    const uint32_t ah = __float_as_uint(a * (1.f - 0x1p-9f)) & 0xffff0000u;
+    const uint32_t bh = __float_as_uint(b * (1.f - 0x1p-9f)) & 0xffff0000u;
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a - __uint_as_float(ah), b - __uint_as_float(bh));
+    rest = *reinterpret_cast<const uint32_t*>(&r);
+    return __byte_perm(ah, bh, 0x7632);
+  } else {
+    uint32_t h;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b * (1.f - 0x1p-10f)), "f"(a * (1.f - 0x1p-10f)));
+    const __half2 hh = *reinterpret_cast<const __half2*>(&h);
+    const __half2 r = __floats2half2_rn(a - __low2float(hh), b - __high2float(hh));
+    const uint32_t least = (a > 0.f ? 1u : 0u) | (b > 0.f ? 0x10000u : 0u);
+    asm("max.u16x2 %0, %1, %2;" : "=r"(rest) : "r"(*reinterpret_cast<const uint32_t*>(&r)), "r"(least));
+    asm("max.u16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(least));
+    return h;
   }
 }
 // Bytes 0 and 2 (or 1 and 3) of a word of int8 values as an exact f16 pair.
@@ -371,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t rest;
-          ph[mb][j][q] = movtrans(pack_split<MBF>(e[2 * q], e[2 * q + 1], rest));
+          ph[mb][j][q] = movtrans(KV8 ? pack_split<MBF>(e[2 * q], e[2 * q + 1], rest)
+                                      : pack_above_zero<MBF>(e[2 * q], e[2 * q + 1], rest));
           if constexpr (SPLIT) pl[mb][j][q] = movtrans(rest);
         }
       }
