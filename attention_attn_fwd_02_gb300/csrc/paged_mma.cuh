@@ -28,7 +28,10 @@
 // int8 caches enter the MMAs as exact f16 integers (0x6400 | (x ^ 0x80) is
 // 1152 + x, minus 1152).  The scales leave the loop: Q is scaled by k_scale,
 // and by a power of two for each head that puts its largest element next to
-// 2^11, and enters as two f16 halves; v_scale multiplies the finished row.
+// 2^11, and enters as two f16 halves (22 bits: a score of 200 keeps an error of
+// 2^-14, where one f16 value would leave 0.05); v_scale multiplies the finished
+// row.  With Q and P as one f16 value each the batch of 64 takes 110 us, with P
+// as one 114, with both in halves 119 (and the result carries the output's rounding only).
 #pragma once
 
 #include <type_traits>
@@ -133,8 +136,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
   using C = Cfg<BF16, KV8, D, NT, MODE>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr bool MBF = BF16 && !KV8;   // MMA type bf16
-  // P and (int8) Q in two halves, except where one f16 value is already eight times finer than a bf16 result.
-  constexpr bool SPLIT = !(BF16 && KV8);
   using S = Scores<XF>;   // (masks come with XF)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int st_key[kWarps][C::kStages];         // first key of a warp's stage
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
   }
 
   // Q as the B operand (n = head, k = channels).
-  uint32_t qh[NT][D / 16][2], ql[KV8 && SPLIT ? NT : 1][D / 16][2];
+  uint32_t qh[NT][D / 16][2], ql[KV8 ? NT : 1][D / 16][2];
   float cs[NT][2];   // what a raw product is multiplied by, for the accumulator's two head columns
   auto load_q = [&]() {
     const int g = out.u / w.n_hc, h0 = g * p.qpg + (out.u % w.n_hc) * C::kHeads;
@@ -229,10 +230,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           uint32_t rest[2];
           qh[j][c][0] = pack_split<false>(v[c][0] * up, v[c][2] * up, rest[0]);
           qh[j][c][1] = pack_split<false>(v[c][1] * up, v[c][3] * up, rest[1]);
-          if constexpr (SPLIT) {
-            ql[j][c][0] = rest[0];
-            ql[j][c][1] = rest[1];
-          }
+          ql[j][c][0] = rest[0];
+          ql[j][c][1] = rest[1];
         }
         const float down = p.scale * S::kUnit * ldexpf(1.f, -ex);
         cs[j][0] = __shfl_sync(kAll, down, 8 * tig);       // heads 2 tig and 2 tig + 1 of the column tile
@@ -312,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
               mma<false>(q ? sd[j] : sc[mb][j], a, qh[j][c + q][0], qh[j][c + q][1]);
-              if constexpr (SPLIT) mma<false>(q ? sd[j] : sc[mb][j], a, ql[j][c + q][0], ql[j][c + q][1]);
+              mma<false>(q ? sd[j] : sc[mb][j], a, ql[j][c + q][0], ql[j][c + q][1]);
             }
           }
         }
@@ -397,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           uint32_t rest;
           ph[mb][j][q] = movtrans(KV8 ? pack_split<MBF>(e[2 * q], e[2 * q + 1], rest)
                                       : pack_above_zero<MBF>(e[2 * q], e[2 * q + 1], rest));
-          if constexpr (SPLIT) pl[mb][j][q] = movtrans(rest);
+          pl[mb][j][q] = movtrans(rest);
         }
       }
     }
@@ -411,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             mma<MBF>(o[c][j], a, ph[mb][j][0], ph[mb][j][1]);
-            if constexpr (SPLIT) mma<MBF>(o[c][j], a, pl[mb][j][0], pl[mb][j][1]);
+            mma<MBF>(o[c][j], a, pl[mb][j][0], pl[mb][j][1]);
           }
         }
       } else {
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
               mma<false>(o[c + q][j], a, ph[mb][j][0], ph[mb][j][1]);
-              if constexpr (SPLIT) mma<false>(o[c + q][j], a, pl[mb][j][0], pl[mb][j][1]);
+              mma<false>(o[c + q][j], a, pl[mb][j][0], pl[mb][j][1]);
             }
           }
         }

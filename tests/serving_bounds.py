@@ -10,7 +10,7 @@ and a base-2 exponential of 2^-22.  (A mask below -2^100 absorbs its score on
 both sides.)  The float32 sums over keys run through about n / 16 steps, each
 of which a tensor-core product may truncate: (16 + n / 8) u sum w |v|.  A
 probability that enters its product rounded adds p_rel of itself and p_abs of the
-row's largest one: `single` is one value of the element type (`f16` one of f16), `halves` two (16
+row's largest one: `single` is one value of the element type, `halves` two (16
 bits of bf16; of f16 21 bits and what lies under its smallest value, see the
 kernels), float32 none.  Last, the output's own rounding.
 """
@@ -28,8 +28,6 @@ def p_error(dt, how):
     """(relative, relative to the row's largest probability) error of a probability."""
     if dt == torch.float32:
         return 0.0, 0.0
-    if how == "f16":
-        return 2.0 ** -11, 2.0 ** -35
     if how == "single":
         return HALF[dt], 0.0 if dt == torch.bfloat16 else 2.0 ** -32
     return (2.0 ** -15, 0.0) if dt == torch.bfloat16 else (2.0 ** -20, 2.0 ** -34)

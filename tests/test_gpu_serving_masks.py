@@ -104,9 +104,8 @@ def test_paged_masks(dt, D, H, G, B, rows, opt):
     sink = randn(g, H) if opt.get("sink") else None
     vis = (torch.arange(rows, device="cuda")[None] < n[:, None])[:, None]
     o, lse, tol, tol_l = sb.attention(q.transpose(1, 2), sb.rows_of(k, table, ps, rows), sb.rows_of(v, table, ps, rows),
-                                      vis, p="f16" if i8 and dt == "bf16" else "halves", mask=mask, sink=sink,
-                                      softcap=opt.get("softcap", 0.0), kv_scales=sc,
-                                      extra_score=2.0 ** -12 if i8 and dt == "bf16" else 2.0 ** -22 if i8 else 0.0)
+                                      vis, mask=mask, sink=sink, softcap=opt.get("softcap", 0.0), kv_scales=sc,
+                                      extra_score=2.0 ** -22 if i8 else 0.0)
     kw = dict(k_scale=sc[0], v_scale=sc[1]) if i8 else {}
     got, got_l = attn.decode_paged(q, k, v, table, n, mask=mask, head_sink=sink, softcap=opt.get("softcap", 0.0),
                                    max_rows=rows, masked_rows="zero", return_lse=True, **kw)

@@ -63,9 +63,7 @@ def test_paged_spread_weight(dt, i8, below, at):
     top = float(kw["k_scale"].double() * 127) if i8 else float(score.double())
     others, e = torch.tensor(n - 1.0, dtype=torch.float64, device="cuda"), math.exp(-top)
     o, l = expected(others, e)
-    # the score carries a float32 product, and int8's scaled query its own rounding
-    ds = top * (2.0 ** -11 if i8 and dt == "bf16" else 2.0 ** -20)
-    tol, tol_l = bounds(DT[dt], "f16" if i8 and dt == "bf16" else "halves", n, o, ds)
+    tol, tol_l = bounds(DT[dt], "halves", n, o, top * 2.0 ** -20)
     assert float(((got[:, 0, 0, :2].double() - o).abs() / tol).max()) <= 1
     assert float((lse[:, 0, 0].double() - (l + top)).abs().max()) <= tol_l
 
