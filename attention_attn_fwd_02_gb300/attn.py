@@ -4,7 +4,9 @@ Argument marshalling only: every step of the computation runs in the CUDA
 library.  The low-level functions keep the C names (attn_fwd, attn_decode,
 attn_combine, ...) and take integer device addresses; ``fwd``, ``decode`` and
 ``combine`` build the problem struct from torch tensors, allocate the outputs
-and the workspace with torch, and call them on torch's current stream.
+and the workspace with torch, and call them on torch's current stream, or on
+the cudaStream_t given as ``stream``: what a call allocates then belongs to that
+stream, as under ``torch.cuda.stream``.
 There is no CPU fallback: if the library is missing, loading it raises.
 """
 from __future__ import annotations
@@ -304,6 +306,18 @@ def _check(code, where):
         raise AttnError(code, where)
 
 
+def _empty(stream, device, shape, dtype):
+    """torch.empty for a call that launches on `stream` (None: torch's current one).  The allocator hands a freed
+    block on in the order of the stream it was allocated under, so that has to be the stream of the kernels."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    # (0 and 1 both name the legacy default stream)
+    on = torch.cuda.default_stream(device) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(on):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check_same(q, *, ints=(), floats=(), **same):
     """Raise unless the tensors are on q's device, `same` have q's dtype, ints are int32 and floats float32."""
     torch = _torch()
@@ -348,7 +362,7 @@ def fwd(q, k, v, *, layout="bshd", causal=False, causal_offset=None, scale=0.0, 
     B, Sq, H, D = q.shape[0], q.shape[sd], q.shape[hd], q.shape[3]
     G, Sk = k.shape[hd], k.shape[sd]
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty(stream, q.device, q.shape, q.dtype)
     d = dict(batch=B, heads=H, kv_heads=G, q_len=Sq, k_len=Sk, head_dim=D, dtype=_dtype_name(q), scale=scale,
              causal=causal, causal_offset=causal_offset, masked_rows=masked_rows,
              q_layout=_layout4(q, hd), k_layout=_layout4(k, hd), v_layout=_layout4(v, hd),
@@ -363,7 +377,7 @@ def fwd(q, k, v, *, layout="bshd", causal=False, causal_offset=None, scale=0.0, 
     if seg is not None:
         d["seg_batch_stride"] = 0 if seg.dim() == 1 else seg.stride(0)
     if return_lse and lse is None:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, q.device, (B, H, Sq), torch.float32)
     if lse is not None:
         d["lse_layout"] = (lse.stride(0), lse.stride(1))
     p = make_problem(d)
@@ -371,13 +385,13 @@ def fwd(q, k, v, *, layout="bshd", causal=False, causal_offset=None, scale=0.0, 
         _check_same(q, k=k, v=v, out=out)
         with torch.cuda.device(q.device):
             ws_bytes = attn_fwd_window_workspace_size(p, first_keys)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
+            ws = _empty(stream, q.device, ws_bytes, torch.uint8) if ws_bytes else None
             st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
             _check(attn_fwd_window(p, first_keys, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(mask), _ptr(seg),
                                    _ptr(k_lens), _ptr(lse), _ptr(ws), ws_bytes, st), "attn_fwd_window")
         return (out, lse) if return_lse else out
     ws_bytes = attn_fwd_workspace_size(p)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
+    ws = _empty(stream, q.device, ws_bytes, torch.uint8) if ws_bytes else None
     st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
     _check(attn_fwd(p, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(mask), _ptr(seg), _ptr(k_lens), _ptr(lse),
                     _ptr(ws), ws_bytes, st), "attn_fwd")
@@ -396,7 +410,7 @@ def decode(q, k_cache, v_cache, k_lens=None, *, scale=0.0, mask=None, masked_row
     B, Sq, H, D = q.shape
     G, cap = k_cache.shape[1], k_cache.shape[2]
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty(stream, q.device, q.shape, q.dtype)
     d = dict(batch=B, heads=H, kv_heads=G, q_len=Sq, k_len=cap, head_dim=D, dtype=_dtype_name(q), scale=scale,
              causal=window_left is not None, causal_align="klens", window_left=window_left,
              k_lens_kind=k_lens_kind, softcap=softcap, smooth_softmax=smooth_softmax,
@@ -409,13 +423,13 @@ def decode(q, k_cache, v_cache, k_lens=None, *, scale=0.0, mask=None, masked_row
         d["mask_layout"] = (0, mask.stride(0) if mask.shape[0] > 1 else 0,
                             mask.stride(1) if mask.shape[1] > 1 else 0, mask.stride(2) if mask.shape[2] > 1 else 0)
     if return_lse and lse is None:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, q.device, (B, H, Sq), torch.float32)
     if lse is not None:
         d["lse_layout"] = (lse.stride(0), lse.stride(1))
     p = make_problem(d)
     ws_bytes = attn_decode_workspace_size(p)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, q.device, ws_bytes, torch.uint8)
     st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
     _check(attn_decode(p, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(mask), None, _ptr(k_lens),
                        _ptr(lse), _ptr(workspace), workspace.numel(), st), "attn_decode")
@@ -444,7 +458,7 @@ def decode_paged(q, k_pool, v_pool, table, k_lens=None, *, page_layout="hnd", sc
     if rows > table.shape[1] * ps:
         raise ValueError("max_rows: the table holds fewer rows")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty(stream, q.device, q.shape, q.dtype)
     i8 = k_pool.dtype == torch.int8
     kv = {} if i8 else dict(k_pool=k_pool, v_pool=v_pool)
     _check_same(q, out=out, ints=(table, k_lens), floats=(mask, lse, head_sink, k_scale, v_scale), **kv)
@@ -464,14 +478,14 @@ def decode_paged(q, k_pool, v_pool, table, k_lens=None, *, page_layout="hnd", sc
         d["mask_layout"] = (0, mask.stride(0) if mask.shape[0] > 1 else 0,
                             mask.stride(1) if mask.shape[1] > 1 else 0, 0)
     if return_lse and lse is None:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, q.device, (B, H, Sq), torch.float32)
     if lse is not None:
         d["lse_layout"] = (lse.stride(0), lse.stride(1))
     p, pages = make_problem(d), make_pages(ps, k_pool.shape[0], _ptr(table), table.stride(0))
     with torch.cuda.device(q.device):
         ws_bytes = attn_decode_paged_workspace_size(p, pages, first_keys)
         if workspace is None:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _empty(stream, q.device, ws_bytes, torch.uint8)
         st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
         _check(attn_decode_paged(p, pages, first_keys, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(mask),
                                  _ptr(k_lens), _ptr(lse), _ptr(workspace), workspace.numel(), st),
@@ -495,7 +509,7 @@ def qkv_prep(q, k, v, k_cache, v_cache, table=None, *, page_layout="hnd", q_weig
     B, S, H, D = q.shape
     G = k.shape[2]
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty(stream, q.device, q.shape, q.dtype)
     i8 = k_cache.dtype == torch.int8
     kv = {} if i8 else dict(k_cache=k_cache, v_cache=v_cache)
     _check_same(q, k=k, v=v, out=out, q_weight=q_weight, k_weight=k_weight, ints=(positions, rows, table),
@@ -545,8 +559,8 @@ def combine(part_o, part_lse, *, out_dtype=None, masked_rows="nan", return_lse=F
     torch = _torch()
     rows, n, D = part_o.shape
     out_dtype = out_dtype or torch.float32
-    out = torch.empty((rows, D), dtype=out_dtype, device=part_o.device)
-    lse = torch.empty((rows,), dtype=torch.float32, device=part_o.device) if return_lse else None
+    out = _empty(stream, part_o.device, (rows, D), out_dtype)
+    lse = _empty(stream, part_o.device, (rows,), torch.float32) if return_lse else None
     st = torch.cuda.current_stream(part_o.device).cuda_stream if stream is None else stream
     code = {torch.float32: ATTN_F32, torch.float16: ATTN_F16, torch.bfloat16: ATTN_BF16}[out_dtype]
     _check(attn_combine(n, rows, D, _ptr(part_o), _ptr(part_lse), code, _ptr(out), D, _ptr(lse),
