@@ -332,6 +332,34 @@ def _check_same(q, *, ints=(), floats=(), **same):
                 raise ValueError(f"expected {dt} on {q.device}, got {t.dtype} on {t.device}")
 
 
+def _check_extents(B, H, Sq, keys, *, mask, lse, head_sink, k_lens):
+    """Raise unless what the kernels index by (entry, head, row, key) covers the problem."""
+    if mask is not None:
+        if mask.dim() != 4 or (mask.shape[3] > 1 and mask.stride(3) != 1):
+            raise ValueError("mask must be float32, 4-D, keys contiguous")
+        if any(m not in (1, n) for m, n in zip(mask.shape, (B, H, Sq))) or mask.shape[3] < keys:
+            raise ValueError(f"mask: expected [{B}|1, {H}|1, {Sq}|1, {keys} keys or more], got {tuple(mask.shape)}")
+    if lse is not None and (lse.shape != (B, H, Sq) or (Sq > 1 and lse.stride(2) != 1)):
+        raise ValueError(f"lse: expected [{B}, {H}, {Sq}], contiguous rows, got {tuple(lse.shape)}")
+    if head_sink is not None and (head_sink.shape != (H,) or not head_sink.is_contiguous()):
+        raise ValueError(f"head_sink: expected contiguous [{H}], got {tuple(head_sink.shape)}")
+    if k_lens is not None and (k_lens.shape != (B,) or not k_lens.is_contiguous()):
+        raise ValueError("k_lens: expected contiguous int32 [batch]")
+
+
+def _check_scales(i8, G, D, k_scale, v_scale):
+    """Raise unless int8 caches have two scales, or two for every kv head and channel."""
+    if not i8:
+        return
+    if k_scale is None or v_scale is None:
+        raise ValueError("int8 caches: expected k_scale and v_scale")
+    if k_scale.numel() != v_scale.numel() or k_scale.numel() not in (1, G * D):
+        raise ValueError(f"k_scale, v_scale: expected both of 1 or both of {G * D} elements, got {k_scale.numel()} and "
+                         f"{v_scale.numel()}")
+    if not (k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("k_scale, v_scale: expected contiguous tensors")
+
+
 def _page_dims(pool, table, page_layout):
     """(kv heads, page size, layout) of a pool [pages, G, page_size, D] ('hnd') or [pages, page_size, G, D] ('nhd')."""
     if page_layout not in ("hnd", "nhd") or pool.dim() != 4:
@@ -382,7 +410,12 @@ def fwd(q, k, v, *, layout="bshd", causal=False, causal_offset=None, scale=0.0, 
         d["lse_layout"] = (lse.stride(0), lse.stride(1))
     p = make_problem(d)
     if first_keys:
-        _check_same(q, k=k, v=v, out=out)
+        _check_extents(B, H, Sq, Sk, mask=mask, lse=lse, head_sink=head_sink, k_lens=k_lens)
+        if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D or out.shape != q.shape:
+            raise ValueError("q, k, v and out disagree")
+        if seg is not None and (seg.shape not in ((Sq,), (B, Sq)) or (Sq > 1 and seg.stride(-1) != 1)):
+            raise ValueError("seg: expected [q_len] or [batch, q_len], contiguous rows")
+        _check_same(q, k=k, v=v, out=out, ints=(seg, k_lens), floats=(mask, lse, head_sink))
         with torch.cuda.device(q.device):
             ws_bytes = attn_fwd_window_workspace_size(p, first_keys)
             ws = _empty(stream, q.device, ws_bytes, torch.uint8) if ws_bytes else None
@@ -443,7 +476,8 @@ def decode_paged(q, k_pool, v_pool, table, k_lens=None, *, page_layout="hnd", sc
     """Single-query decode over a paged cache: q [B, 1, H, D]; pools [pages, G, page_size, D]
     ('hnd') or [pages, page_size, G, D] ('nhd'); table int32 [B, pages of an entry]: entry b's
     row r is row r % page_size of page table[b, r // page_size], and a value that names no page
-    hides its rows.  max_rows: rows an entry can hold (default: what its list holds).  window_left
+    hides its rows.  max_rows: rows an entry can hold (default: what its list holds); a mask
+    [B|1, H|1, 1, max_rows or more] covers them.  window_left
     and first_keys: keep the last window_left + 1 valid keys and the first first_keys ones.
     Everything else as for decode."""
     torch = _torch()
@@ -452,14 +486,16 @@ def decode_paged(q, k_pool, v_pool, table, k_lens=None, *, page_layout="hnd", sc
     _, _, vl = _page_dims(v_pool, table, page_layout)
     if v_pool.shape != k_pool.shape or k_pool.shape[3] != D or table.shape[0] != B:
         raise ValueError("q, pools and table disagree")
-    if k_lens is not None and (k_lens.shape != (B,) or not k_lens.is_contiguous()):
-        raise ValueError("k_lens: expected contiguous int32 [batch]")
     rows = table.shape[1] * ps if max_rows is None else max_rows
     if rows > table.shape[1] * ps:
         raise ValueError("max_rows: the table holds fewer rows")
     if out is None:
         out = _empty(stream, q.device, q.shape, q.dtype)
     i8 = k_pool.dtype == torch.int8
+    _check_extents(B, H, Sq, rows, mask=mask, lse=lse, head_sink=head_sink, k_lens=k_lens)
+    _check_scales(i8, G, D, k_scale, v_scale)
+    if out.shape != q.shape:
+        raise ValueError("out: expected the queries' shape")
     kv = {} if i8 else dict(k_pool=k_pool, v_pool=v_pool)
     _check_same(q, out=out, ints=(table, k_lens), floats=(mask, lse, head_sink, k_scale, v_scale), **kv)
     if i8 and (v_pool.dtype != torch.int8 or k_pool.device != q.device or v_pool.device != q.device):
@@ -473,8 +509,6 @@ def decode_paged(q, k_pool, v_pool, table, k_lens=None, *, page_layout="hnd", sc
              k_scale_ptr=_ptr(k_scale), v_scale_ptr=_ptr(v_scale), k_layout=kl, v_layout=vl,
              o_layout=_layout4(out, 2))
     if mask is not None:
-        if mask.dim() != 4 or mask.stride(3) != 1:
-            raise ValueError("mask must be float32, 4-D, keys contiguous")
         d["mask_layout"] = (0, mask.stride(0) if mask.shape[0] > 1 else 0,
                             mask.stride(1) if mask.shape[1] > 1 else 0, 0)
     if return_lse and lse is None:
@@ -486,6 +520,8 @@ def decode_paged(q, k_pool, v_pool, table, k_lens=None, *, page_layout="hnd", sc
         ws_bytes = attn_decode_paged_workspace_size(p, pages, first_keys)
         if workspace is None:
             workspace = _empty(stream, q.device, ws_bytes, torch.uint8)
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on {q.device}")
         st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
         _check(attn_decode_paged(p, pages, first_keys, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(mask),
                                  _ptr(k_lens), _ptr(lse), _ptr(workspace), workspace.numel(), st),
@@ -512,6 +548,7 @@ def qkv_prep(q, k, v, k_cache, v_cache, table=None, *, page_layout="hnd", q_weig
         out = _empty(stream, q.device, q.shape, q.dtype)
     i8 = k_cache.dtype == torch.int8
     kv = {} if i8 else dict(k_cache=k_cache, v_cache=v_cache)
+    _check_scales(i8, G, D, k_scale, v_scale)
     _check_same(q, k=k, v=v, out=out, q_weight=q_weight, k_weight=k_weight, ints=(positions, rows, table),
                 floats=(cos, sin, k_scale, v_scale), **kv)
     if i8 and (v_cache.dtype != torch.int8 or k_cache.device != q.device or v_cache.device != q.device):
