@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "attn.h"
+#include "smem_limit.h"
 
 namespace attn {
 
@@ -168,32 +169,6 @@ __device__ __forceinline__ void append_row(const Problem& p, int b, int g, int64
 __device__ __forceinline__ int64_t append_target(const Problem& p, int b) {
   const int64_t L = p.klens ? clamp64((int64_t)p.klens[b] + p.klens_plus, 0, p.Sk) : p.Sk;
   return L - 1;
-}
-
-// Raises a kernel's dynamic shared-memory limit to `bytes` on the current
-// device once; the setting lasts for the process, so later launches only look
-// it up (the attribute call costs microseconds, which small problems feel).
-inline cudaError_t ensure_smem(const void* kern, int bytes) {
-  struct Entry {
-    const void* k;
-    int dev, bytes;
-  };
-  static std::mutex mu;
-  static Entry tab[256];
-  static int n = 0;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-      if (tab[i].k == kern && tab[i].dev == dev && tab[i].bytes >= bytes) return cudaSuccess;
-  }
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) {
-    std::lock_guard<std::mutex> lock(mu);
-    if (n < 256) tab[n++] = {kern, dev, bytes};
-  }
-  return e;
 }
 
 // Device addresses of a __device__ symbol, per (device, context).  A host
