@@ -137,6 +137,25 @@ __device__ __forceinline__ float fold_sink(float& m, float& l, float s) {
   return f;
 }
 
+// How a pass holds scores and their reference maxima.  An additive mask may
+// hold any float32 down to the lowest, whose product with log2(e) has none: a
+// pass that takes masks keeps natural units (NAT) and multiplies the difference
+// to the reference; the others keep log2 units, where that is one FMA with the
+// scale.
+template <bool NAT>
+struct Scores {
+  static constexpr float kLog2 = 1.4426950408889634f, kLn = 0.69314718055994531f;
+  static constexpr float kUnit = NAT ? 1.f : kLog2;   // of a natural score
+  // exp(x - ref) of scores or references; ref is not -inf.
+  static __device__ __forceinline__ float weight(float x, float ref) {
+    return ex2_approx(NAT ? (x - ref) * kLog2 : x - ref);
+  }
+  // A finished row's reference in natural units: there the sink's logit joins it (fold_sink<false>).
+  static __device__ __forceinline__ float natural(float M) { return NAT ? M : M * kLn; }
+  // LSE from that and log2 of the sum relative to it.
+  static __device__ __forceinline__ float lse(float M, float log2_l) { return fmaf(log2_l, kLn, M); }
+};
+
 // The cache update before a decode step with append: the new key and value
 // rows of (batch b, kv head g) go to cache row `row` (the entry's last valid
 // row).  Float caches take a copy; an int8 cache takes x / scale rounded to

@@ -266,9 +266,10 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const __grid_const
       qa[ds][3] = ld2(gid + 8, ds * 16 + 8 + tig * 2);
     }
   }
-  const float c = p.scale * kLog2e;
+  using S = Scores<XF>;   // (masks come with XF)
+  const float c = p.scale * S::kUnit;
   const bool capped = XF && p.softcap > 0.f;
-  const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * kLog2e;
+  const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * S::kUnit;
   const float* mrow = XF && p.M ? p.M + p.m.off + (int64_t)b * p.m.bs : nullptr;
 
   float o[16][4];
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const __grid_const
       mma16816<BF16>(sc[0], qa[ds], kb[0], kb[1]);
       mma16816<BF16>(sc[1], qa[ds], kb[2], kb[3]);
     }
-    // Scores in log2 units; keys past the end are hidden.
+    // Scores (in the units of S); keys past the end are hidden.
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const __grid_const
         const int64_t key = k0 + nt * 8 + tig * 2 + (e & 1);
         const int hh = gid + (e >> 1) * 8;
         float x = capped ? cap2 * tanh_exp2(sc[nt][e] * kinv) : sc[nt][e] * c;
-        if (mrow && key < end && hh < nh) x = fmaf(mrow[(int64_t)(h0 + hh) * p.m.hs + key], kLog2e, x);
+        if (mrow && key < end && hh < nh) x += mrow[(int64_t)(h0 + hh) * p.m.hs + key];
         sc[nt][e] = key < end ? x : -INFINITY;
       }
     // Per head row: maximum over the 16 keys (a quad of lanes shares a row).
@@ -330,8 +331,8 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const __grid_const
       float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (mx > m_ref[r] + kSlack) {
-        const float corr = ex2(m_ref[r] - mx);
+      if (mx > m_ref[r] + (XF ? kSlack * kLn2 : kSlack)) {
+        const float corr = S::weight(m_ref[r], mx);
         l[r] *= corr;
 #pragma unroll
         for (int nt = 0; nt < 16; ++nt) {
@@ -348,10 +349,10 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const __grid_const
       float pv[2][4];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        pv[nt][0] = ex2(sc[nt][0] - mu0);
-        pv[nt][1] = ex2(sc[nt][1] - mu0);
-        pv[nt][2] = ex2(sc[nt][2] - mu1);
-        pv[nt][3] = ex2(sc[nt][3] - mu1);
+        pv[nt][0] = S::weight(sc[nt][0], mu0);
+        pv[nt][1] = S::weight(sc[nt][1], mu0);
+        pv[nt][2] = S::weight(sc[nt][2], mu1);
+        pv[nt][3] = S::weight(sc[nt][3], mu1);
       }
       l[0] += (pv[0][0] + pv[0][1]) + (pv[1][0] + pv[1][1]);
       l[1] += (pv[0][2] + pv[0][3]) + (pv[1][2] + pv[1][3]);
@@ -420,12 +421,12 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const __grid_const
       float L = 0.f, a = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(red_m[w][hh] - M);
+        const float f = S::weight(red_m[w][hh], M);
         L = fmaf(f, red_l[w][hh], L);
         a = fmaf(f, red_acc[(w * kMHeads + hh) * kD + d], a);
       }
       ov = a / L;
-      lse = (M + __log2f(L)) * kLn2;
+      lse = XF ? S::lse(M, __log2f(L)) : (M + __log2f(L)) * kLn2;
     }
     sp.part_o[(row * sp.n_splits + split) * kD + d] = ov;
     if (d == 0) sp.part_lse[row * sp.n_splits + split] = lse;

@@ -185,12 +185,13 @@ __global__ void __launch_bounds__(kThreads) decode_q8_kernel(const __grid_consta
   // channel): head 8j + gid, channel block c; b0 holds channels 16c + 4tig and
   // + 2, b1 channels + 1 and + 3 (the order the K bytes arrive in).  qs sums
   // the thread's rounded Q' values, for the bias correction below.
+  using S = Scores<XF>;   // (masks come with XF)
   uint32_t qb[NT][8][2];
   float kinit[NT][2];
   {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     const T* Q = static_cast<const T*>(p.Q);
-    const float cs = p.scale * kLog2e;
+    const float cs = p.scale * S::kUnit;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int hh = 8 * j + gid;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) decode_q8_kernel(const __grid_consta
     }
   }
   const bool capped = XF && p.softcap > 0.f;
-  const float kinv = capped ? 1.f / (p.softcap * kLog2e) : 0.f, cap2 = p.softcap * kLog2e;
+  const float cap2 = p.softcap * S::kUnit, kinv = capped ? 1.f / cap2 : 0.f;
   const float* mrow = XF && p.M ? p.M + p.m.off + (int64_t)b * p.m.bs : nullptr;
   const bool plain = !XF;
 
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) decode_q8_kernel(const __grid_consta
           const int64_t key = k0 + gid + 8 * (e >> 1);
           const int hh = 8 * j + 2 * tig + (e & 1);
           float x = capped ? cap2 * tanh_exp2(st[j][e] * kinv) : st[j][e];
-          if (mrow && key < end && hh < nh) x = fmaf(mrow[(int64_t)(h0 + hh) * p.m.hs + key], kLog2e, x);
+          if (mrow && key < end && hh < nh) x += mrow[(int64_t)(h0 + hh) * p.m.hs + key];
           st[j][e] = key < end ? x : -INFINITY;
         }
     }
@@ -306,8 +307,8 @@ __global__ void __launch_bounds__(kThreads) decode_q8_kernel(const __grid_consta
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        if (mx > m_ref[j][q] + kSlack) {
-          const float corr = ex2_approx(m_ref[j][q] - mx);
+        if (mx > m_ref[j][q] + (XF ? kSlack * kLn2 : kSlack)) {
+          const float corr = S::weight(m_ref[j][q], mx);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             o[c][j][q] *= corr;
@@ -320,8 +321,8 @@ __global__ void __launch_bounds__(kThreads) decode_q8_kernel(const __grid_consta
       }
       const float mu0 = m_ref[j][0] == -INFINITY ? 0.f : m_ref[j][0];
       const float mu1 = m_ref[j][1] == -INFINITY ? 0.f : m_ref[j][1];
-      __half2 p01 = __floats2half2_rn(ex2_approx(st[j][0] - mu0), ex2_approx(st[j][1] - mu1));
-      __half2 p23 = __floats2half2_rn(ex2_approx(st[j][2] - mu0), ex2_approx(st[j][3] - mu1));
+      __half2 p01 = __floats2half2_rn(S::weight(st[j][0], mu0), S::weight(st[j][1], mu1));
+      __half2 p23 = __floats2half2_rn(S::weight(st[j][2], mu0), S::weight(st[j][3], mu1));
       // P as an 8-key x 8-head matrix per key half; transposed, it is the B
       // operand (k = keys 2tig, 2tig + 1 (+ 8), n = head gid).
       pb[j][0] = movtrans(*reinterpret_cast<uint32_t*>(&p01));
@@ -397,12 +398,12 @@ __global__ void __launch_bounds__(kThreads) decode_q8_kernel(const __grid_consta
       float L = 0.f, a = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_approx(red_m[w][hh] - M);
+        const float f = S::weight(red_m[w][hh], M);
         L = fmaf(f, red_l[w][hh], L);
         a = fmaf(f, red_acc[(w * kHc + hh) * kD + d], a);
       }
       ov = a / L * p.v_scale[per_channel ? g * kD + d : 0];
-      lse = (M + __log2f(L)) * kLn2;
+      lse = XF ? S::lse(M, __log2f(L)) : (M + __log2f(L)) * kLn2;
     }
     sp.part_o[(row * sp.n_splits + split) * kD + d] = ov;
     if (d == 0) sp.part_lse[row * sp.n_splits + split] = lse;

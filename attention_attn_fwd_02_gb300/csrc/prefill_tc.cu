@@ -56,6 +56,11 @@ constexpr int kProducerRegs = 56;
 constexpr int kSplitRegs = 8 * 32 * kSoftmaxRegs + 4 * 32 * kProducerRegs;
 static_assert(kSplitRegs <= kThreads * ((65536 / kThreads) & ~7), "register split exceeds the block's registers");
 constexpr float kLog2e = 1.4426950408889634f;
+// Masked passes keep natural references: an additive mask may hold any float32
+// down to the lowest.  Beyond kFar the rounding of a reference times log2(e)
+// would enter the exponent (or the product has no float32): the scores are then
+// taken relative to it first.
+constexpr float kFar = 0x1p20f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kSlack = 8.0f;     // log2 units
 
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = p.scale * kLog2e;
     // Soft-capping: the scaled product s becomes cap2 * tanh(s_raw * kinv) in log2 units.
     const bool capped = p.softcap > 0.f;
-    const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * kLog2e;
+    const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * Scores<MASK>::kUnit;
     // Without softcap and with a positive scale the scores of a masked problem
     // stay in natural units, s * scale + mask (one packed FMA for two keys),
     // and the exponent's multiplier takes log2(e).  Scores under a softcap or a
@@ -465,12 +470,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // test), so that the common kernels do not carry that path's registers.
     const bool mask_nat = MASK && !capped && sc > 0.f;
     const bool explicit_x = XF;
-    const float c_eff = mask_nat ? kLog2e : (explicit_x ? 1.f : sc);
+    const float c_eff = MASK ? kLog2e : (explicit_x ? 1.f : sc);
+    using S = Scores<MASK>;
+    constexpr float kRise = MASK ? kSlack * kLn2 : kSlack;   // in the units of m_ref
     const uint64_t scale2 = f2u(p.scale, p.scale);
     const float* mrow = nullptr;
     if (MASK && qrow < p.Sq)
       mrow = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)(h + t * ht_step) * p.m.hs + (int64_t)qrow * p.m.rs;
     float m_ref = -INFINITY, l = 0.f;
+    auto fold = [&](float sink) {
+      return MASK ? fold_sink<false>(m_ref, l, sink) : fold_sink<true>(m_ref, l, sink * kLog2e);
+    };
     bool ok = true;
     uint32_t x[BN];
     const int n_my = t ? n_tiles : n0;   // this query tile's key tiles
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else if (explicit_x) {
-          // Scores to log2 units with the additive mask, one 32-column chunk at a
+          // Scores (natural with the additive mask, else in log2 units), one 32-column chunk at a
           // time (the wait's memory clobber keeps at most 32 mask loads live).
 #pragma unroll
           for (int c = 0; c < BN / 32; ++c) {
@@ -584,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               float v = -INFINITY;
               if (kk >= lo && kk < hi) {
                 const float s = __uint_as_float(x[e]);
-                const float t = capped ? cap2 * tanh_exp2(s * kinv) : s * sc;
-                v = MASK ? fmaf(mrow[kk], kLog2e, t) : t;
+                const float t = capped ? cap2 * tanh_exp2(s * kinv) : s * (MASK ? p.scale : sc);
+                v = MASK ? mrow[kk] + t : t;
               }
               x[e] = __float_as_uint(v);
               if ((e & 7) == 7) asm volatile("" ::: "memory");  // at most 8 mask loads in flight
@@ -604,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx0 = max3(mx0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
             mx1 = max3(mx1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
           }
-          const float mt = fmaxf(mx0, mx1) * c_eff;
-          const bool raise = mt > m_ref + kSlack;     // also true for the first tile with a visible key
-          if (raise) corr = ex2(m_ref - mt);          // 0 when m_ref = -inf
+          const float mt = fmaxf(mx0, mx1) * (MASK ? 1.f : c_eff);
+          const bool raise = mt > m_ref + kRise;     // also true for the first tile with a visible key
+          if (raise) corr = S::weight(m_ref, mt);     // 0 when m_ref = -inf
           // O holds earlier tiles' sums only if m_ref was finite; it is rescaled
           // below, after P is stored (warp-uniform TMEM traffic).
           rescale = raise && m_ref > -INFINITY;
@@ -615,7 +625,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_ref = mt;
           }
         }
-        const float neg = -(m_ref == -INFINITY ? 0.f : m_ref);
+        float neg = -(m_ref == -INFINITY ? 0.f : MASK ? m_ref * kLog2e : m_ref);
+        if constexpr (MASK) {
+          const bool far = fabsf(m_ref) > kFar && fabsf(m_ref) < INFINITY;
+          if (__any_sync(0xffffffffu, far)) {
+            const float shift = far ? m_ref : 0.f;
+  #pragma unroll
+            for (int e = 0; e < BN; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - shift);
+            if (far) neg = 0.f;
+          }
+        }
         const uint64_t c2 = f2u(c_eff, c_eff), n2 = f2u(neg, neg);
         float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
 #pragma unroll
@@ -671,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = qrow < p.Sq && ht < (g + 1) * p.qpg;
       // The sink logit joins the denominator (and rescales the accumulated O);
       // with key ranges the merge adds it once.
-      const float o_mul = p.sink_on && sp.n_splits == 1 ? fold_sink<true>(m_ref, l, sink_logit(p, ht) * kLog2e) : 1.f;
+      const float o_mul = p.sink_on && sp.n_splits == 1 ? fold(sink_logit(p, ht)) : 1.f;
       const bool hidden_row = (l == 0.f);         // no visible key; a NaN l stays a NaN row
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       T* orow = valid ? static_cast<T*>(p.O) + p.o.off + (int64_t)b * p.o.bs + (int64_t)ht * p.o.hs +
@@ -699,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
           }
         }
-        if (valid) sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
+        if (valid) sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
       } else {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -726,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (valid && p.lse)
           p.lse[(int64_t)b * p.lse_bs + (int64_t)ht * p.lse_hs + qrow] =
-              hidden_row ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
+              hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
       }
     }
   }

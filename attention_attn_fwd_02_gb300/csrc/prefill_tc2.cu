@@ -68,6 +68,11 @@ constexpr int kUnits = 4;               // ring units
 constexpr int kUnit = 32768;            // bytes per unit: a CTA's half of a K or V tile
 constexpr int kKHalf = BN / 2;          // keys of a K tile each CTA holds
 constexpr float kLog2e = 1.4426950408889634f;
+// Masked passes keep natural references: an additive mask may hold any float32
+// down to the lowest.  Beyond kFar the rounding of a reference times log2(e)
+// would enter the exponent (or the product has no float32): the scores are then
+// taken relative to it first.
+constexpr float kFar = 0x1p20f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kSlack = 8.0f;          // log2 units
 constexpr int kMaskCap = 4096;
@@ -499,7 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const float sc = p.scale * kLog2e;
     // Soft-capping: the scaled product s becomes cap2 * tanh(s_raw * kinv) in log2 units.
     const bool capped = p.softcap > 0.f;
-    const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * kLog2e;
+    const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * Scores<MASK>::kUnit;
     // With a mask, no softcap and a positive scale the scores stay in natural
     // units, s * scale + mask (one packed FMA for two keys), and the exponent's
     // multiplier takes log2(e); scores under a softcap or a scale that is not
@@ -508,12 +513,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // not carry that path.
     const bool mask_nat = MASK && !capped && sc > 0.f;
     const bool explicit_x = XF;
-    const float c_eff = mask_nat ? kLog2e : (explicit_x ? 1.f : sc);
+    const float c_eff = MASK ? kLog2e : (explicit_x ? 1.f : sc);
+    using S = Scores<MASK>;
+    constexpr float kRise = MASK ? kSlack * kLn2 : kSlack;   // in the units of m_ref
     const uint64_t scale2 = f2u(p.scale, p.scale);
     const float* mrow = nullptr;
     if (MASK && qrow < p.Sq)
       mrow = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)h * p.m.hs + (int64_t)qrow * p.m.rs;
     float m_ref = -INFINITY, l = 0.f;
+    auto fold = [&](float sink) {
+      return MASK ? fold_sink<false>(m_ref, l, sink) : fold_sink<true>(m_ref, l, sink * kLog2e);
+    };
     bool ok = true;
     uint32_t x[kHalf];
     for (int i = 0; i < n_tiles; ++i) {
@@ -576,13 +586,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       } else if (explicit_x) {
-        // Scores to log2 units plus the additive mask.
+        // Scores (natural with the additive mask, else in log2 units).
 #pragma unroll
         for (int e = 0; e < kHalf; ++e) {
           const int kk = k0 + e;
           const float s = __uint_as_float(x[e]);
-          const float t = capped ? cap2 * tanh_exp2(s * kinv) : s * sc;
-          const float v = MASK ? fmaf(mv[e], kLog2e, t) : t;
+          const float t = capped ? cap2 * tanh_exp2(s * kinv) : s * (MASK ? p.scale : sc);
+          const float v = MASK ? mv[e] + t : t;
           x[e] = __float_as_uint((kk >= lo && kk < hi) ? v : -INFINITY);
         }
       } else if (!inside) {
@@ -608,16 +618,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       fence_after();
-      const float mt = fmaxf(sb.red_max[slot][0][r], sb.red_max[slot][1][r]) * c_eff;
-      const bool raise = mt > m_ref + kSlack;  // also true for the first tile with a visible key
+      const float mt = fmaxf(sb.red_max[slot][0][r], sb.red_max[slot][1][r]) * (MASK ? 1.f : c_eff);
+      const bool raise = mt > m_ref + kRise;  // also true for the first tile with a visible key
       float corr = 1.f;
-      if (raise) corr = ex2(m_ref - mt);       // 0 when m_ref = -inf
+      if (raise) corr = S::weight(m_ref, mt);  // 0 when m_ref = -inf
       const bool rescale = raise && m_ref > -INFINITY;
       if (raise) {
         l *= corr;
         m_ref = mt;
       }
-      const float neg = -(m_ref == -INFINITY ? 0.f : m_ref);
+      float neg = -(m_ref == -INFINITY ? 0.f : MASK ? m_ref * kLog2e : m_ref);
+      if constexpr (MASK) {
+        const bool far = fabsf(m_ref) > kFar && fabsf(m_ref) < INFINITY;
+        if (__any_sync(0xffffffffu, far)) {
+          const float shift = far ? m_ref : 0.f;
+#pragma unroll
+          for (int e = 0; e < kHalf; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - shift);
+          if (far) neg = 0.f;
+        }
+      }
       const uint64_t c2 = f2u(c_eff, c_eff), n2 = f2u(neg, neg);
       float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
 #pragma unroll
@@ -685,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool valid = qrow < p.Sq && head_ok;
       // The sink logit joins the denominator (and rescales the accumulated O);
       // with key ranges the merge adds it once.
-      const float o_mul = p.sink_on && sp.n_splits == 1 ? fold_sink<true>(m_ref, l, sink_logit(p, h) * kLog2e) : 1.f;
+      const float o_mul = p.sink_on && sp.n_splits == 1 ? fold(sink_logit(p, h)) : 1.f;
       const bool hidden_row = (l == 0.f);  // no visible key; a NaN l stays a NaN row
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       T* orow = valid ? static_cast<T*>(p.O) + p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs +
@@ -714,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (valid && ch == 0)
-          sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
+          sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
       } else {
         // With a tensor map for O, each warp stages its 32 rows x 128 channels
         // in the ring, in the map's box layout (two boxes of 64 channels, rows
@@ -765,7 +784,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (valid && p.lse && ch == 0)
           p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + qrow] =
-              hidden_row ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
+              hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
       }
     }
   }

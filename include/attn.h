@@ -29,6 +29,9 @@
  * non-zero weight (k_len = 0 included) gives NaN in every O element, or 0
  * under ATTN_MASKED_ROWS_ZERO, and LSE = -inf.  Out-of-range k_lens and seg
  * values are clamped to [0, k_len] (a convention of this library).
+ * Only -inf hides: a finite mask of any size, the lowest float32 among them,
+ * is added in float32, where from about 2^28 on it absorbs the score beside it
+ * (a row that carries one such value throughout has the mean of its keys' V).
  *
  * Score transforms ("com.microsoft.GroupQueryAttention", attributes softcap
  * and smooth_softmax, input head_sink).  With softcap c > 0 the scaled dot

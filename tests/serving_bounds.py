@@ -6,8 +6,8 @@ O' - O = sum_k w_k (exp(dx_k) - 1) (v_k - O), so to first order
 |dO| <= sum_k w_k |dx_k| |v_k - O|.  Scores: a float32 sum of D products and two
 more roundings, (D + 4) u sum_d |q_d k_d| scale with u = 2^-24, the roundings of
 the scaled value and of its difference to the reference, u (2 |x| + 2 |x - top|),
-and a base-2 exponential of 2^-22.  (A mask below -2^100 absorbs its score on
-both sides.)  The float32 sums over keys run through about n / 16 steps, each
+and a base-2 exponential of 2^-22.  (A mask of 2^28 or more absorbs its score, as
+the float32 sum does.)  The float32 sums over keys run through about n / 16 steps, each
 of which a tensor-core product may truncate: (16 + n / 8) u sum w |v|.  A
 probability that enters its product rounded adds p_rel of itself and p_abs of the
 row's largest one: `single` is one value of the element type, `halves` two (16
@@ -21,7 +21,25 @@ import math
 import torch
 
 U32 = 2.0 ** -24
+ABSORBS = 2.0 ** 28   # a mask whose float32 spacing is 32
+LOW = torch.finfo(torch.float32).min
 HALF = {torch.float32: U32, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+
+
+def mask_kinds(g, *shape):
+    """Masks [..., keys] with a kind a row: all lowest; lowest and -inf; two values below -2.4e38; one at zero among
+    lowest; ordinary ones; all -inf; all -1e9; some 1e9 among ordinary ones."""
+    rows, keys = shape[:-1], shape[-1]
+    m = torch.full(shape, LOW, device="cuda")
+    kind = torch.randint(0, 8, rows, generator=g, device="cuda")[..., None]
+    r = torch.rand(shape, generator=g, device="cuda")
+    m = torch.where((kind == 1) & (r < 0.5), -math.inf, m)
+    m = torch.where((kind == 2) & (r < 0.3), -3.0e38, m)
+    m = torch.where((kind == 3) & (torch.arange(keys, device="cuda") == 2), 0.0, m)
+    m = torch.where(kind == 4, r, m)
+    m = torch.where(kind == 6, -1e9, m)
+    m = torch.where(kind == 7, torch.where(r < 0.2, 1e9, r), m)
+    return torch.where(kind == 5, -math.inf, m)
 
 
 def p_error(dt, how):
@@ -53,7 +71,7 @@ def attention(q, k, v, vis, *, p="halves", scale=0.0, mask=None, softcap=0.0, si
     if softcap:
         x = softcap * torch.tanh(x / softcap)
     if mask is not None:
-        x = x + mask.double()
+        x = torch.where(mask.abs() >= ABSORBS, mask.double(), x + mask.double())
     x = x.masked_fill(~vis[:, None], -math.inf)
     top = x.amax(-1, keepdim=True)
     sg = torch.full((B, H, Sq, 1), -math.inf, dtype=torch.float64, device=dev)
@@ -67,7 +85,7 @@ def attention(q, k, v, vis, *, p="halves", scale=0.0, mask=None, softcap=0.0, si
     o = w @ v
     lse = (base + torch.log(den)).squeeze(-1)
     # bounds
-    size = torch.where(x.abs() < 2.0 ** 100, x.abs(), 0.0)
+    size = torch.where(x.abs() < ABSORBS, x.abs(), 0.0)
     away = torch.where(x > -math.inf, (x - base).abs(), 0.0).clamp(max=200)
     dx = (D + 4) * U32 * mag + extra_score * mag + U32 * (2 * size + 2 * away) + 2.0 ** -22
     if softcap:

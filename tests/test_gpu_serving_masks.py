@@ -4,8 +4,6 @@ all carry the lowest value has the mean of their V (its scores are absorbed), a
 key beside a higher value has no weight, and only -inf takes a key out."""
 from __future__ import annotations
 
-import math
-
 import pytest
 
 import serving_bounds as sb
@@ -14,7 +12,7 @@ from attention_attn_fwd_02_gb300 import attn, build
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
-LOW = torch.finfo(torch.float32).min
+LOW = sb.LOW
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -35,20 +33,6 @@ def randn(g, *shape, dt=torch.float32):
     return torch.randn(*shape, generator=g, device="cuda").to(dt)
 
 
-def kinds(g, *shape):
-    """Masks [*shape, keys] with a kind a row: all lowest; lowest and -inf; two values below -2.4e38; one at zero
-    among lowest; ordinary ones; all -inf."""
-    rows, keys = shape[:-1], shape[-1]
-    m = torch.full(shape, LOW, device="cuda")
-    kind = torch.randint(0, 6, rows, generator=g, device="cuda")[..., None]
-    r = torch.rand(shape, generator=g, device="cuda")
-    m = torch.where((kind == 1) & (r < 0.5), -math.inf, m)
-    m = torch.where((kind == 2) & (r < 0.3), -3.0e38, m)
-    m = torch.where((kind == 3) & (torch.arange(keys, device="cuda") == 2), 0.0, m)
-    m = torch.where(kind == 4, r, m)
-    return torch.where(kind == 5, -math.inf, m)
-
-
 @pytest.mark.parametrize("dt,D,H,G,Sq,Sk,w,first,opt", [
     ("bf16", 128, 4, 2, 300, 700, 90, 5, {}),
     ("f16", 64, 4, 2, 300, 300, 90, 40, dict(sink=True)),
@@ -64,7 +48,7 @@ def kinds(g, *shape):
 def test_window_masks(dt, D, H, G, Sq, Sk, w, first, opt):
     g = gen(3 + D + Sq)
     q, k, v = (randn(g, 1, h, n, D, dt=DT[dt]) for h, n in ((H, Sq), (G, Sk), (G, Sk)))
-    mask = kinds(g, 1, 1, Sq, Sk)
+    mask = sb.mask_kinds(g, 1, 1, Sq, Sk)
     sink = randn(g, H) if opt.get("sink") else None
     i, j = torch.arange(Sq, device="cuda")[:, None] + Sk - Sq, torch.arange(Sk, device="cuda")[None]
     vis = ((j <= i) & ((j >= i - w) | (j < first)))[None]
@@ -100,7 +84,7 @@ def test_paged_masks(dt, D, H, G, B, rows, opt):
     q = randn(g, B, 1, H, D, dt=DT[dt])
     table = torch.randint(0, 60, (B, -(-rows // ps)), generator=g, device="cuda").to(torch.int32)
     n = torch.randint(rows // 2, rows + 1, (B,), generator=g, device="cuda").to(torch.int32)
-    mask = kinds(g, B, H, 1, rows)
+    mask = sb.mask_kinds(g, B, H, 1, rows)
     sink = randn(g, H) if opt.get("sink") else None
     vis = (torch.arange(rows, device="cuda")[None] < n[:, None])[:, None]
     o, lse, tol, tol_l = sb.attention(q.transpose(1, 2), sb.rows_of(k, table, ps, rows), sb.rows_of(v, table, ps, rows),
