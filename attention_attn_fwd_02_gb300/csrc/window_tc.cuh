@@ -156,10 +156,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   using S = Scores<XF>;   // (masks come with XF)
   constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
-  // A row's reference is a maximum, less a lead where P is f16: p is 2^7 at that maximum (a tile of 128 such keys
-  // sums to 2^14 and causes no scan), and what f16 cannot hold (2^-25) is 2^-32 of the row's largest probability,
-  // for all keys together n 2^-32: under a quarter of f16's half step up to 2^19 keys of window.
-  constexpr float kLead = (BF16 ? 0.f : 7.f) * (XF ? kLn2 : 1.f);
+  // A row's reference is a maximum, less a lead where P is f16: p is 2^5 at that maximum, and what f16 cannot hold
+  // (2^-25) is 2^-30 of the row's largest probability, for all keys together n 2^-30: under a quarter of f16's half
+  // step up to 2^17 keys of window.  More lead takes room from the lag (kLagMax): a first tile of four keys puts the
+  // reference some units under the next tile's sums, and with a lead of 7 most warps scanned twice there (4096
+  // tokens, 32/8 heads, head_dim 64: 65 -> 74 us).
+  constexpr float kLead = (BF16 ? 0.f : 5.f) * (XF ? kLn2 : 1.f);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int my_items = (n_items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   // The two query tiles are rows [q0, q0 + 256) of one head, or with
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scan.
         auto step = [&](auto cols) {
           constexpr int N = decltype(cols)::value;
-          constexpr float kLagMax = BF16 ? 0x1p64f : 0x1p15f;
+          constexpr float kLagMax = BF16 ? 0x1p64f : 65504.f;   // (no p of f16 overflows below)
           bool scan = __any_sync(0xffffffffu, !(m_ref > -INFINITY));
 #pragma unroll 1
           for (int pass = 0; pass < 2; ++pass) {

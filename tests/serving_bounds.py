@@ -47,7 +47,7 @@ def p_error(dt, how):
     if dt == torch.float32:
         return 0.0, 0.0
     if how == "single":
-        return HALF[dt], 0.0 if dt == torch.bfloat16 else 2.0 ** -32
+        return HALF[dt], 0.0 if dt == torch.bfloat16 else 2.0 ** -30   # half f16's least value, 2^-25, on a top of 2^5
     return (2.0 ** -15, 0.0) if dt == torch.bfloat16 else (2.0 ** -20, 2.0 ** -34)
 
 
