@@ -418,6 +418,8 @@ def fwd(q, k, v, *, layout="bshd", causal=False, causal_offset=None, scale=0.0, 
         _check_same(q, k=k, v=v, out=out, ints=(seg, k_lens), floats=(mask, lse, head_sink))
         with torch.cuda.device(q.device):
             ws_bytes = attn_fwd_window_workspace_size(p, first_keys)
+            if ws_bytes and mask is not None:
+                ws_bytes += 4 * 16 * B * H * Sq + 256   # the sums of up to 16 parts
             ws = _empty(stream, q.device, ws_bytes, torch.uint8) if ws_bytes else None
             st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
             _check(attn_fwd_window(p, first_keys, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(mask), _ptr(seg),

@@ -544,9 +544,9 @@ int attn_fwd_window(const attn_problem* p, int32_t first_keys, const void* q, co
   if (n > 1 && !cluster) {
     const bool enough = workspace && workspace_bytes >= decode_ws_bytes(p, n);
     if (enough && aligned(workspace, 256)) {
-      // Under a mask the parts' sums take the room of a part.
+      // Under a mask the parts' sums take the room of a part, unless the workspace has more.
       int parts = n;
-      while (mask && parts > 1 && sums_ws_bytes(p, parts) > decode_ws_bytes(p, n)) --parts;
+      while (mask && parts > 1 && sums_ws_bytes(p, parts) > workspace_bytes) --parts;
       if (parts > 1)
         s = split_in(workspace, (size_t)p->batch * p->heads * p->q_len, parts, 0, p->head_dim, mask != nullptr);
     } else if (p->key_splits > 1)

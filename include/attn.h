@@ -275,8 +275,11 @@ ATTN_API int attn_decode_append(const attn_problem* p, const void* q, const void
  * p->key_splits >= 1 asks for a count.  float32 problems and asked-for counts
  * take a workspace (float32 [B*H*q_len][parts][head_dim] and
  * [B*H*q_len][parts], each 256-byte aligned); the parts the library chooses
- * for f16/bf16 meet in shared memory.  Returns 0 for an invalid problem;
- * attn_fwd_window then reports the error. */
+ * for f16/bf16 meet in shared memory.  With a mask the parts also keep a sum
+ * each ([B*H*q_len][parts] floats more, 256-byte aligned): a call whose
+ * workspace has no room for them takes as many parts as fit, one fewer as a
+ * rule.  Returns 0 for an invalid problem; attn_fwd_window then reports the
+ * error. */
 ATTN_API size_t attn_fwd_window_workspace_size(const attn_problem* p, int32_t first_keys);
 
 /* attn_fwd with first_keys (>= 0) keys of each row's span visible behind its
