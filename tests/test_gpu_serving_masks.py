@@ -115,3 +115,31 @@ def test_lowest_sinks(dt):
     got, lse = attn.fwd(qq, kv, kv, head_sink=sink, return_lse=True, **kw)
     assert torch.equal(got, attn.fwd(qq, kv, kv, masked_rows="zero", **kw))
     assert (lse[:, :, :5] == LOW).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dt,D,splits", [("f32", 64, 0), ("f32", 48, 5), ("bf16", 64, 6), ("f16", 96, 2), ("f16", 128, 16)])
+@pytest.mark.parametrize("room", [0, 1 << 16])
+def test_masked_parts_stay_in_the_workspace(dt, D, splits, room):
+    """The workspace the query asks for holds masked parts and their sums (fewer parts), a larger one all parts."""
+    g, guard = gen(D + splits), 1 << 12
+    H, G, Sq, Sk, w, first = 2, 1, 40, 2000, 1500, 5
+    q, k, v = (randn(g, 1, h, n, D, dt=DT[dt]) for h, n in ((H, Sq), (G, Sk), (G, Sk)))
+    mask = sb.mask_kinds(g, 1, 1, Sq, Sk)
+    out, lse = torch.empty_like(q), torch.empty(1, H, Sq, device="cuda")
+    p = attn.make_problem(dict(
+        batch=1, heads=H, kv_heads=G, q_len=Sq, k_len=Sk, head_dim=D, dtype=dt, causal=True, window_left=w,
+        masked_rows="zero", key_splits=splits, mask_layout=(0, 0, 0, mask.stride(2)), lse_layout=lse.stride()[:2],
+        **{f"{n}_layout": attn._layout4(t, 1) for n, t in (("q", q), ("k", k), ("v", v), ("o", out))}))
+    size = attn.attn_fwd_window_workspace_size(p, first)
+    assert size
+    size += room
+    ws = torch.full((size + 2 * guard,), 171, dtype=torch.uint8, device="cuda")
+    assert attn.attn_fwd_window(p, first, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), mask.data_ptr(), None,
+                                None, lse.data_ptr(), ws.data_ptr() + guard, size,
+                                torch.cuda.current_stream().cuda_stream) == 0
+    i, j = torch.arange(Sq, device="cuda")[:, None] + Sk - Sq, torch.arange(Sk, device="cuda")[None]
+    vis = ((j <= i) & ((j >= i - w) | (j < first)))[None]
+    o, l, tol, tol_l = sb.attention(q, k, v, vis, p="single", mask=mask)
+    sb.check(out, o, tol, "O")
+    sb.check(lse, l, tol_l, "LSE")
+    assert (ws[:guard] == 171).all() and (ws[guard + size:] == 171).all()
