@@ -14,7 +14,8 @@
 //
 // The scales leave the loop: Q . (k8 * s_k) = (Q * s_k) . k8, so Q is scaled
 // by the key scales once (per channel), and by scale * log2(e) so that scores
-// come out in log2 units, then rounded to f16; and
+// come out in log2 units (under a mask or a softcap by scale: natural ones),
+// then rounded to f16; and
 // sum p (v8 * s_v) = s_v * sum p v8, so the value scale multiplies the finished
 // partial O.  The integers enter the tensor cores as exact f16 values with a
 // bias: a byte x becomes the f16 with bits 0x6400 | (x ^ 0x80), whose value is
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) decode_q8_kernel(const __grid_consta
     // Rows past the range end need no clearing: their probabilities are 0 and
     // every int8 value is finite (rows past the capacity are zero-filled).
     // S^T = K Q'^T for the warp's 16 keys (MMA rows: keys gid, gid + 8),
-    // started at the bias correction so that it holds the scores in log2 units.
+    // started at the bias correction so that it holds the scores in their units.
     float st[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {

@@ -13,7 +13,7 @@
 // deterministic.
 //
 // Short lists have no fragments and no join.  Few units: a unit is a thread-block
-// cluster's of 2, 4 or 8 CTAs, each with a part of its list, which merges the
+// cluster's of 2 to 8 CTAs, each with a part of its list, which merges the
 // parts through distributed shared memory.  Many: a CTA takes whole units, one
 // after the other.
 #pragma once
@@ -28,7 +28,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kSlack = 8.0f;   // log2 units: how far a score may rise above the reference maximum
+constexpr float kSlack = 8.0f;   // log2 units: how far a score may rise above a reference that is a maximum
 constexpr unsigned kAll = 0xffffffffu;
 
 // How a pass's CTAs divide the units: equal shares of all tiles, a cluster a
@@ -427,6 +427,7 @@ cudaError_t launch_join(const Work& w, cudaStream_t st);
 // 21.0, 12 of up to 6000 rows 41.8 -> 32.7 (clusters); 57 of 900 to 1000 rows
 // 48.9 -> 38.6, 90 of up to 100 rows 19.9 -> 12.6 (whole units); the other way
 // round, 8/8 heads: one sequence of 12000 rows 16.1 against 21.0 in clusters.
+// (float32 passes take the same limits, which were measured in bf16 alone.)
 inline void plan_work(Work& w, int tile, int heads, int ctas) {
   w.unit = tile;
   w.heads = heads;

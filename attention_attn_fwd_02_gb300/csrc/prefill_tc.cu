@@ -459,13 +459,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tm = tmem + lane_off + (t ? C::kS1 : C::kS0);
     const uint32_t o_tm = tmem + lane_off + (t ? C::kO1 : C::kO0);
     const float sc = p.scale * kLog2e;
-    // Soft-capping: the scaled product s becomes cap2 * tanh(s_raw * kinv) in log2 units.
+    // Soft-capping: the scaled product s becomes cap2 * tanh(s_raw * kinv), in log2 units
+    // or, with a mask, natural ones.
     const bool capped = p.softcap > 0.f;
     const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * Scores<MASK>::kUnit;
     // Without softcap and with a positive scale the scores of a masked problem
     // stay in natural units, s * scale + mask (one packed FMA for two keys),
     // and the exponent's multiplier takes log2(e).  Scores under a softcap or a
-    // scale that is not positive are formed in log2 units one at a time, in an
+    // scale that is not positive are formed one at a time, in an
     // instantiation of their own (XF, chosen by the launcher from the same
     // test), so that the common kernels do not carry that path's registers.
     const bool mask_nat = MASK && !capped && sc > 0.f;

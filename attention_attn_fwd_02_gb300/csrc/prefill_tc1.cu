@@ -439,13 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       return wait_warp(pair_bar, (uint32_t)phase & 1u, &sb.abort, p.status);
     };
     const float sc = p.scale * kLog2e;
-    // Soft-capping: the scaled product s becomes cap2 * tanh(s_raw * kinv) in log2 units.
+    // Soft-capping: the scaled product s becomes cap2 * tanh(s_raw * kinv), in log2 units
+    // or, with a mask, natural ones.
     const bool capped = p.softcap > 0.f;
     const float kinv = capped ? p.scale / p.softcap : 0.f, cap2 = p.softcap * Scores<MASK>::kUnit;
     // With a mask, no softcap and a positive scale the scores stay in natural
     // units, s * scale + mask (one packed FMA for two keys), and the exponent's
     // multiplier takes log2(e); scores under a softcap or a scale that is not
-    // positive are formed in log2 units, in an instantiation of their own (XF,
+    // positive are formed one at a time, in an instantiation of their own (XF,
     // chosen by the launcher from the same test).
     const bool mask_nat = MASK && !capped && sc > 0.f;
     const bool explicit_x = XF;

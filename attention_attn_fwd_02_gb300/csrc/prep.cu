@@ -220,7 +220,10 @@ struct Vec<__half> {
 // MB): one warp a row and scalar loads 422 us; this form with one item a warp,
 // Q, K and V mixed 121 us; of one kind, packed arithmetic 96 us; striding
 // 71.6 us (5.66 TB/s) with 3 groups and 3 CTAs an SM (2 and 4: 74.0, 4 and 2:
-// 88).
+// 88).  Three CTAs leave 80 registers a thread, where the f16/bf16 instances
+// spill 20 to 36 bytes: with two CTAs and no spills 80.0 against 70.3 us.  Into
+// an int8 cache 100.5 us (a division and a rounding an element).  The form of
+// one warp a row, which head_dim 80 and 96 take: 404 and 422 us for such prompts.
 constexpr int kSteps = 3;
 constexpr int kCtasPerSm = 3;
 

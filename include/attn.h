@@ -58,6 +58,13 @@
  * finite, or rows of that tile that hide the key may become NaN (tensor-core
  * products multiply them by zero).
  *
+ * Precision.  Scores, softmax statistics and sums are float32.  With f16/bf16
+ * Q the tensor-core passes round a probability once to the element type before
+ * its product with V ("Attention", section "Matrix hardware"); attn_decode over
+ * an int8 cache rounds it, and the scaled query, to f16.  float32 and CUDA-core
+ * passes round neither, and attn_decode_paged takes both in two halves, so that
+ * its results carry their own rounding only.
+ *
  * Execution.  Calls are asynchronous on `stream` (a cudaStream_t; NULL = the
  * legacy default stream): they validate on the host, enqueue kernels and
  * return.  No call synchronises the host except attn_device_status.  No C++
