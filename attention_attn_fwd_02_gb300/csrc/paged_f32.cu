@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
                      st_key[warp][s] + key];
         }
         sc[h] = seen ? v : -INFINITY;
-        rise |= sc[h] > m_ref[h] + kRise;
+        rise |= sc[h] - m_ref[h] > kRise;
       }
       if (__any_sync(kAll, rise)) {
 #pragma unroll
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
           float mx = sc[h];
 #pragma unroll
           for (int x = 1; x < KEYS; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, x));
-          if (mx > m_ref[h] + kRise) {
+          if (mx - m_ref[h] > kRise) {
             const float f = S::weight(m_ref[h], mx);
             l[h] *= f;
 #pragma unroll

@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           for (int e = 0; e < 4; ++e)
             if (!((vis >> (16 * mb + gid + 8 * (e >> 1))) & 1u)) sc[mb][j][e] = -INFINITY;
     }
-    // The reference moves only when a score rises above it by more than kRise.
+    // The reference moves only when a score rises above it by more than kRise (by their difference, which is exact
+    // where large masks leave no room for kRise beside a reference).
     float top[NT][2];
     bool rise = false;
 #pragma unroll
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
         top[j][q] = fmaxf(sc[0][j][q], sc[0][j][q + 2]);
 #pragma unroll
         for (int mb = 1; mb < MB; ++mb) top[j][q] = fmaxf(top[j][q], fmaxf(sc[mb][j][q], sc[mb][j][q + 2]));
-        rise |= top[j][q] > m_ref[j][q] + kRise;
+        rise |= top[j][q] - m_ref[j][q] > kRise;
       }
     if (__any_sync(kAll, rise)) {
 #pragma unroll
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-          if (mx > m_ref[j][q] + kRise) {
+          if (mx - m_ref[j][q] > kRise) {
             mx -= kLead;
             const float f = S::weight(m_ref[j][q], mx);
             l[j][q] *= f;

@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (MASK && qrow < p.Sq)
       mrow = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)(h + t * ht_step) * p.m.hs + (int64_t)qrow * p.m.rs;
     float m_ref = -INFINITY, l = 0.f;
+    auto row_lse = [&]() { return MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2; };
     auto fold = [&](float sink) {
       return MASK ? fold_sink<false>(m_ref, l, sink) : fold_sink<true>(m_ref, l, sink * kLog2e);
     };
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool far = fabsf(m_ref) > kFar && fabsf(m_ref) < INFINITY;
           if (__any_sync(0xffffffffu, far)) {
             const float shift = far ? m_ref : 0.f;
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < BN; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - shift);
             if (far) neg = 0.f;
           }
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
           }
         }
-        if (valid) sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
+        if (valid) sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : row_lse();
       } else {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (valid && p.lse)
           p.lse[(int64_t)b * p.lse_bs + (int64_t)ht * p.lse_hs + qrow] =
-              hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
+              hidden_row ? -INFINITY : row_lse();
       }
     }
   }

@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (MASK && qrow < p.Sq)
       mrow = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)h * p.m.hs + (int64_t)qrow * p.m.rs;
     float m_ref = -INFINITY, l = 0.f;
+    auto row_lse = [&]() { return MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2; };
     auto fold = [&](float sink) {
       return MASK ? fold_sink<false>(m_ref, l, sink) : fold_sink<true>(m_ref, l, sink * kLog2e);
     };
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (valid && ch == 0)
-          sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
+          sp.part_lse[prow * sp.n_splits + split] = hidden_row ? -INFINITY : row_lse();
       } else {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (valid && p.lse && ch == 0)
           p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + qrow] =
-              hidden_row ? -INFINITY : (MASK ? S::lse(m_ref, __log2f(l)) : (m_ref + __log2f(l)) * kLn2);
+              hidden_row ? -INFINITY : row_lse();
       }
     }
   }

@@ -130,8 +130,8 @@ cudaError_t launch_combine_t(int n_splits, int64_t rows, int D, const float* po,
   if (rows <= 0) return cudaSuccess;
   const int64_t blocks = (rows + 3) / 4;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  combine_kernel<T, Mask><<<(unsigned)blocks, 128, 0, st>>>(n_splits, rows, D, po, pl, sums, static_cast<T*>(o), ol, H, Sq,
-                                                      lse, lbs, lhs, lrs, masked_zero, sink_on, sink, mask);
+  combine_kernel<T, Mask><<<(unsigned)blocks, 128, 0, st>>>(n_splits, rows, D, po, pl, sums, static_cast<T*>(o), ol, H,
+                                                            Sq, lse, lbs, lhs, lrs, masked_zero, sink_on, sink, mask);
   return cudaGetLastError();
 }
 

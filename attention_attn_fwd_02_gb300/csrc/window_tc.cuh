@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx1 = max3(mx1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
               }
               float mt = fmaxf(mx0, mx1) * c_eff;
-              const bool raise = mt > m_ref + kRise;      // also true for the first tile with a visible key
+              const bool raise = mt - m_ref > kRise;      // also true for the first tile with a visible key
               mt -= kLead;
               if (raise) corr = S::weight(m_ref, mt);     // 0 when m_ref = -inf
               rescale = raise && m_ref > -INFINITY;       // O holds earlier tiles' sums
