@@ -32,7 +32,8 @@ EXPORTS = ("attn_fwd_workspace_size", "attn_fwd", "attn_decode_workspace_size", 
            "attn_device_status", "attn_status_string", "attn_version", "attn_decode_noalloc",
            "attn_decode_noalloc_max_scratch", "attn_decode_append", "attn_probe_ex2", "attn_test_inject",
            "attn_fwd_window", "attn_fwd_window_workspace_size", "attn_decode_paged",
-           "attn_decode_paged_workspace_size", "attn_qkv_prep")
+           "attn_decode_paged_workspace_size", "attn_qkv_prep", "attn_qkv_prep_axes", "attn_fwd_shared",
+           "attn_fwd_shared_workspace_size")
 
 
 class attn_layout(ctypes.Structure):
@@ -69,6 +70,14 @@ class attn_prep(ctypes.Structure):
                 ("k_out", attn_layout), ("v_out", attn_layout), ("pos_batch_stride", ctypes.c_int64),
                 ("row_batch_stride", ctypes.c_int64), ("kv_dtype", ctypes.c_int32),
                 ("kv_scale_kind", ctypes.c_int32), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class attn_prefix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("table", ctypes.c_void_p)]
+
+
+class attn_axes(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("pos_axis_stride", ctypes.c_int64), ("axis", ctypes.c_uint8 * 128)]
 
 
 class AttnError(RuntimeError):
@@ -118,6 +127,13 @@ def lib():
         L.attn_decode_paged.restype = ctypes.c_int
         L.attn_qkv_prep.argtypes = [PP, PG] + [vp] * 13
         L.attn_qkv_prep.restype = ctypes.c_int
+        PX, PA = ctypes.POINTER(attn_prefix), ctypes.POINTER(attn_axes)
+        L.attn_fwd_shared_workspace_size.argtypes = [P, PG, PX]
+        L.attn_fwd_shared_workspace_size.restype = sz
+        L.attn_fwd_shared.argtypes = [P, PG, PX, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.attn_fwd_shared.restype = ctypes.c_int
+        L.attn_qkv_prep_axes.argtypes = [PP, PG, PA] + [vp] * 13
+        L.attn_qkv_prep_axes.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -177,6 +193,22 @@ def attn_qkv_prep(p, pages, q, k, v, q_weight, k_weight, cos, sin, positions, ro
                   stream) -> int:
     return lib().attn_qkv_prep(ctypes.byref(p), pages, q, k, v, q_weight, k_weight, cos, sin, positions, rows, q_out,
                                k_out, v_out, stream)
+
+
+def attn_fwd_shared_workspace_size(p: attn_problem, pages: attn_pages, prefix: attn_prefix) -> int:
+    return lib().attn_fwd_shared_workspace_size(ctypes.byref(p), pages, prefix)
+
+
+def attn_fwd_shared(p, pages, prefix, q, k_pool, v_pool, o, mask, k_lens, lse, workspace, workspace_bytes,
+                    stream) -> int:
+    return lib().attn_fwd_shared(ctypes.byref(p), pages, prefix, q, k_pool, v_pool, o, mask, k_lens, lse, workspace,
+                                 workspace_bytes, stream)
+
+
+def attn_qkv_prep_axes(p, pages, axes, q, k, v, q_weight, k_weight, cos, sin, positions, rows, q_out, k_out, v_out,
+                       stream) -> int:
+    return lib().attn_qkv_prep_axes(ctypes.byref(p), pages, axes, q, k, v, q_weight, k_weight, cos, sin, positions,
+                                    rows, q_out, k_out, v_out, stream)
 
 
 def attn_probe_ex2(blocks, iters, sink, stream) -> int:
@@ -255,6 +287,19 @@ def make_problem(d: dict) -> attn_problem:
 def make_pages(page_size: int, n_pages: int, table, table_stride: int) -> attn_pages:
     """attn_pages; table is the device address of the int32 page lists."""
     return attn_pages(page_size, n_pages, table, table_stride)
+
+
+def make_prefix(rows: int, table) -> attn_prefix:
+    """attn_prefix; table is the device address of the prefix's int32 page list (None without rows)."""
+    return attn_prefix(rows, table)
+
+
+def make_axes(axis, pos_axis_stride: int) -> attn_axes:
+    """attn_axes from the axis of each rotated pair (whole numbers from 0) and the positions' axis stride."""
+    axis = list(axis)
+    if len(axis) > 128 or any(not 0 <= a < 256 for a in axis):
+        raise ValueError("axis: expected at most 128 axes, whole numbers from 0")
+    return attn_axes(max(axis, default=0) + 1, pos_axis_stride, (ctypes.c_uint8 * 128)(*axis))
 
 
 def make_prep(d: dict) -> attn_prep:
@@ -531,16 +576,79 @@ def decode_paged(q, k_pool, v_pool, table, k_lens=None, *, page_layout="hnd", sc
     return (out, lse) if return_lse else out
 
 
+def fwd_shared(q, k_pool, v_pool, prefix_table, prefix_rows, table, k_lens=None, *, page_layout="hnd", causal=True,
+               causal_offset=None, scale=0.0, mask=None, masked_rows="nan", return_lse=False, out=None, lse=None,
+               workspace=None, stream=None, k_lens_kind="count", softcap=0.0, smooth_softmax=False, head_sink=None,
+               k_scale=None, v_scale=None, max_rows=None):
+    """Attention of a batch whose entries share a prefix, over a paged cache: q [B, Sq, H, D] (Sq = 1: a
+    decode step); pools as for decode_paged; prefix_table int32 [pages of the prefix]: its first prefix_rows
+    rows are in front of every entry's own keys, which table and k_lens describe as for decode_paged.  Every
+    query sees the whole prefix, and own keys up to its diagonal: right-aligned to each entry's length, or
+    with causal_offset own key i + causal_offset; causal=False: all of them.  mask: float32 [B|1, H|1, Sq|1,
+    prefix_rows + max_rows or more].  Everything else as for decode_paged (attn_fwd_shared)."""
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("expected q [B, Sq, H, D]")
+    B, Sq, H, D = q.shape
+    G, ps, kl = _page_dims(k_pool, table, page_layout)
+    _, _, vl = _page_dims(v_pool, table, page_layout)
+    if v_pool.shape != k_pool.shape or k_pool.shape[3] != D or table.shape[0] != B:
+        raise ValueError("q, pools and table disagree")
+    if prefix_table.dim() != 1 or not prefix_table.is_contiguous() or not 0 <= prefix_rows <= prefix_table.numel() * ps:
+        raise ValueError("prefix_table: expected a contiguous list of the pages of prefix_rows rows")
+    rows = table.shape[1] * ps if max_rows is None else max_rows
+    if rows > table.shape[1] * ps:
+        raise ValueError("max_rows: the table holds fewer rows")
+    if out is None:
+        out = _empty(stream, q.device, q.shape, q.dtype)
+    i8 = k_pool.dtype == torch.int8
+    _check_extents(B, H, Sq, prefix_rows + rows, mask=mask, lse=lse, head_sink=head_sink, k_lens=k_lens)
+    _check_scales(i8, G, D, k_scale, v_scale)
+    if out.shape != q.shape:
+        raise ValueError("out: expected the queries' shape")
+    kv = {} if i8 else dict(k_pool=k_pool, v_pool=v_pool)
+    _check_same(q, out=out, ints=(prefix_table, table, k_lens), floats=(mask, lse, head_sink, k_scale, v_scale), **kv)
+    if i8 and (v_pool.dtype != torch.int8 or k_pool.device != q.device or v_pool.device != q.device):
+        raise ValueError("int8 pools: both int8, on the queries' device")
+    d = dict(batch=B, heads=H, kv_heads=G, q_len=Sq, k_len=rows, head_dim=D, dtype=_dtype_name(q), scale=scale,
+             causal=causal, causal_align="klens" if causal_offset is None else "fixed", causal_offset=causal_offset,
+             k_lens_kind=k_lens_kind, softcap=softcap, smooth_softmax=smooth_softmax, head_sink_ptr=_ptr(head_sink),
+             masked_rows=masked_rows, q_layout=_layout4(q, 2), kv_dtype="i8" if i8 else None,
+             kv_scale="channel" if (k_scale is not None and k_scale.numel() > 1) else "tensor",
+             k_scale_ptr=_ptr(k_scale), v_scale_ptr=_ptr(v_scale), k_layout=kl, v_layout=vl, o_layout=_layout4(out, 2))
+    if mask is not None:
+        d["mask_layout"] = (0, *(mask.stride(x) if mask.shape[x] > 1 else 0 for x in range(3)))
+    if return_lse and lse is None:
+        lse = _empty(stream, q.device, (B, H, Sq), torch.float32)
+    if lse is not None:
+        d["lse_layout"] = (lse.stride(0), lse.stride(1))
+    p, pages = make_problem(d), make_pages(ps, k_pool.shape[0], _ptr(table), table.stride(0))
+    prefix = make_prefix(prefix_rows, _ptr(prefix_table))
+    with torch.cuda.device(q.device):
+        ws_bytes = attn_fwd_shared_workspace_size(p, pages, prefix)
+        if workspace is None:
+            workspace = _empty(stream, q.device, ws_bytes, torch.uint8) if ws_bytes else None
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on {q.device}")
+        st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(attn_fwd_shared(p, pages, prefix, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(mask),
+                               _ptr(k_lens), _ptr(lse), _ptr(workspace), size, st), "attn_fwd_shared")
+    return (out, lse) if return_lse else out
+
+
 def qkv_prep(q, k, v, k_cache, v_cache, table=None, *, page_layout="hnd", q_weight=None, k_weight=None, norm=True,
              eps=1e-6, cos=None, sin=None, interleaved=False, positions=None, rows=None, k_scale=None, v_scale=None,
-             out=None, stream=None):
+             out=None, stream=None, axes=None):
     """The step before attention: RMS norm of each head of Q and K, rotation of their first
     2 * cos.shape[1] elements (no rotation without cos and sin), and the write of K and V into
     the cache.  q [B, S, H, D], k and v [B, S, G, D] (slices of a packed projection are fine);
     caches [B, G, cap, D] without a table, pools as for decode_paged with one.  cos, sin float32
     [positions, rot / 2]; positions and rows int32 [B, S] (default: the token's index): where the
     angle is taken and which cache row K and V go to (out of range: not written).  int8 caches
-    take float32 k_scale / v_scale as decode does.  Returns the prepared queries [B, S, H, D]."""
+    take float32 k_scale / v_scale as decode does.  axes: the axis (0 to 3) of each rotated pair; positions
+    are then int32 [axes, B, S], and pair j takes its angle at positions[axes[j]] (attn_qkv_prep_axes).
+    Returns the prepared queries [B, S, H, D]."""
     torch = _torch()
     if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
         raise ValueError("expected q [B, S, H, D] and k, v [B, S, G, D]")
@@ -573,23 +681,34 @@ def qkv_prep(q, k, v, k_cache, v_cache, table=None, *, page_layout="hnd", q_weig
     if (cos is None) != (sin is None) or (cos is not None and (
             cos.dim() != 2 or cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous())):
         raise ValueError("cos, sin: expected two contiguous float32 [positions, rot / 2]")
-    for name, t in (("positions", positions), ("rows", rows)):
+    if axes is not None:
+        axes = [int(a) for a in axes]
+        if cos is None or len(axes) != cos.shape[1] or not all(0 <= a < 4 for a in axes):
+            raise ValueError("axes: expected an axis from 0 to 3 for each rotated pair")
+        if positions is not None and (positions.dim() != 3 or positions.shape[0] <= max(axes)):
+            raise ValueError("positions: expected int32 [axes, batch, tokens]")
+    spots = positions if axes is None or positions is None else positions[0]
+    for name, t in (("positions", spots), ("rows", rows)):
         if t is not None and (t.shape != (B, S) or (S > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{name}: expected int32 [batch, tokens]")
+            raise ValueError(f"{name}: expected int32 [{'axes, ' if t is not rows and axes else ''}batch, tokens]")
     p = make_prep(dict(
         batch=B, seq_len=S, heads=H, kv_heads=G, head_dim=D, rot_dim=0 if cos is None else 2 * cos.shape[1],
         dtype=_dtype_name(q), interleaved=interleaved, norm=norm, eps=eps,
         max_pos=0 if cos is None else cos.shape[0], cache_rows=cap, q_layout=_layout4(q, 2), k_layout=_layout4(k, 2),
         v_layout=_layout4(v, 2), q_out_layout=_layout4(out, 2), k_out_layout=kl, v_out_layout=vl,
-        pos_batch_stride=0 if positions is None else positions.stride(0),
+        pos_batch_stride=0 if spots is None else spots.stride(0),
         row_batch_stride=0 if rows is None else rows.stride(0), kv_dtype="i8" if i8 else None,
         kv_scale="channel" if (k_scale is not None and k_scale.numel() > 1) else "tensor",
         k_scale_ptr=_ptr(k_scale), v_scale_ptr=_ptr(v_scale)))
     with torch.cuda.device(q.device):
         st = torch.cuda.current_stream(q.device).cuda_stream if stream is None else stream
-        _check(attn_qkv_prep(p, pages, _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
-                             _ptr(sin), _ptr(positions), _ptr(rows), _ptr(out), _ptr(k_cache), _ptr(v_cache), st),
-               "attn_qkv_prep")
+        args = (_ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions),
+                _ptr(rows), _ptr(out), _ptr(k_cache), _ptr(v_cache), st)
+        if axes is None:
+            _check(attn_qkv_prep(p, pages, *args), "attn_qkv_prep")
+        else:
+            stride = 0 if positions is None else positions.stride(0)
+            _check(attn_qkv_prep_axes(p, pages, make_axes(axes, stride), *args), "attn_qkv_prep_axes")
     return out
 
 

@@ -424,6 +424,46 @@ int paged_plan(const attn_problem* p, int32_t first_keys) {
   return n < 1 ? 1 : (int)n;
 }
 
+// A problem over the concatenated keys of the prefix and an entry's own.
+Problem with_prefix(Problem r, const attn_prefix* x) {
+  r.prefix = x->rows;
+  r.Sk += x->rows;
+  r.coff = clamp64(r.coff, -(int64_t{1} << 40), int64_t{1} << 40) + x->rows;   // (no row or key index is beyond 2^31)
+  return r;
+}
+
+int check_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* x) {
+  int rc = check_problem(p);
+  if (rc) return rc;
+  if (!x || x->rows < 0 || p->window_left >= 0) return ATTN_ERR_INVALID_ARG;
+  if (x->rows > kMaxFirst || p->k_len > kMaxFirst - x->rows || p->q_len > kMaxFirst) return ATTN_ERR_UNSUPPORTED;
+  if (x->rows > 0 && !x->table) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(x->table, 4)) return ATTN_ERR_ALIGNMENT;
+  return check_pages(pages, p->k_len);
+}
+
+// The CUDA-core pass's plan for a batch with a prefix: parts of each row block's tile list.
+int shared_plan(const attn_problem* p, const attn_prefix* x) {
+  const int64_t rows = (int64_t)p->q_len * (p->heads / p->kv_heads);
+  const int64_t blocks = (int64_t)(p->batch > 0 ? p->batch : 1) * p->kv_heads * ((rows + 15) / 16);
+  int64_t n = (4096 + blocks - 1) / blocks;
+  n = n < 64 ? n : 64;
+  const int64_t tiles = ((int64_t)x->rows + p->k_len + 127) / 128;
+  n = n < tiles ? n : tiles;
+  return n < 1 ? 1 : (int)n;
+}
+
+// Workspace of attn_fwd_shared, whichever pass a call's alignment takes.
+size_t shared_bytes(const attn_problem* p, const attn_prefix* x) {
+  if (p->batch == 0 || p->q_len == 0) return 0;
+  int status = 0;
+  const Problem r = with_prefix(
+      resolve(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, &status), x);
+  const int n = shared_plan(p, x);
+  const size_t a = n > 1 ? sums_ws_bytes(p, n) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
+  return a > b ? a : b;
+}
+
 // Workspace of attn_decode_paged, whichever pass a call's alignment takes.
 size_t paged_bytes(const attn_problem* p, int32_t first_keys) {
   int status = 0;
@@ -603,6 +643,42 @@ int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t fi
   return from_cuda(launch_combine(r, s, p->dtype, st));
 }
 
+size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix) {
+  if (check_shared(p, pages, prefix) != ATTN_OK) return 0;
+  return shared_bytes(p, prefix);
+}
+
+int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix, const void* q,
+                    const void* k_pool, const void* v_pool, void* o, const float* mask, const int32_t* k_lens,
+                    float* lse, void* workspace, size_t workspace_bytes, attn_stream stream) {
+  int rc = check_shared(p, pages, prefix);
+  if (rc) return rc;
+  if (p->batch == 0 || p->q_len == 0) return ATTN_OK;
+  rc = check_pointers(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse);
+  if (rc) return rc;
+  if (prefix->rows > 0 && (!k_pool || !v_pool)) return ATTN_ERR_INVALID_ARG;
+  const size_t need = shared_bytes(p, prefix);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  int* status = nullptr;
+  rc = status_ptr(&status);
+  if (rc) return rc;
+  const Problem r = with_prefix(resolve(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse, status), prefix);
+  const Ext x = make_ext(0, pages, prefix);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p->q_len == 1) {
+    int used = 0;
+    rc = paged_try(r, x, workspace, st, &used);
+    if (rc || used) return rc;
+  }
+  const int n = shared_plan(p, prefix);
+  Split s{1, 1, nullptr, nullptr};
+  if (n > 1) s = split_in(workspace, (size_t)p->batch * p->heads * p->q_len, n, 0, p->head_dim, true);
+  rc = from_cuda(launch_simt_ext(r, x, s, st));
+  if (rc) return rc;
+  return n > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;
+}
+
 int attn_combine(int32_t n_splits, int32_t rows, int32_t head_dim, const float* part_o, const float* part_lse,
                  int32_t out_dtype, void* o, int64_t o_row_stride, float* lse, int32_t masked_rows,
                  attn_stream stream) {
@@ -654,6 +730,6 @@ int attn_test_inject(int32_t fault) {
   return ATTN_OK;
 }
 
-int attn_version(void) { return 260; }
+int attn_version(void) { return 270; }
 
 }  // extern "C"

@@ -26,6 +26,7 @@ struct Problem {
   int64_t coff;                  // causal offset (resolved)
   int masked_zero;
   int window;                    // left window (keys behind the diagonal), -1 = none
+  int prefix;                    // leading keys, of Sk, that every row of every entry sees (visible.cuh)
   int align_klens;               // 1: causal offset of entry b is L_b - Sq
   int klens_plus;                // added to k_lens[b] (1 for last-index lengths)
   float softcap;                 // 0: off; > 0: scores are softcap * tanh(scale q.k / softcap)

@@ -210,7 +210,7 @@ struct Ring {
   uint32_t ring;           // shared-memory address of this warp's stages
   int* key;                // [STAGES] first key of a stage
   uint32_t* vis;           // [STAGES] its visible keys, bit r = row r
-  int units, warp, lane, page;
+  int units, warp, lane, page, page_row;
   bool one_page, same;
 
   __device__ __forceinline__ Ring(const Work& work, const Cursor& at, int n_units, uint8_t* smem, int* keys,
@@ -222,21 +222,23 @@ struct Ring {
     ring = smem_u32(smem) + warp * STAGES * kStage;
     key = keys + warp * STAGES;
     vis = masks + warp * STAGES;
-    one_page = w.x.page_size % KEYS == 0;   // a stage's keys share a page
+    one_page = w.x.page_size % KEYS == 0 && w.x.prefix % KEYS == 0;   // a stage's keys share a page
     same = p.k.bs == p.v.bs && p.k.hs == p.v.hs && p.k.rs == p.v.rs;
     look_up();
   }
   // The page of row lane % KEYS of the next tile.
   __device__ __forceinline__ void look_up() {
     const int k = in.tl.tile(in.tile) * kTile + warp * KEYS + lane % KEYS;
-    page = visible(in.v, k) ? page_of(w.x, in.b, k) : -1;
+    page = -1;
+    page_row = 0;
+    if (visible(in.v, k)) page = page_of(w.x, in.b, k, page_row);
   }
   // Copies the next tile into stage s; with `more` moves on and looks up the pages of the tile behind it.
   __device__ __forceinline__ void issue(int s, bool more) {
     const Problem& p = w.p;
-    const int k0 = in.tl.tile(in.tile) * kTile + warp * KEYS, kr = lane % KEYS;
+    const int k0 = in.tl.tile(in.tile) * kTile + warp * KEYS;
     const uint32_t mask = __ballot_sync(kAll, page >= 0);
-    const int g = in.u / w.n_hc, r = k0 + kr - page_index(w.x, k0 + kr) * w.x.page_size, pg = max(page, 0);
+    const int g = in.u / w.n_hc, r = page_row, pg = max(page, 0);
     const int64_t ko = ((int64_t)pg * p.k.bs + (int64_t)g * p.k.hs + (int64_t)r * p.k.rs) * ES;
     const int64_t vo = same ? ko : ((int64_t)pg * p.v.bs + (int64_t)g * p.v.hs + (int64_t)r * p.v.rs) * ES;
     if (lane == 0) {

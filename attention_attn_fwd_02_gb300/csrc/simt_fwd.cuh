@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
       // Keys of the tile that the CTA reads: visible to some row, and in a page of the pool.
       if (threadIdx.x < kTile) {
         const int kk = t0 + threadIdx.x;
-        const bool here = visible(uv, kk) && (!x.page_size || page_of(x, b, kk) >= 0);
+        int row;
+        const bool here = visible(uv, kk) && (!x.page_size || page_of(x, b, kk, row) >= 0);
         const uint32_t m = __ballot_sync(0xffffffffu, here);
         if (threadIdx.x == 0) s_paged = m;
       }
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_attn_kernel(Problem p, Split
         if constexpr (EXT) {
           here = here && ((tile_keys >> j) & 1u);
           if (here && x.page_size) {
-            const int64_t pg = page_of(x, b, kk);
-            const int r = kk % x.page_size;
+            int r;
+            const int64_t pg = page_of(x, b, kk, r);
             ko = p.k.off + pg * p.k.bs + (int64_t)g * p.k.hs + (int64_t)r * p.k.rs + d;
             vo = p.v.off + pg * p.v.bs + (int64_t)g * p.v.hs + (int64_t)r * p.v.rs + d;
           }

@@ -1,4 +1,5 @@
-// visible.cuh -- key visibility of windows with first keys, and paged caches.
+// visible.cuh -- key visibility of windows with first keys and of shared
+// prefixes, and paged caches.
 //
 // A row's visible keys are [lo, fe) and [wl, hi): the first keys of its span
 // and the keys from its window's left end to its diagonal.  A kernel takes the
@@ -10,7 +11,9 @@
 
 namespace attn {
 
-// First keys and page lists, passed by value next to a Problem.
+// First keys and page lists, passed by value next to a Problem.  With a shared
+// prefix (Problem::prefix) keys 0 .. prefix - 1 of every entry are the rows of
+// prefix_table, and an entry's own rows, in its list of `table`, follow them.
 struct Ext {
   int first;             // first keys visible behind the window
   int page_size;         // 0: K and V are not paged
@@ -19,11 +22,17 @@ struct Ext {
   int64_t table_stride;
   uint32_t div_mul;      // k / page_size = umulhi(k, div_mul) >> div_shift for 0 <= k < 2^31 (page_size > 1)
   int div_shift;
+  int prefix;
+  const int32_t* prefix_table;
 };
 
-inline Ext make_ext(int first, const attn_pages* pages) {
-  Ext x{first, 0, 0u, nullptr, 0, 0u, 0};
+inline Ext make_ext(int first, const attn_pages* pages, const attn_prefix* prefix = nullptr) {
+  Ext x{first, 0, 0u, nullptr, 0, 0u, 0, 0, nullptr};
   if (!pages) return x;
+  if (prefix) {
+    x.prefix = prefix->rows;
+    x.prefix_table = prefix->table;
+  }
   x.page_size = pages->page_size;
   x.n_pages = (uint32_t)pages->n_pages;
   x.table = pages->table;
@@ -48,12 +57,12 @@ struct Vis {
 
 __device__ __forceinline__ Vis row_vis(const Problem& p, int first, int b, int i) {
   int64_t kl = p.Sk;
-  if (p.klens) kl = clamp64((int64_t)p.klens[b] + p.klens_plus, 0, p.Sk);
+  if (p.klens) kl = p.prefix + clamp64((int64_t)p.klens[b] + p.klens_plus, 0, p.Sk - p.prefix);
   int64_t hi = kl, lo = 0, wl = 0;
   if (p.seg) lo = clamp64((int64_t)p.seg[(int64_t)b * p.seg_bs + i], 0, p.Sk);
   if (p.causal) {
     const int64_t diag = (int64_t)i + (p.align_klens ? kl - p.Sq : p.coff);
-    hi = min(hi, max(diag + 1, (int64_t)0));
+    hi = min(hi, max(diag + 1, (int64_t)p.prefix));
     if (p.window >= 0) wl = diag - p.window;
   }
   lo = min(lo, hi);
@@ -106,9 +115,13 @@ __device__ __forceinline__ void list_part(int n, int part, int parts, int& begin
   end = (int)((int64_t)n * (part + 1) / parts);
 }
 
-// Page of key k of entry b, or -1 when the entry's list names no page of the pool there.
-__device__ __forceinline__ int page_of(const Ext& x, int b, int k) {
-  const int32_t pg = __ldg(x.table + (int64_t)b * x.table_stride + page_index(x, k));
+// Page of key k of entry b, or -1 when its list names no page of the pool there; row: the key's row in it.
+__device__ __forceinline__ int page_of(const Ext& x, int b, int k, int& row) {
+  const bool shared = k < x.prefix;
+  if (!shared) k -= x.prefix;
+  const int at = page_index(x, k);
+  row = k - at * x.page_size;
+  const int32_t pg = __ldg((shared ? x.prefix_table : x.table + (int64_t)b * x.table_stride) + at);
   return (uint32_t)pg < x.n_pages ? pg : -1;
 }
 

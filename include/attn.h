@@ -340,6 +340,45 @@ ATTN_API int attn_decode_paged(const attn_problem* p, const attn_pages* pages, i
                                const int32_t* k_lens, float* lse, void* workspace, size_t workspace_bytes,
                                attn_stream stream);
 
+/* A prefix that the entries of a batch share: its keys are in front of every
+ * entry's own.  Prefix row r is row r % page_size of page table[r / page_size]
+ * of the pools that hold the entries' own rows. */
+typedef struct {
+  int32_t rows;           /* keys of the prefix, >= 0 */
+  const int32_t* table;   /* DEVICE int32 [ceil(rows / page_size)]; may be NULL when rows == 0 */
+} attn_prefix;
+
+/* Bytes of device workspace attn_fwd_shared needs; from the shape alone
+ * (batch, heads, q_len, k_len, prefix rows, page size).  0 when it needs none
+ * and for an invalid problem. */
+ATTN_API size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn_pages* pages,
+                                               const attn_prefix* prefix);
+
+/* Attention of a batch whose entries share a prefix, over one paged cache: the
+ * decode step (q_len 1), drafted tokens or prompts (any q_len) of requests
+ * with one long instruction, document, image or video in common.  Entry b's
+ * keys are the prefix->rows keys of the prefix and behind them its own keys,
+ * rows 0 .. L_b - 1 of its list in pages (L_b from k_lens and p->k_len as for
+ * attn_fwd).  Every row sees the whole prefix; own keys are visible as for
+ * attn_fwd, counted from the entry's first own row: all L_b of them without
+ * causal, up to i + off_b with it (a row whose diagonal is in front of the own
+ * keys sees the prefix alone).  The result is that of attn_fwd over the
+ * concatenated keys; the prefix's keys are read once for all entries (short
+ * prefixes and the types named below: once an entry, out of L2).
+ * p->window_left must be -1 (ATTN_ERR_INVALID_ARG).  mask columns are the
+ * concatenated keys: column prefix->rows is an entry's first own row.  List
+ * values outside [0, n_pages) hold no rows, as for attn_decode_paged, in the
+ * prefix's list too.  prefix->rows + p->k_len and q_len are at most 2^30
+ * (ATTN_ERR_UNSUPPORTED); p->key_splits is not used.  Types, int8 pools, score
+ * transforms, masked rows, LSE, determinism and errors as for
+ * attn_decode_paged.  Rows of the pools that no row of their entry (of the
+ * batch, in the prefix) sees are never read into the result; with q_len > 1
+ * the V values of visible keys must be finite (attn_fwd). */
+ATTN_API int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix, const void* q,
+                             const void* k_pool, const void* v_pool, void* o, const float* mask,
+                             const int32_t* k_lens, float* lse, void* workspace, size_t workspace_bytes,
+                             attn_stream stream);
+
 /* The step before attention ("com.microsoft.GroupQueryAttention": rotary
  * embedding with cos / sin caches, half-split or interleaved, and RMS norms
  * of Q and K for each head), with the cache write in the same pass.  For every
@@ -383,6 +422,28 @@ ATTN_API int attn_qkv_prep(const attn_prep* p, const attn_pages* pages, const vo
                            const void* q_weight, const void* k_weight, const float* cos, const float* sin,
                            const int32_t* positions, const int32_t* rows, void* q_out, void* k_out, void* v_out,
                            attn_stream stream);
+
+/* attn_qkv_prep with positions on several axes (time, height and width of an
+ * image's or video's patches): rotated pair j takes its angle at the token's
+ * position on axis axis[j],
+ *   cos, sin = cos[pos_a, j], sin[pos_a, j],  a = axis[j],
+ *   pos_a = positions[a * pos_axis_stride + b * pos_batch_stride + i], clamped to [0, max_pos).
+ * Any assignment of pairs to axes is taken: a stretch of pairs an axis, axes in
+ * turn from pair to pair, halves.  Where an axis has frequencies of its own,
+ * they are the columns of cos and sin that its pairs use. */
+#define ATTN_MAX_AXES 4
+typedef struct {
+  int32_t n_axes;            /* 1 .. ATTN_MAX_AXES */
+  int64_t pos_axis_stride;   /* elements from one axis's positions to the next's, >= 0 */
+  uint8_t axis[128];         /* axis of pair j < rot_dim / 2, below n_axes */
+} attn_axes;
+
+/* Arguments, results and errors as for attn_qkv_prep (positions NULL: position
+ * i on every axis); axes is required. */
+ATTN_API int attn_qkv_prep_axes(const attn_prep* p, const attn_pages* pages, const attn_axes* axes, const void* q,
+                                const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                const float* cos, const float* sin, const int32_t* positions, const int32_t* rows,
+                                void* q_out, void* k_out, void* v_out, attn_stream stream);
 
 /* Size in bytes of the fixed scratch array attn_decode_noalloc uses. */
 ATTN_API size_t attn_decode_noalloc_max_scratch(void);
