@@ -19,6 +19,7 @@
 #include "paged.cuh"
 #include "visible.cuh"
 #include "prep.h"
+#include "shared.h"
 
 namespace attn {
 
@@ -454,14 +455,16 @@ int shared_plan(const attn_problem* p, const attn_prefix* x) {
 }
 
 // Workspace of attn_fwd_shared, whichever pass a call's alignment takes.
-size_t shared_bytes(const attn_problem* p, const attn_prefix* x) {
+size_t shared_bytes(const attn_problem* p, const attn_pages* pages, const attn_prefix* x) {
   if (p->batch == 0 || p->q_len == 0) return 0;
   int status = 0;
   const Problem r = with_prefix(
       resolve(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, &status), x);
   const int n = shared_plan(p, x);
   const size_t a = n > 1 ? sums_ws_bytes(p, n) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
-  return a > b ? a : b;
+  shr::Work w;
+  const size_t c = shared_tc_plan(r, pages->page_size, w) && w.splits > 1 ? sums_ws_bytes(p, w.splits) : 0;
+  return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
 // Workspace of attn_decode_paged, whichever pass a call's alignment takes.
@@ -645,7 +648,7 @@ int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t fi
 
 size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix) {
   if (check_shared(p, pages, prefix) != ATTN_OK) return 0;
-  return shared_bytes(p, prefix);
+  return shared_bytes(p, pages, prefix);
 }
 
 int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix, const void* q,
@@ -657,7 +660,7 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   rc = check_pointers(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse);
   if (rc) return rc;
   if (prefix->rows > 0 && (!k_pool || !v_pool)) return ATTN_ERR_INVALID_ARG;
-  const size_t need = shared_bytes(p, prefix);
+  const size_t need = shared_bytes(p, pages, prefix);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   if (need > 0 && !aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
   int* status = nullptr;
@@ -666,14 +669,23 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   const Problem r = with_prefix(resolve(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse, status), prefix);
   const Ext x = make_ext(0, pages, prefix);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t rows = (size_t)p->batch * p->heads * p->q_len;
+  int used = 0;
+  Split s{1, 1, nullptr, nullptr};
+  shr::Work w;
+  if (shared_tc_plan(r, x.page_size, w)) {
+    if (w.splits > 1) s = split_in(workspace, rows, w.splits, 0, p->head_dim, true);
+    rc = shared_tc_try(r, x, w, s, st, &used);
+    if (rc) return rc;
+    if (used) return w.splits > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;
+  }
   if (p->q_len == 1) {
-    int used = 0;
     rc = paged_try(r, x, workspace, st, &used);
     if (rc || used) return rc;
   }
   const int n = shared_plan(p, prefix);
-  Split s{1, 1, nullptr, nullptr};
-  if (n > 1) s = split_in(workspace, (size_t)p->batch * p->heads * p->q_len, n, 0, p->head_dim, true);
+  s = Split{1, 1, nullptr, nullptr};
+  if (n > 1) s = split_in(workspace, rows, n, 0, p->head_dim, true);
   rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;
   return n > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;

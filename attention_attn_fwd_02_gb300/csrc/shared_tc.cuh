@@ -1,0 +1,733 @@
+// shared_tc.cuh -- f16/bf16 attention of a batch over a shared prefix and each
+// entry's own keys in a paged cache, head_dim 64 or 128, on the tensor cores.
+//
+// What it computes: O = softmax(scale Q K^T + mask) V and the LSE over the
+// prefix's keys and the entry's own ones, or partial results of both that are
+// merged by their maxima and sums.
+//
+// What bounds it: HBM for one token an entry, as a key tile of 128 x head_dim
+// is read once for up to 256 rows of all entries (64 entries of 4 heads a kv
+// head fill both row tiles); the tensor cores and the exponentials, as in the
+// prefill kernel, once the rows are prompts.
+//
+// The tile step is the windowed kernel's (window_tc.cuh): a persistent CTA an
+// SM, two 128-row tiles that ping-pong, S = Q K^T and O += P V as tcgen05 MMAs
+// with TMEM accumulators, a thread to a row of S, P over S as packed pairs, a
+// reference maximum that moves with a slack.  What is its own:
+//   - a block of one row tile deals its key tiles to both row tiles of the
+//     kernel in turn, so that one's softmax overlaps the other's products;
+//   - K and V tiles are put together from a page list: the copy warp's lanes
+//     look up a page each, a tile ahead, and issue a TMA box of `piece` rows and
+//     64 columns each.  A piece without a page is copied from a page behind the
+//     pool: it arrives as zeros and counts its bytes;
+//   - Q rows come from wherever (entry, query, head) puts them: each softmax
+//     thread loads its own row of the next item while the tensor cores finish
+//     the current one's, so rows pack without gaps whatever the strides.
+// P enters the product as one value of the element type, as in attn_fwd.
+#pragma once
+
+#include <type_traits>
+
+#include "prefill_tc.h"
+#include "shared.h"
+#include "tc_ptx.cuh"
+#include "tma.h"
+
+namespace attn {
+namespace shr {
+
+using namespace tc;
+
+constexpr int BM = kRows;
+constexpr int BN = kKeys;
+constexpr int kThreads = 384;
+// Registers after the split, as in the prefill kernel: 8 warps x 216 and 4
+// warps x 56 fit the 168 a thread that the block is launched with.
+constexpr int kSoftmaxRegs = 216;
+constexpr int kProducerRegs = 56;
+constexpr int kSplitRegs = 8 * 32 * kSoftmaxRegs + 4 * 32 * kProducerRegs;
+static_assert(kSplitRegs <= kThreads * ((65536 / kThreads) & ~7), "register split exceeds the block's registers");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kSlack = 8.0f;     // log2 units
+constexpr int kNotes = 8;          // key tiles whose pages are noted: stages + 3 at least (see the copy warp)
+
+// A row block's part of its tile list, as the roles read it.
+struct Item {
+  int b, g;              // b < 0: a prefix item
+  int row0, rows;        // first row, and the rows there are
+  int t0, np, o0, n;     // np prefix tiles from t0, then n - np own tiles from o0
+  int n0;                // the tiles of row tile 0: the first n0 (not alt)
+  int own_end;           // own keys that some row of the block sees
+  int alt, some1, slot;  // key tiles in turn; row tile 1 has rows; first partial result
+  __device__ __forceinline__ bool has(int t, int i) const {
+    return alt ? (i & 1) == t : t ? some1 != 0 : i < n0;
+  }
+};
+
+struct Bars {
+  uint64_t q_full[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t item_full[2], item_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;                  // 64-column (128-byte) chunks
+  static constexpr int kStages = D <= 64 ? 4 : 2;
+  static constexpr int kQTile = BM * D * 2;               // bytes
+  static constexpr int kKTile = BN * D * 2;
+  static constexpr int kSmem = 2 * kQTile + 2 * kStages * kKTile;
+  static constexpr int kS0 = 0, kS1 = BN, kO0 = 2 * BN, kO1 = 2 * BN + D;
+  static_assert(2 * BN + 2 * D <= 512, "TMEM budget");
+  static_assert(kNotes >= kStages + 3, "notes of key tiles");
+};
+
+// The lowest n bits (n may lie outside [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// 32 bytes to global memory in one store (32-byte aligned).
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Own keys that row i of entry b sees: the first ones, up to its diagonal.
+__device__ __forceinline__ int own_seen(const Problem& p, int b, int i) { return row_vis(p, 0, b, i).hi - p.prefix; }
+
+// XF: scores under a mask, a softcap or a scale that is not positive.
+template <int D, bool BF16, bool XF>
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const Problem p, const Ext x, const Work w, const int wide_rows, const int drop_first_copy,
+                     const Split sp) {
+  using C = Cfg<D>;
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_s = smem;
+  uint8_t* k_s = q_s + 2 * C::kQTile;
+  uint8_t* v_s = k_s + C::kStages * C::kKTile;
+  __shared__ Bars sb;
+  __shared__ Item items[2];
+  __shared__ uint32_t no_page[kNotes];   // of a key tile: which of its pieces have no page
+
+  using S = Scores<XF>;   // (masks come with XF)
+  constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
+  // A row's reference is a maximum, less a lead where P is f16: p is 2^5 at that maximum, and what f16 cannot hold
+  // (2^-25) is 2^-30 of the row's largest probability (window_tc.cuh).
+  constexpr float kLead = (BF16 ? 0.f : 5.f) * (XF ? kLn2 : 1.f);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int my_items = (w.n_items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    sb.abort = 0;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sb.k_full[s], 1);
+      mbar_init(&sb.k_empty[s], 1);
+      mbar_init(&sb.v_full[s], 1);
+      mbar_init(&sb.v_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sb.q_full[i], BM);
+      mbar_init(&sb.s_full[i], 1);
+      mbar_init(&sb.p_full[i], BM);
+      mbar_init(&sb.o_done[i], 1);
+      mbar_init(&sb.item_full[i], 32);
+      mbar_init(&sb.item_empty[i], 2 + 2 * BM);   // the copy and MMA warps and every softmax thread
+    }
+    mbar_init(&sb.mma_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&sb.tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sb.tmem_base;
+
+  if (warp == 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    // ---------------- items ----------------
+    for (int k = 0; k < my_items; ++k) {
+      const int buf = k & 1;
+      if (k >= 2 && !wait_warp(&sb.item_empty[buf], (uint32_t)((k >> 1) - 1) & 1u, &sb.abort, p.status)) break;
+      const int id = (int)blockIdx.x + k * (int)gridDim.x;
+      const int all = p.prefix / BN + (p.prefix % BN > 0);   // the prefix's tiles
+      Item it;
+      int i0, i1;
+      if (id < w.n_a) {   // the blocks of a part side by side: they read the same keys
+        const int blk = id % w.blocks_a, rest = id / w.blocks_a, part = rest / p.G;
+        it.b = -1;
+        it.g = rest % p.G;
+        it.row0 = blk * 2 * BM;
+        it.rows = p.B * p.Sq * p.qpg;
+        it.own_end = 0;
+        it.alt = w.alt_a;
+        it.slot = part << w.alt_a;
+        list_part(all, part, w.parts_a, i0, i1);
+        it.t0 = i0;
+        it.np = it.n = it.n0 = i1 - i0;
+        it.o0 = 0;
+      } else {   // the last row blocks, which see the most keys, first
+        int rest = id - w.n_a;
+        const int part = rest % w.parts_b;
+        rest /= w.parts_b;
+        it.g = rest % p.G;
+        rest /= p.G;
+        it.b = rest % p.B;
+        const int blk = w.blocks_b - 1 - rest / p.B;
+        it.row0 = blk * 2 * BM;
+        it.rows = p.Sq * p.qpg;
+        it.own_end = own_seen(p, it.b, (min(it.row0 + 2 * BM, it.rows) - 1) / p.qpg);
+        const int end0 = own_seen(p, it.b, (min(it.row0 + BM, it.rows) - 1) / p.qpg);
+        it.alt = w.alt_b;
+        it.slot = (w.parts_a << w.alt_a) + (part << w.alt_b);
+        const int np = w.joined ? all : 0;
+        list_part(np + (it.own_end + BN - 1) / BN, part, w.parts_b, i0, i1);
+        it.t0 = min(i0, np);
+        it.np = min(i1, np) - it.t0;
+        it.o0 = max(i0 - np, 0);
+        it.n = i1 - i0;
+        it.n0 = min(max(np + (end0 + BN - 1) / BN - i0, 0), it.n);
+      }
+      it.some1 = it.row0 + BM < it.rows;
+      if (lane == 0) items[buf] = it;
+      __syncwarp();
+      mbar_arrive(&sb.item_full[buf]);
+    }
+  } else if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    // ---------------- copies: every lane a piece of a tile ----------------
+    const int pieces = BN / w.piece;   // 1 .. 16
+    const int piece = lane % pieces, chunk = lane / pieces;
+    const bool copies = chunk < C::kChunks;
+    const int at = chunk * BN * 128 + piece * w.piece * 128;
+    // This lane's piece of tile i of an item: its page (n_pages: none) and row in it.
+    auto look_up = [&](const Item& it, int i, int& row) {
+      const bool pre = i < it.np;
+      const int r = (pre ? it.t0 + i : it.o0 + i - it.np) * BN + piece * w.piece;
+      row = 0;
+      if (r >= (pre ? p.prefix : it.own_end)) return (int)x.n_pages;   // behind the last key: not masked as a missing page
+      const int pi = page_index(x, r);
+      row = r - pi * x.page_size;
+      const int32_t pg = __ldg((pre ? x.prefix_table : x.table + (int64_t)it.b * x.table_stride) + pi);
+      return (uint32_t)pg < x.n_pages ? (int)pg : -1;
+    };
+    int gt = 0;        // tiles whose K and V copies were issued
+    int k_only = -1;   // a tile whose K copy was issued but not its V copy
+    bool ok = true;
+    for (int k = 0; ok && k < my_items; ++k) {
+      const int buf = k & 1;
+      if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
+      const Item& it = items[buf];
+      const int n = it.n, g = it.g;
+      int row = 0, page = 0;
+      if (n > 0) page = look_up(it, 0, row);
+      for (int i = 0; i < n; ++i) {
+        const int s = gt % C::kStages;
+        const uint32_t ph = (uint32_t)(gt / C::kStages) & 1u;
+        const uint32_t missing = __ballot_sync(0xffffffffu, page < 0 && chunk == 0);
+        const int pg = page < 0 ? (int)x.n_pages : page, prow = row;
+        if (i + 1 < n) page = look_up(it, i + 1, row);   // arrives while this tile waits for its stage
+        if (!(ok = wait_warp(&sb.k_empty[s], ph ^ 1u, &sb.abort, p.status))) break;
+        if (lane == 0) {
+          // Slot gt % kNotes was read for tile gt - kNotes: S of tile gt - kStages is done, which followed the row
+          // tiles' reading of the notes up to tile gt - kStages - 3.
+          no_page[gt % kNotes] = missing;
+          mbar_expect_tx(&sb.k_full[s], C::kKTile);
+        }
+        __syncwarp();
+        // Test hook (attn_test_inject): the first CTA's first K copy is
+        // announced but never issued, so the MMA warp's wait runs out.
+        const bool dropped = drop_first_copy && gt == 0 && blockIdx.x == 0;
+        if (copies && !dropped) tma_load_4d(k_s + s * C::kKTile + at, &tm_k, &sb.k_full[s], chunk * 64, prow, g, pg);
+        if (!(ok = wait_warp(&sb.v_empty[s], ph ^ 1u, &sb.abort, p.status))) {
+          k_only = gt;
+          break;
+        }
+        if (lane == 0) mbar_expect_tx(&sb.v_full[s], C::kKTile);
+        __syncwarp();
+        if (copies) tma_load_4d(v_s + s * C::kKTile + at, &tm_v, &sb.v_full[s], chunk * 64, prow, g, pg);
+        ++gt;
+      }
+      if (ok && lane == 0) mbar_arrive(&sb.item_empty[buf]);
+    }
+    // Copies still in flight land before the CTA can exit.  Earlier copies
+    // completed before their stage was refilled.
+    if (lane == 0) {
+      for (int i = gt > C::kStages ? gt - C::kStages : 0; i < gt; ++i) {
+        const int s = i % C::kStages;
+        const uint32_t ph = (uint32_t)(i / C::kStages) & 1u;
+        drain_bar(&sb.k_full[s], ph, p.status);
+        drain_bar(&sb.v_full[s], ph, p.status);
+      }
+      if (k_only >= 0) drain_bar(&sb.k_full[k_only % C::kStages], (uint32_t)(k_only / C::kStages) & 1u, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    // ---------------- MMA issuer (warp-wide; one elected lane issues) ----------------
+    constexpr uint32_t kIdQK = idesc_f16(BF16, false, BM, BN);
+    constexpr uint32_t kIdPV = idesc_f16(BF16, true, BM, D);
+    const uint32_t q_addr = su32(q_s), k_addr = su32(k_s), v_addr = su32(v_s);
+    const uint64_t qd0 = sdesc(q_addr, 16, 1024), qd1 = sdesc(q_addr + C::kQTile, 16, 1024);
+    const uint64_t kd0 = sdesc(k_addr, 16, 1024), vd0 = sdesc(v_addr, BN * 128, 1024);
+    auto issue_qk = [&](int tt, int s) {
+      fence_after();
+      const uint64_t ad = tt ? qd1 : qd0;
+      const uint64_t bd0 = sdesc_add(kd0, (uint32_t)(s * C::kKTile));
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t a = sdesc_add(ad, (uint32_t)((kk / 4) * BM * 128 + (kk % 4) * 32));
+        const uint64_t bd = sdesc_add(bd0, (uint32_t)((kk / 4) * BN * 128 + (kk % 4) * 32));
+        mma_ss_w(tmem + (tt ? C::kS1 : C::kS0), a, bd, kIdQK, kk > 0);
+      }
+      mma_commit_w(&sb.s_full[tt]);
+    };
+    auto issue_pv = [&](int tt, int s, bool start) {
+      fence_after();
+      const uint64_t bd0 = sdesc_add(vd0, (uint32_t)(s * C::kKTile));
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk) {
+        const uint64_t bd = sdesc_add(bd0, (uint32_t)(kk * 16 * 128));
+        mma_ts_w(tmem + (tt ? C::kO1 : C::kO0), tmem + (tt ? C::kS1 : C::kS0) + kk * 8, bd, kIdPV,
+                 (!start || kk > 0) ? 1u : 0u);
+      }
+      mma_commit_w(&sb.o_done[tt]);
+    };
+    // Zeroes the V rows of a tile's keys that no row of the item sees (they may hold anything).
+    auto clear_tail = [&](const Item& it, int i, int s) {
+      const bool pre = i < it.np;
+      const int seen = (pre ? p.prefix - (it.t0 + i) * BN : it.own_end - (it.o0 + i - it.np) * BN);
+      if (seen >= BN) return;
+      for (int u = seen * (C::kChunks * 8) + lane; u < BN * (C::kChunks * 8); u += 32) {
+        const int row = u / (C::kChunks * 8), rest = u % (C::kChunks * 8);
+        *reinterpret_cast<uint4*>(v_s + s * C::kKTile + (rest / 8) * BN * 128 + row * 128 + (rest % 8) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    int gt = 0, c0 = 0, c1 = 0;   // tiles, and P V steps of each row tile so far
+    bool ok = true, issued = false;
+    auto k_ready = [&](int j) {
+      return wait_warp(&sb.k_full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, &sb.abort, p.status);
+    };
+    for (int k = 0; ok && k < my_items; ++k) {
+      const int buf = k & 1;
+      if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
+      const Item& it = items[buf];
+      const int n = it.n;
+      // (every phase of both, also where a row tile has nothing to do: a phase left out would be taken for the next)
+      if (!(ok = wait_warp(&sb.q_full[0], (uint32_t)k & 1u, &sb.abort, p.status))) break;
+      if (!(ok = wait_warp(&sb.q_full[1], (uint32_t)k & 1u, &sb.abort, p.status))) break;
+      if (n > 0) {
+        issued = true;
+        bool start0 = true, start1 = true;
+        if (it.alt) {
+          // Tile i belongs to row tile i % 2: P V of tile i, then S of tile i + 2.
+          for (int i = 0; i < 2 && i < n; ++i) {
+            if (!(ok = k_ready(gt + i))) break;
+            issue_qk(i, (gt + i) % C::kStages);
+            mma_commit_w(&sb.k_empty[(gt + i) % C::kStages]);
+          }
+          if (!ok) break;
+          for (int i = 0; i < n; ++i, ++gt) {
+            const int s = gt % C::kStages, t = i & 1;
+            const uint32_t ph = (uint32_t)(gt / C::kStages) & 1u;
+            if (!(ok = wait_warp(&sb.v_full[s], ph, &sb.abort, p.status))) break;
+            clear_tail(it, i, s);
+            if (!(ok = wait_warp(&sb.p_full[t], (uint32_t)(t ? c1 : c0) & 1u, &sb.abort, p.status))) break;
+            issue_pv(t, s, t ? start1 : start0);
+            mma_commit_w(&sb.v_empty[s]);
+            if (t) {
+              start1 = false;
+              ++c1;
+            } else {
+              start0 = false;
+              ++c0;
+            }
+            if (i + 2 < n) {
+              if (!(ok = k_ready(gt + 2))) break;
+              issue_qk(t, (gt + 2) % C::kStages);
+              mma_commit_w(&sb.k_empty[(gt + 2) % C::kStages]);
+            }
+          }
+        } else {
+          const int n0 = it.n0;
+          const bool some1 = it.some1 != 0;
+          if (!(ok = k_ready(gt))) break;
+          if (n0 > 0) issue_qk(0, gt % C::kStages);
+          if (some1) issue_qk(1, gt % C::kStages);
+          mma_commit_w(&sb.k_empty[gt % C::kStages]);
+          bool rv = mbar_test(&sb.v_full[gt % C::kStages], (uint32_t)(gt / C::kStages) & 1u);   // the next V landed?
+          for (int i = 0; i < n; ++i, ++gt) {
+            const int s = gt % C::kStages, s1 = (gt + 1) % C::kStages;
+            const uint32_t ph = (uint32_t)(gt / C::kStages) & 1u, ph1 = (uint32_t)((gt + 1) / C::kStages) & 1u;
+            const bool more = i + 1 < n, has0 = i < n0;
+            const bool rp0 = !has0 || mbar_test(&sb.p_full[0], (uint32_t)c0 & 1u);
+            if (!(ok = wait_ready(rv, &sb.v_full[s], ph, &sb.abort, p.status))) break;
+            clear_tail(it, i, s);
+            const bool rk = !more || mbar_test(&sb.k_full[s1], ph1);
+            // Row tile 0: P0 V, then the next S0.  (P of an item's first tile
+            // follows the threads' reading of the previous item's O, so O may be
+            // overwritten.)
+            if (has0) {
+              if (!(ok = wait_ready(rp0, &sb.p_full[0], (uint32_t)c0 & 1u, &sb.abort, p.status))) break;
+              issue_pv(0, s, start0);
+              start0 = false;
+              ++c0;
+            }
+            const bool rp1 = !some1 || mbar_test(&sb.p_full[1], (uint32_t)c1 & 1u);
+            if (more) {
+              if (!(ok = wait_ready(rk, &sb.k_full[s1], ph1, &sb.abort, p.status))) break;
+              if (i + 1 < n0) issue_qk(0, s1);
+            }
+            rv = more && mbar_test(&sb.v_full[s1], ph1);
+            // Row tile 1: P1 V, then the next S1.
+            if (some1) {
+              if (!(ok = wait_ready(rp1, &sb.p_full[1], (uint32_t)c1 & 1u, &sb.abort, p.status))) break;
+              issue_pv(1, s, start1);
+              start1 = false;
+              ++c1;
+            }
+            mma_commit_w(&sb.v_empty[s]);
+            if (more) {
+              if (some1) issue_qk(1, s1);
+              mma_commit_w(&sb.k_empty[s1]);
+            }
+          }
+        }
+      }
+      if (ok && lane == 0) mbar_arrive(&sb.item_empty[buf]);
+      __syncwarp();
+    }
+    // Every MMA issued above has completed before TMEM is freed.
+    if (issued) {
+      mma_commit_w(&sb.mma_done);
+      if (lane == 0) drain_bar(&sb.mma_done, 0, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ---------------- softmax: one thread per query row ----------------
+    const int t = warp / 4, r = (warp % 4) * 32 + lane;   // row tile, row in it = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp % 4) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_off + (t ? C::kS1 : C::kS0);
+    const uint32_t o_tm = tmem + lane_off + (t ? C::kO1 : C::kO0);
+    const float sc = p.scale * kLog2e;
+    const bool capped = XF && p.softcap > 0.f;
+    const float kinv = capped ? p.scale / p.softcap : 0.f;
+    const float c_eff = XF ? 1.f : sc;   // of a value in x, to the units of m_ref
+    uint32_t xs[BN];
+    // This thread's row of an item: entry, query and head (false: there is none).
+    auto row_of = [&](const Item& it, int& b, int& i, int& h) {
+      const int row = it.row0 + (it.alt ? r : t * BM + r);
+      if (row >= it.rows) {
+        b = i = h = 0;
+        return false;
+      }
+      const int q = row / p.qpg;
+      h = it.g * p.qpg + row - q * p.qpg;
+      b = it.b;
+      i = q;
+      if (it.b < 0) {
+        b = q / p.Sq;
+        i = q - b * p.Sq;
+      }
+      return true;
+    };
+    // Loads this thread's query row into its place of the tile (128-byte swizzle); zeros for a row that is not.
+    auto load_q = [&](const Item& it) {
+      int b, i, h;
+      const bool here = row_of(it, b, i, h);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.Q) + p.q.off + (int64_t)b * p.q.bs +
+                                                        (int64_t)h * p.q.hs + (int64_t)i * p.q.rs);
+      uint4 v[D / 8];
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) v[u] = here ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u)
+        *reinterpret_cast<uint4*>(q_s + t * C::kQTile + (u / 8) * BM * 128 + r * 128 + (((u % 8) ^ (r & 7)) << 4)) = v[u];
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&sb.q_full[t]);
+    };
+    int j = 0;    // key tiles so far
+    int gt = 0;   // key tiles of the items so far
+    bool ok = my_items > 0 && wait_warp(&sb.item_full[0], 0u, &sb.abort, p.status);
+    if (ok) load_q(items[0]);
+    for (int k = 0; ok && k < my_items; ++k) {
+      const int buf = k & 1;
+      const Item& it = items[buf];   // (its phase was waited for with the queries)
+      const int n = it.n;
+      int b, qi, h;
+      const bool valid = row_of(it, b, qi, h);
+      const bool idle = !__any_sync(0xffffffffu, valid);   // no row of this warp exists: its P is not used
+      // Keys of the prefix and own keys that the row sees; a row that does not exist hides nothing.
+      const int seen_pre = valid ? p.prefix : 0x7fffffff;
+      const int seen_own = !valid ? 0x7fffffff : it.b < 0 ? 0 : own_seen(p, b, qi);
+      const float* mrow = nullptr;
+      if (XF && p.M && valid)
+        mrow = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)h * p.m.hs + (int64_t)qi * p.m.rs;
+      float m_ref = -INFINITY, l = 0.f;
+      int done = 0;
+      for (int i = 0; i < n; ++i) {
+        if (!it.has(t, i)) continue;
+        if (!(ok = wait_warp(&sb.s_full[t], (uint32_t)j & 1u, &sb.abort, p.status))) break;
+        fence_after();
+        const bool pre = i < it.np;
+        const int k0 = (pre ? it.t0 + i : it.o0 + i - it.np) * BN;
+        const int seen_n = (pre ? seen_pre : seen_own) - k0;   // the row sees the tile's first seen_n keys
+        const uint32_t missing = no_page[(gt + i) % kNotes];
+        // Which of columns 32 c .. of the tile the row sees.
+        auto seen_bits = [&](int c) {
+          uint32_t bits = low_bits(seen_n - 32 * c);
+          if (missing)
+            for (int q = 0; q < 32; q += min(w.piece, 32))
+              if ((missing >> ((32 * c + q) / w.piece)) & 1u) bits &= ~(low_bits(w.piece) << q);
+          return bits;
+        };
+        bool rescale = false;
+        float corr = 1.f;
+        // With a finite reference maximum P is computed against it without
+        // scanning for the tile's maximum; a row whose tile sum reaches kLagMax
+        // makes the warp redo the tile with the scan.
+        constexpr float kLagMax = BF16 ? 0x1p64f : 65504.f;   // (no p of f16 overflows below)
+        if (!idle) {
+          bool scan = __any_sync(0xffffffffu, !(m_ref > -INFINITY));
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            if constexpr (XF) {
+              const float* mk = mrow ? mrow + (pre ? 0 : p.prefix) + k0 : nullptr;
+#pragma unroll
+              for (int c = 0; c < BN / 32; ++c) {
+                const uint32_t seen = seen_bits(c);
+                tmem_ld32(s_tm + c * 32, xs + c * 32);
+                tmem_ld_wait_regs<1>(xs + c * 32);
+#pragma unroll
+                for (int e = c * 32; e < c * 32 + 32; ++e) {
+                  float v = -INFINITY;
+                  if ((seen >> (e % 32)) & 1u) {
+                    const float s = __uint_as_float(xs[e]);
+                    v = capped ? p.softcap * tanh_exp2(s * kinv) : s * p.scale;
+                    if (mk) v += mk[e];
+                  }
+                  xs[e] = __float_as_uint(v);
+                  if ((e & 7) == 7) asm volatile("" ::: "memory");  // at most 8 mask loads in flight
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_tm + c * 32, xs + c * 32);
+              tmem_ld_wait_regs<BN / 32>(xs);
+              if (seen_n < BN || missing) {   // hide by bits, one select a column
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) {
+                  const uint32_t seen = seen_bits(c);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!(seen & (1u << e))) xs[c * 32 + e] = __float_as_uint(-INFINITY);
+                }
+              }
+            }
+            if (scan) {
+              float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < BN; e += 4) {
+                mx0 = max3(mx0, __uint_as_float(xs[e]), __uint_as_float(xs[e + 1]));
+                mx1 = max3(mx1, __uint_as_float(xs[e + 2]), __uint_as_float(xs[e + 3]));
+              }
+              float mt = fmaxf(mx0, mx1) * c_eff;
+              const bool raise = mt - m_ref > kRise;      // also true for the first tile with a visible key
+              mt -= kLead;
+              if (raise) corr = S::weight(m_ref, mt);     // 0 when m_ref = -inf
+              rescale = raise && m_ref > -INFINITY;       // O holds earlier tiles' sums
+              if (raise) {
+                l *= corr;
+                m_ref = mt;
+              }
+            }
+            const float neg = -(m_ref == -INFINITY ? 0.f : m_ref);
+            const uint64_t c2 = f2u(c_eff, c_eff), n2 = f2u(neg, neg);
+            float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < BN; e += 4) {
+              float a0, a1, b0, b1;
+              fma2(a0, a1, __uint_as_float(xs[e]), __uint_as_float(xs[e + 1]), c2, n2);
+              fma2(b0, b1, __uint_as_float(xs[e + 2]), __uint_as_float(xs[e + 3]), c2, n2);
+              if constexpr (XF) {   // natural differences
+                fma2(a0, a1, a0, a1, f2u(kLog2e, kLog2e), 0);
+                fma2(b0, b1, b0, b1, f2u(kLog2e, kLog2e), 0);
+              }
+              a0 = ex2(a0);
+              a1 = ex2(a1);
+              b0 = ex2(b0);
+              b1 = ex2(b1);
+              add2(la0, la1, a0, a1);
+              add2(lb0, lb1, b0, b1);
+              xs[e / 2] = pack2<BF16>(a0, a1);
+              xs[e / 2 + 1] = pack2<BF16>(b0, b1);
+            }
+            const float lt = (la0 + la1) + (lb0 + lb1);
+            if (scan || !__any_sync(0xffffffffu, lt >= kLagMax)) {   // NaN sums stay (a NaN row)
+              l += lt;
+              break;
+            }
+            scan = true;
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) tmem_st32(s_tm + c * 32, xs + c * 32);
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          // P V of the previous tile must have landed in O before it is scaled.
+          if (!(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
+          fence_after();
+          const float f = rescale ? corr : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_tm + c * 32, o);
+            tmem_ld_wait_regs<1>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(o_tm + c * 32, o);
+          }
+        }
+        tmem_st_wait();
+        fence_before();
+        mbar_arrive(&sb.p_full[t]);
+        ++j;
+        ++done;
+      }
+      if (!ok) break;
+      gt += n;
+      // The next item's queries: this row tile's last S, whose phase was waited for above, was its queries' last use.
+      if (k + 1 < my_items) {
+        if (!(ok = wait_warp(&sb.item_full[buf ^ 1], (uint32_t)((k + 1) >> 1) & 1u, &sb.abort, p.status))) break;
+        load_q(items[buf ^ 1]);
+      }
+      // ---- epilogue: O / l, special rows, LSE ----
+      if (done > 0 && !(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
+      fence_after();
+      const bool split = w.splits > 1;
+      // The sink logit joins the denominator (and rescales the accumulated O); with parts the merge adds it once.
+      float M = S::natural(m_ref);
+      const float o_mul = p.sink_on && !split && valid ? fold_sink<false>(M, l, sink_logit(p, h)) : 1.f;
+      const bool hidden_row = (l == 0.f);         // no visible key; a NaN l stays a NaN row
+      const float inv = o_mul / l;
+      const float fill = p.masked_zero ? 0.f : NAN;
+      T* orow = static_cast<T*>(p.O) + p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs + (int64_t)qi * p.o.rs;
+      const int64_t prow = (((int64_t)b * p.H + h) * p.Sq + qi) * w.splits + it.slot + (it.alt ? t : 0);
+      float* po = split ? sp.part_o + prow * D : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (done > 0) {
+          tmem_ld32(o_tm + c * 32, o);
+          tmem_ld_wait_regs<1>(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (split) {
+          if (valid && !hidden_row) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store32(po + c * 32 + e, o + e);
+          }
+        } else {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float a = hidden_row ? fill : __uint_as_float(o[e]) * inv;
+            const float bb = hidden_row ? fill : __uint_as_float(o[e + 1]) * inv;
+            y[e / 2] = pack2<BF16>(a, bb);
+          }
+          if (valid) {
+            if (wide_rows) {
+              store32(orow + c * 32, y);
+              store32(orow + c * 32 + 16, y + 8);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+              for (int v4 = 0; v4 < 4; ++v4)
+                dst[v4] = make_uint4(y[4 * v4], y[4 * v4 + 1], y[4 * v4 + 2], y[4 * v4 + 3]);
+            }
+          }
+        }
+      }
+      if (valid) {
+        if (split) {
+          sp.part_lse[prow] = hidden_row ? -INFINITY : M;
+          sp.part_l[prow] = l;
+        } else if (p.lse) {
+          p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + qi] = hidden_row ? -INFINITY : S::lse(M, __log2f(l));
+        }
+      }
+      fence_before();   // O's loads come before the next item's P, and so before its P V
+      mbar_arrive(&sb.item_empty[buf]);
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ---- host side -----------------------------------------------------------------------
+
+template <int D, bool BF16, bool XF>
+int launch(const Problem& p, const Ext& x, const Work& w, const Split& sp, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!tma_map_bhsd(&mk, p.K, p.dtype, D, x.page_size, p.G, (int)x.n_pages, p.k, w.piece) ||
+      !tma_map_bhsd(&mv, p.V, p.dtype, D, x.page_size, p.G, (int)x.n_pages, p.v, w.piece))
+    return -1;  // not describable: caller falls back
+  const int smem = Cfg<D>::kSmem + 1024;
+  auto kern = shared_tc_kernel<D, BF16, XF>;
+  // setmaxnreg.inc waits until the block's register pool holds the larger
+  // count, so the pool the kernel is launched with must cover the split.
+  static const bool regs_ok = [] {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, (const void*)shared_tc_kernel<D, BF16, XF>) != cudaSuccess) return false;
+    return a.numRegs * kThreads >= kSplitRegs;
+  }();
+  if (!regs_ok) return -1;
+  if (ensure_smem((const void*)kern, smem) != cudaSuccess) return ATTN_ERR_CUDA;
+  // Rows of O on 32-byte boundaries take 32-byte stores.
+  auto even = [](int64_t stride, int64_t extent) { return extent <= 1 || stride % 16 == 0; };
+  const int wide = ((uintptr_t)p.O + (uintptr_t)p.o.off * 2) % 32 == 0 && even(p.o.bs, p.B) && even(p.o.hs, p.H) &&
+                           even(p.o.rs, p.Sq)
+                       ? 1
+                       : 0;
+  const int drop = take_injection() == ATTN_INJECT_DROP_FIRST_COPY ? 1 : 0;
+  kern<<<(unsigned)(w.n_items < kSms ? w.n_items : kSms), kThreads, smem, st>>>(mk, mv, p, x, w, wide, drop, sp);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D>
+int launch_d(const Problem& p, const Ext& x, const Work& w, const Split& sp, cudaStream_t st) {
+  const bool xf = p.M != nullptr || p.softcap > 0.f || !(p.scale * kLog2e > 0.f);
+  if (p.dtype == ATTN_BF16)
+    return xf ? launch<D, true, true>(p, x, w, sp, st) : launch<D, true, false>(p, x, w, sp, st);
+  return xf ? launch<D, false, true>(p, x, w, sp, st) : launch<D, false, false>(p, x, w, sp, st);
+}
+
+}  // namespace shr
+}  // namespace attn
