@@ -433,6 +433,15 @@ Problem with_prefix(Problem r, const attn_prefix* x) {
   return r;
 }
 
+// The problem of the entries' own keys alone.
+Problem own_problem(Problem r) {
+  r.Sk -= r.prefix;
+  r.coff -= r.prefix;
+  r.m.off += r.prefix;
+  r.prefix = 0;
+  return r;
+}
+
 int check_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* x) {
   int rc = check_problem(p);
   if (rc) return rc;
@@ -463,7 +472,11 @@ size_t shared_bytes(const attn_problem* p, const attn_pages* pages, const attn_p
   const int n = shared_plan(p, x);
   const size_t a = n > 1 ? sums_ws_bytes(p, n) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
   shr::Work w;
-  const size_t c = shared_tc_plan(r, pages->page_size, w) && w.splits > 1 ? sums_ws_bytes(p, w.splits) : 0;
+  size_t c = 0;
+  if (shared_tc_plan(r, pages->page_size, w) && w.splits > 1) {
+    c = sums_ws_bytes(p, w.splits);
+    if (p->q_len == 1) c += paged_own_bytes(own_problem(r), w.own_sms);   // behind the partial results
+  }
   return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
@@ -675,9 +688,9 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   shr::Work w;
   if (shared_tc_plan(r, x.page_size, w)) {
     if (w.splits > 1) s = split_in(workspace, rows, w.splits, 0, p->head_dim, true);
-    rc = shared_tc_try(r, x, w, s, st, &used);
-    if (rc) return rc;
-    if (used) return w.splits > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;
+    void* ws_own = static_cast<char*>(workspace) + sums_ws_bytes(p, w.splits);   // (used with one query an entry)
+    rc = shared_tc_try(r, x, w, s, own_problem(r), make_ext(0, pages), ws_own, st, &used);
+    if (rc || used) return rc;
   }
   if (p->q_len == 1) {
     rc = paged_try(r, x, workspace, st, &used);

@@ -27,6 +27,16 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 size_t rows_of(const Work& w) { return (size_t)w.ctas * 2 * w.heads; }
 size_t sums_bytes(const Work& w) { return round256(rows_of(w) * 2 * sizeof(float)); }   // part_m and part_l
 
+size_t parts_bytes(const Work& w) { return round256(rows_of(w) * w.p.D * sizeof(float)) + sums_bytes(w); }
+
+// Lays the fragments' arrays out in a workspace; returns what is behind them.
+char* lay_out(Work& w, void* workspace) {
+  w.part_o = static_cast<float*>(workspace);
+  w.part_m = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(rows_of(w) * w.p.D * sizeof(float)));
+  w.part_l = w.part_m + rows_of(w);
+  return static_cast<char*>(workspace) + parts_bytes(w);
+}
+
 }  // namespace
 }  // namespace paged
 
@@ -36,8 +46,29 @@ size_t paged_ws_bytes(const Problem& p, int first) {
   w.x.first = first;
   int rc = 0;
   if (p.B < 1 || !paged::pass(w, false, nullptr, &rc) || w.cluster || w.stride) return 0;
-  return paged::round256(paged::rows_of(w) * p.D * sizeof(float)) + paged::sums_bytes(w) +
-         paged::round256(w.ctas * sizeof(paged::CutUnit));
+  return paged::parts_bytes(w) + paged::round256(w.ctas * sizeof(paged::CutUnit));
+}
+
+size_t paged_own_bytes(const Problem& p, int sms) {
+  paged::Work w{};
+  w.p = p;
+  w.own.sms = sms;
+  int rc = 0;
+  if (p.B < 1 || !paged::pass(w, false, nullptr, &rc) || w.cluster || w.stride) return 0;
+  return paged::parts_bytes(w) + paged::round256((size_t)p.B * p.G * w.n_hc * sizeof(int2));
+}
+
+bool paged_own(const Problem& p, const Ext& x, const paged::OwnPart& own, void* workspace, cudaStream_t st,
+               paged::Work* done, int* rc) {
+  paged::Work w{};
+  w.p = p;
+  w.x = x;
+  w.own = own;
+  if (!paged::pass(w, false, st, rc)) return false;
+  if (!w.cluster && !w.stride) w.own.note = reinterpret_cast<int2*>(paged::lay_out(w, workspace));
+  paged::pass(w, true, st, rc);
+  *done = w;
+  return true;
 }
 
 int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, int* used) {
@@ -54,13 +85,8 @@ int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, 
   w.x = x;
   int rc = 0;
   if (!paged::pass(w, false, st, &rc)) return ATTN_OK;
-  if (!w.cluster && !w.stride) {   // only shares have fragments
-    w.part_o = static_cast<float*>(workspace);
-    w.part_m = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        paged::round256(paged::rows_of(w) * p.D * sizeof(float)));
-    w.part_l = w.part_m + paged::rows_of(w);
-    w.cuts = reinterpret_cast<paged::CutUnit*>(reinterpret_cast<char*>(w.part_m) + paged::sums_bytes(w));
-  }
+  if (!w.cluster && !w.stride)   // only shares have fragments
+    w.cuts = reinterpret_cast<paged::CutUnit*>(paged::lay_out(w, workspace));
   *used = 1;
   paged::pass(w, true, st, &rc);
   return rc;

@@ -43,6 +43,21 @@ struct CutUnit {
   int c0, late;
 };
 
+// What a pass does with its results when its keys are the own keys of a batch
+// with a prefix (shared.h; o null: it is another call).  Finished rows are kept for a
+// merge with the prefix's, at row * stride of o [..][D], m and l.  A unit cut by
+// shares is joined by that merge too: its note says where its fragments are.
+struct OwnPart {
+  float* o;
+  float* m;   // natural maxima (-inf: no visible key)
+  float* l;   // sums
+  int64_t stride;
+  int sms;    // SMs that the pass is planned for
+  // Of each unit [B][G * n_hc], in the workspace: its first fragment's slot (the others: slot 0 of the shares behind) and
+  // how many there are (0: the rows are kept).
+  int2* note;
+};
+
 struct Work {
   Problem p;
   Ext x;
@@ -56,6 +71,7 @@ struct Work {
   CutUnit* cuts;   // [ctas]
   int cluster;     // > 0: CTAs of the cluster that holds one unit (no shares)
   int stride;      // > 0: CTA c takes the units c, c + stride, ... (no shares)
+  OwnPart own;
 };
 
 __device__ __forceinline__ int entry_tiles(const Work& w, int b) {
@@ -289,6 +305,21 @@ struct Ring {
   }
 };
 
+// Notes that the rows of unit u of entry b are kept.
+__device__ __forceinline__ void note_kept(const Work& w, int b, int u) {
+  w.own.note[(int64_t)b * w.p.G * w.n_hc + u] = make_int2(0, 0);
+}
+// A finished row kept as a partial result, column d.
+__device__ __forceinline__ void keep_row(const Work& w, int b, int h, int d, float M, float L, float a) {
+  const int64_t at = ((int64_t)b * w.p.H + h) * w.own.stride;
+  const bool none = L == 0.f;
+  w.own.o[at * w.p.D + d] = none ? 0.f : a / L;
+  if (d == 0) {
+    w.own.m[at] = none ? -INFINITY : M;
+    w.own.l[at] = L;
+  }
+}
+
 // Where a row's finished fragment goes.  M: reference maximum in the units of
 // Scores<NAT> (-inf: no visible key), L: sum relative to it, a: numerator of element d.
 template <typename T, bool NAT>
@@ -304,6 +335,10 @@ __device__ __forceinline__ void put_row(const Work& w, bool whole, int cta, int 
       w.part_m[at] = none ? -INFINITY : M;
       w.part_l[at] = L;
     }
+    return;
+  }
+  if (w.own.o) {
+    keep_row(w, b, h, d, M, L, a);
     return;
   }
   if (p.sink_on) a *= fold_sink<false>(M, L, sink_logit(p, h));
@@ -322,6 +357,10 @@ __device__ __forceinline__ void fill_entry(const Work& w, int b) {
   for (int x = threadIdx.x; x < p.H * p.D; x += kThreads) {
     const int h = x / p.D, d = x - h * p.D;
     float M = -INFINITY, L = 0.f;
+    if (w.own.o) {
+      keep_row(w, b, h, d, M, L, 0.f);
+      continue;
+    }
     if (p.sink_on) fold_sink<false>(M, L, sink_logit(p, h));
     const bool none = L == 0.f;
     static_cast<T*>(p.O)[p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs + d] =
@@ -336,7 +375,11 @@ __device__ __forceinline__ void fill_entry(const Work& w, int b) {
 template <typename T>
 __device__ __forceinline__ void fill_entries(const Work& w, int cta) {
   for (int b = cta; b < w.p.B; b += w.ctas)
-    if (entry_tiles(w, b) == 0) fill_entry<T>(w, b);
+    if (entry_tiles(w, b) == 0) {
+      fill_entry<T>(w, b);
+      if (w.own.note)
+        for (int u = threadIdx.x; u < w.p.G * w.n_hc; u += kThreads) note_kept(w, b, u);
+    }
 }
 
 // Notes a cut unit that ends in share `cta` (whose first fragment it is), `first` tiles into its list.
@@ -344,7 +387,9 @@ __device__ __forceinline__ void note_cut(const Work& w, const Share& s, int cta,
   const int64_t at = s.t0 - first;
   const int c0 = share_of(s.total, s.shares, at);
   // (Share c0 has a fragment in front of it if it begins in front of the last unit's end.)
-  w.cuts[cta] = {c.b, c.u, c0, share_begin(s.total, s.shares, c0) < at - kEnd ? 1 : 0};
+  const int late = share_begin(s.total, s.shares, c0) < at - kEnd ? 1 : 0;
+  if (w.own.o) w.own.note[(int64_t)c.b * w.p.G * w.n_hc + c.u] = make_int2(2 * c0 + late, cta - c0 + 1);
+  else w.cuts[cta] = {c.b, c.u, c0, late};
 }
 
 // ---- units held by a cluster ----
@@ -434,7 +479,7 @@ inline void plan_work(Work& w, int tile, int heads, int ctas) {
   w.unit = tile;
   w.heads = heads;
   w.n_hc = (w.p.qpg + heads - 1) / heads;
-  const int64_t units = (int64_t)w.p.B * w.p.G * w.n_hc, n = (int64_t)kSms * ctas;
+  const int64_t units = (int64_t)w.p.B * w.p.G * w.n_hc, n = (int64_t)(w.own.sms ? w.own.sms : kSms) * ctas;
   int64_t span = w.p.Sk;
   if (w.p.causal && w.p.window >= 0) {
     const int64_t seen = (int64_t)w.p.window + 1 + w.x.first + 2 * tile;   // both parts may end inside tiles
@@ -453,19 +498,23 @@ inline void plan_work(Work& w, int tile, int heads, int ctas) {
 template <typename Kernel>
 int launch_pass(Kernel kern, const Work& w, int smem, cudaStream_t st) {
   if (ensure_smem((const void*)kern, smem) != cudaSuccess) return ATTN_ERR_CUDA;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)w.cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)w.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)w.ctas);
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = smem;
   c.stream = st;
-  c.attrs = &at;
+  c.attrs = at;
   c.numAttrs = w.cluster ? 1 : 0;
+  if (w.own.o) {   // the prefix's pass is in front: both run side by side where there is room
+    at[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[c.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
   if (cudaLaunchKernelEx(&c, kern, w) != cudaSuccess) return ATTN_ERR_CUDA;
-  return w.cluster || w.stride || launch_join(w, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return w.cluster || w.stride || w.own.o || launch_join(w, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace paged
@@ -473,5 +522,12 @@ int launch_pass(Kernel kern, const Work& w, int smem, cudaStream_t st) {
 // Fast passes: *used = 1 when one took the problem.  bytes: workspace they need.
 size_t paged_ws_bytes(const Problem& p, int first);
 int paged_try(const Problem& p, const Ext& x, void* workspace, cudaStream_t st, int* used);
+
+// The pass over the own keys of a batch with a prefix: the programmatic
+// dependent of the pass in front, which it waits for at its end.  paged_own:
+// false when there is none.  *done: the pass's plan, for the merge.
+size_t paged_own_bytes(const Problem& p, int sms);
+bool paged_own(const Problem& p, const Ext& x, const paged::OwnPart& own, void* workspace, cudaStream_t st,
+               paged::Work* done, int* rc);
 
 }  // namespace attn

@@ -70,13 +70,14 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
     if (my) out.at_unit(w, units, cta);
   } else {
     let_next_start();
-    if (threadIdx.x == 0) w.cuts[cta].b = -1;
+    if (threadIdx.x == 0 && !w.own.o) w.cuts[cta].b = -1;
     Share s;
     my = find_share(w, units, cta, lane, s, out);
     if (threadIdx.x == 0) share = s;
   }
   if (MODE != kCluster && my == 0) {
     fill_entries<float>(w, cta);
+    if (w.own.o) wait_for_previous();
     return;
   }
   typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
@@ -264,7 +265,10 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
         __syncthreads();
       }
       if constexpr (MODE == kShares)
-        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, share, cta, out, first_tile);
+        if (unit_ends && threadIdx.x == 0) {
+          if (!whole) note_cut(w, share, cta, out, first_tile);
+          else if (w.own.o) note_kept(w, out.b, out.u);
+        }
       ++frag;
     }
     if (i + 1 < my) {
@@ -284,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, CfgF32<D, NH, MODE>::kCtas) paged_f3
       for (int x = threadIdx.x; x < nh * D; x += kThreads) mine.put(D, x / D, x % D, -INFINITY, 0.f, 0.f);
     cluster_join<float, XF>(w, mine, out.b, h0, nh);
   }
+  if (w.own.o) wait_for_previous();
 }
 
 template <int D, int NH>

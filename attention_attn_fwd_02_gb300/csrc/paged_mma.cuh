@@ -165,13 +165,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     if (my) out.at_unit(w, units, cta);
   } else {
     let_next_start();
-    if (threadIdx.x == 0) w.cuts[cta].b = -1;
+    if (threadIdx.x == 0 && !w.own.o) w.cuts[cta].b = -1;
     Share s;
     my = find_share(w, units, cta, lane, s, out);
     if (threadIdx.x == 0) share = s;
   }
   if (MODE != kCluster && my == 0) {
     fill_entries<T>(w, cta);
+    if (w.own.o) wait_for_previous();
     return;
   }
   typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
@@ -442,7 +443,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
       const int g = out.u / w.n_hc, h0 = g * p.qpg + (out.u % w.n_hc) * C::kHeads;
       const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
       if constexpr (MODE == kShares)
-        if (unit_ends && !whole && threadIdx.x == 0) note_cut(w, share, cta, out, first_tile);
+        if (unit_ends && threadIdx.x == 0) {
+          if (!whole) note_cut(w, share, cta, out, first_tile);
+          else if (w.own.o) note_kept(w, out.b, out.u);
+        }
       if (i + 1 < my) {   // the next unit's queries arrive during the merge
         out.template next<MODE>(w, units);
         load_q();
@@ -508,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
       for (int x = threadIdx.x; x < nh * D; x += kThreads) mine.put(D, x / D, x % D, -INFINITY, 0.f, 0.f);
     cluster_join<T, XF>(w, mine, out.b, h0, nh);
   }
+  if (w.own.o) wait_for_previous();
 }
 
 // Plans the pass; with `launch` enqueues it.

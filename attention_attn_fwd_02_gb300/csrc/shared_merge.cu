@@ -1,0 +1,218 @@
+// shared_merge.cu -- merges the partial results of a batch over a shared prefix.
+//
+// What it computes: O = sum_s l_s exp(m_s - M) O_s / sum_s l_s exp(m_s - M) over
+// a row's partial results s, with the sink's logit as one more term of the
+// denominator, and LSE = M + log of that sum.  Which there are follows from the
+// plan (shared.h) and, for own keys that the decode pass cut, from its notes
+// (paged.cuh).
+//
+// What bounds it: the latency of its loads, a row having up to some forty
+// partial results of one row each.  WARPS warps take a row, each every WARPS-th
+// result; a lane reads a result's maximum and sum, then four columns each of up
+// to eight at a time (at head_dim 64 a warp's halves take every other one), and the warps meet in
+// shared memory.
+#include "shared.h"
+
+namespace attn {
+namespace shr {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 4;
+
+// Cut units of own keys (note null: there are none).
+struct Cuts {
+  const float *o, *m, *l;
+  const int2* note;
+  int heads, n_hc;
+};
+
+// The fragments of unit u: of the last share that begins in front of the unit's end.
+__device__ __forceinline__ int fragments(const Shares& s, int u) {
+  int lo = 0, hi = s.ctas;   // share lo begins in unit u or in front of it, share hi behind it
+  while (hi - lo > 1) {
+    const int c = (lo + hi) / 2;
+    if (s.unit[c] <= u) lo = c;
+    else hi = c;
+  }
+  return s.unit[lo] < u ? 1 : s.frag[lo] + 1;
+}
+
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(32 * kWarps) merge_kernel(const Problem p, const __grid_constant__ Work w,
+                                                            const Split s, const Cuts cuts) {
+  constexpr int kCols = D / 4, kTeams = 32 / kCols;   // lanes of a result's row, results side by side
+  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float4 s_acc[kWarps][kCols];
+  const int warp = threadIdx.x / 32, part = warp % WARPS;
+  const int64_t row = (int64_t)blockIdx.x * (kWarps / WARPS) + warp / WARPS;
+  const int lane = threadIdx.x % 32, team = lane / kCols, d = lane % kCols * 4;
+  const int i = (int)(row % p.Sq), h = (int)(row / p.Sq % p.H);
+  const int64_t b = row / ((int64_t)p.Sq * p.H);
+  const bool here = b < p.B;
+  int n_a = 0, n_b = w.parts_b << w.alt_b;
+  if (w.pre.ctas && here) {
+    const int64_t r = (b * p.Sq + i) * p.qpg + h % p.qpg;
+    const int u = h / p.qpg * w.pre.blocks + (int)(r / (2 * kRows));
+    n_a = fragments(w.pre, u) << (w.pre.is_alt(u) ? 1 : 0);
+  }
+  paged::wait_for_previous();
+  int64_t first = 0, rest = 0;   // rows of a cut unit's first fragment and of the others
+  bool cut = false;
+  if (cuts.note && here) {
+    const int j = h % p.qpg, u = h / p.qpg * cuts.n_hc + j / cuts.heads;
+    const int2 note = cuts.note[b * p.G * cuts.n_hc + u];
+    cut = note.y > 0;
+    if (cut) {
+      n_b = note.y;
+      first = (int64_t)note.x * cuts.heads + j % cuts.heads;
+      rest = (int64_t)(note.x / 2) * 2 * cuts.heads + j % cuts.heads;
+    }
+  }
+  const int n = here ? n_a + n_b : 0;
+  // Result k of the row: own ones of a cut unit are in the decode pass's arrays.
+  auto own_row = [&](int f) { return f == 0 ? first : rest + (int64_t)f * 2 * cuts.heads; };
+  auto kept = [&](int k) { return row * w.splits + (k < n_a ? k : w.own_slot + k - n_a); };
+  auto load_m = [&](int k) { return cut && k >= n_a ? cuts.m[own_row(k - n_a)] : s.part_lse[kept(k)]; };
+  auto load_l = [&](int k) { return cut && k >= n_a ? cuts.l[own_row(k - n_a)] : s.part_l[kept(k)]; };
+  auto load_o = [&](int k) {
+    const float* o = cut && k >= n_a ? cuts.o + own_row(k - n_a) * D : s.part_o + kept(k) * D;
+    return *reinterpret_cast<const float4*>(o + d);
+  };
+  const float sg = p.sink_on && part == 0 && here ? sink_logit(p, h) : -INFINITY;
+  bool bad = isnan(sg) || sg == INFINITY;
+  // This warp's results: part, part + WARPS, ...; the first 32 of them a lane each.
+  const int mine = (n - part + WARPS - 1) / WARPS;
+  const bool one = lane < mine;
+  const float m0 = one ? load_m(part + lane * WARPS) : -INFINITY;
+  const float l0 = one ? load_l(part + lane * WARPS) : 0.f;
+  float M = bad ? -INFINITY : sg;
+  for (int k = lane; k < mine; k += 32) {
+    const float m = k < 32 ? m0 : load_m(part + k * WARPS);
+    if (!(m < INFINITY)) bad = true;   // +inf or NaN
+    else M = fmaxf(M, m);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+  const float mu = M == -INFINITY ? 0.f : M;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < mine; base += 32) {
+    float wt = 0.f;
+    if (base + lane < mine) {
+      const int k = part + (base + lane) * WARPS;
+      const float m = base ? load_m(k) : m0;
+      if (m > -INFINITY) wt = (base ? load_l(k) : l0) * expf(m - mu);
+    }
+    bad = bad || isnan(wt);
+    sum += wt;
+    const int nr = min(32, mine - base);
+    for (int k0 = 0; k0 < nr; k0 += 8 * kTeams) {
+      float f[8];
+      float4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int k = k0 + q * kTeams + team;
+        f[q] = __shfl_sync(kAll, wt, k & 31);
+        if (k >= nr) f[q] = 0.f;
+        if (f[q] != 0.f) v[q] = load_o(part + (base + k) * WARPS);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (f[q] != 0.f) {   // (an empty result was not written)
+          acc.x = fmaf(f[q], v[q].x, acc.x);
+          acc.y = fmaf(f[q], v[q].y, acc.y);
+          acc.z = fmaf(f[q], v[q].z, acc.z);
+          acc.w = fmaf(f[q], v[q].w, acc.w);
+        }
+    }
+  }
+  bad = __any_sync(kAll, bad);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (!bad && sg > -INFINITY) sum += expf(sg - mu);
+  if (bad) sum = NAN;
+  if constexpr (kTeams == 2) {
+    acc.x += __shfl_xor_sync(kAll, acc.x, 16);
+    acc.y += __shfl_xor_sync(kAll, acc.y, 16);
+    acc.z += __shfl_xor_sync(kAll, acc.z, 16);
+    acc.w += __shfl_xor_sync(kAll, acc.w, 16);
+  }
+  if constexpr (WARPS > 1) {
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = sum;
+    }
+    if (team == 0) s_acc[warp][lane % kCols] = acc;
+    __syncthreads();
+    if (part > 0) return;
+    float f[WARPS], top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < WARPS; ++q) top = fmaxf(top, s_m[warp + q]);
+    const float to = top == -INFINITY ? 0.f : top;
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < WARPS; ++q) {
+      f[q] = s_m[warp + q] == -INFINITY ? 0.f : expf(s_m[warp + q] - to);
+      const float l = s_l[warp + q];
+      sum += isnan(l) ? l : f[q] * l;
+      const float4 v = s_acc[warp + q][lane % kCols];
+      acc.x = fmaf(f[q], v.x, acc.x);
+      acc.y = fmaf(f[q], v.y, acc.y);
+      acc.z = fmaf(f[q], v.z, acc.z);
+      acc.w = fmaf(f[q], v.w, acc.w);
+    }
+    M = top;
+  }
+  if (!here) return;
+  const bool nan = isnan(sum), none = !nan && M == -INFINITY;
+  if (team == 0) {
+    const float fill = none && p.masked_zero ? 0.f : NAN, inv = 1.f / sum;
+    const bool plain = !nan && !none;
+    T* out = static_cast<T*>(p.O) + p.o.off + b * p.o.bs + (int64_t)h * p.o.hs + (int64_t)i * p.o.rs + d;
+    const float a[4] = {acc.x, acc.y, acc.z, acc.w};
+    __align__(8) T y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(plain ? a[e] * inv : fill);
+    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);   // (rows of O are on 16-byte boundaries)
+  }
+  if (p.lse && lane == 0)
+    p.lse[b * p.lse_bs + (int64_t)h * p.lse_hs + i] = nan ? NAN : none ? -INFINITY : M + logf(sum);
+}
+
+template <typename T, int D, int WARPS>
+cudaError_t launch(const Problem& p, const Work& w, const Split& s, const Cuts& cuts, cudaStream_t st) {
+  const int64_t blocks = ((int64_t)p.B * p.H * p.Sq * WARPS + kWarps - 1) / kWarps;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)blocks);
+  c.blockDim = dim3(32 * kWarps);
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, merge_kernel<T, D, WARPS>, p, w, s, cuts);
+}
+
+template <typename T>
+cudaError_t launch_t(const Problem& p, const Work& w, const Split& s, const Cuts& cuts, cudaStream_t st) {
+  const bool many = w.splits > 8;
+  if (p.D == 64) return many ? launch<T, 64, 4>(p, w, s, cuts, st) : launch<T, 64, 1>(p, w, s, cuts, st);
+  return many ? launch<T, 128, 4>(p, w, s, cuts, st) : launch<T, 128, 1>(p, w, s, cuts, st);
+}
+
+}  // namespace
+}  // namespace shr
+
+cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const Split& s, const paged::Work* own,
+                                cudaStream_t st) {
+  shr::Cuts cuts{};
+  if (own && own->own.note) cuts = {own->part_o, own->part_m, own->part_l, own->own.note, own->heads, own->n_hc};
+  return p.dtype == ATTN_F16 ? shr::launch_t<__half>(p, w, s, cuts, st)
+                             : shr::launch_t<__nv_bfloat16>(p, w, s, cuts, st);
+}
+
+}  // namespace attn

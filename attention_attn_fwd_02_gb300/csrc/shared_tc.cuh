@@ -104,7 +104,7 @@ __device__ __forceinline__ int own_seen(const Problem& p, int b, int i) { return
 template <int D, bool BF16, bool XF>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const Problem p, const Ext x, const Work w, const int wide_rows, const int drop_first_copy,
+                     const Problem p, const Ext x, const __grid_constant__ Work w, const int wide_rows, const int drop_first_copy,
                      const Split sp) {
   using C = Cfg<D>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -123,8 +123,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (2^-25) is 2^-30 of the row's largest probability (window_tc.cuh).
   constexpr float kLead = (BF16 ? 0.f : 5.f) * (XF ? kLn2 : 1.f);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int my_items = (w.n_items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  __shared__ int items_a, my_items;   // this CTA's prefix items (in front), and all of its items
 
+  paged::let_next_start();
+  if (threadIdx.x == 32) {
+    int n = 0;
+    if (const int c = blockIdx.x; c < w.pre.ctas) {
+      const int u0 = w.pre.unit[c], u1 = w.pre.unit[c + 1], t0 = w.pre.tile[c], t1 = w.pre.tile[c + 1];
+      n = u1 > u0 ? u1 - u0 + (t1 > 0) : t1 > t0;
+    }
+    items_a = n;
+    my_items = n + max(0, (w.n_b - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x);
+  }
   if (threadIdx.x == 0) {
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
@@ -159,28 +169,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // ---------------- items ----------------
+    const int c = min((int)blockIdx.x, kSms - 1);
+    int u = w.pre.unit[c], tile = w.pre.tile[c];
     for (int k = 0; k < my_items; ++k) {
       const int buf = k & 1;
       if (k >= 2 && !wait_warp(&sb.item_empty[buf], (uint32_t)((k >> 1) - 1) & 1u, &sb.abort, p.status)) break;
-      const int id = (int)blockIdx.x + k * (int)gridDim.x;
       const int all = p.prefix / BN + (p.prefix % BN > 0);   // the prefix's tiles
       Item it;
       int i0, i1;
-      if (id < w.n_a) {   // the blocks of a part side by side: they read the same keys
-        const int blk = id % w.blocks_a, rest = id / w.blocks_a, part = rest / p.G;
+      if (k < items_a) {
         it.b = -1;
-        it.g = rest % p.G;
-        it.row0 = blk * 2 * BM;
+        it.g = u / w.pre.blocks;
+        it.row0 = u % w.pre.blocks * 2 * BM;
         it.rows = p.B * p.Sq * p.qpg;
         it.own_end = 0;
-        it.alt = w.alt_a;
-        it.slot = part << w.alt_a;
-        list_part(all, part, w.parts_a, i0, i1);
-        it.t0 = i0;
-        it.np = it.n = it.n0 = i1 - i0;
+        it.alt = w.pre.is_alt(u);
+        it.slot = (k == 0 ? w.pre.frag[c] : 0) << it.alt;   // (a unit that begins here has its first fragment here)
+        it.t0 = tile;
+        it.np = it.n = it.n0 = (u == w.pre.unit[c + 1] ? w.pre.tile[c + 1] : w.pre.tiles) - tile;
         it.o0 = 0;
+        ++u;
+        tile = 0;
       } else {   // the last row blocks, which see the most keys, first
-        int rest = id - w.n_a;
+        int rest = (int)blockIdx.x + (k - items_a) * (int)gridDim.x;
         const int part = rest % w.parts_b;
         rest /= w.parts_b;
         it.g = rest % p.G;
@@ -192,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.own_end = own_seen(p, it.b, (min(it.row0 + 2 * BM, it.rows) - 1) / p.qpg);
         const int end0 = own_seen(p, it.b, (min(it.row0 + BM, it.rows) - 1) / p.qpg);
         it.alt = w.alt_b;
-        it.slot = (w.parts_a << w.alt_a) + (part << w.alt_b);
+        it.slot = w.own_slot + (part << w.alt_b);
         const int np = w.joined ? all : 0;
         list_part(np + (it.own_end + BN - 1) / BN, part, w.parts_b, i0, i1);
         it.t0 = min(i0, np);
@@ -717,7 +728,8 @@ int launch(const Problem& p, const Ext& x, const Work& w, const Split& sp, cudaS
                        ? 1
                        : 0;
   const int drop = take_injection() == ATTN_INJECT_DROP_FIRST_COPY ? 1 : 0;
-  kern<<<(unsigned)(w.n_items < kSms ? w.n_items : kSms), kThreads, smem, st>>>(mk, mv, p, x, w, wide, drop, sp);
+  const int ctas = w.pre.ctas > w.n_b ? w.pre.ctas : w.n_b;
+  kern<<<(unsigned)(ctas < kSms ? ctas : kSms), kThreads, smem, st>>>(mk, mv, p, x, w, wide, drop, sp);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
