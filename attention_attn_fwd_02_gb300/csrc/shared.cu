@@ -111,6 +111,7 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
     const double us_each = (double)p.B * p.G * ceil_div(p.qpg, per) * p.prefix * p.D * 4 / 12.0e6;
     if (us_pre + kMerge + frags * part_us + kPass > us_each) return false;
     w.own_sms = kSms - s.ctas;
+    w.one_tile = all <= kRows;
     w.parts_b = own > 0;
     w.splits = w.own_slot + w.parts_b;
     return true;
@@ -126,6 +127,7 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   w.parts_b = own > 0 ? best_parts(blocks_b, own, w.alt_b, part_us, 0.0, &us_own) : 0;
   if (pre > 0 && p.B > 1 && us_pre + frags * part_us + us_own + kMerge < us_joined) {
     w.splits = w.own_slot + (w.parts_b << w.alt_b);
+    w.one_tile = all <= kRows;
   } else {
     s = Shares{};
     w.own_slot = w.alt_b = 0;

@@ -49,6 +49,7 @@ struct Work {
   int piece;                      // rows of a copy: the largest power of two up to 128 that divides a page
   int own_slot;                   // first partial result of the entry items (or of the decode pass over own keys)
   int splits;                     // partial results of a row (1: the items write O)
+  int one_tile;                   // every item has one row tile
   int own_sms;                    // SMs that the decode pass over own keys is planned for
 };
 

@@ -19,6 +19,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 4;
+constexpr int kFlight = 4;   // results of a row that a team has on their way
 
 // Cut units of own keys (note null: there are none).
 struct Cuts {
@@ -39,7 +40,7 @@ __device__ __forceinline__ int fragments(const Shares& s, int u) {
 }
 
 template <typename T, int D, int WARPS>
-__global__ void __launch_bounds__(32 * kWarps) merge_kernel(const Problem p, const __grid_constant__ Work w,
+__global__ void __launch_bounds__(32 * kWarps, 8) merge_kernel(const Problem p, const __grid_constant__ Work w,
                                                             const Split s, const Cuts cuts) {
   constexpr int kCols = D / 4, kTeams = 32 / kCols;   // lanes of a result's row, results side by side
   __shared__ float s_m[kWarps], s_l[kWarps];
@@ -107,18 +108,18 @@ __global__ void __launch_bounds__(32 * kWarps) merge_kernel(const Problem p, con
     bad = bad || isnan(wt);
     sum += wt;
     const int nr = min(32, mine - base);
-    for (int k0 = 0; k0 < nr; k0 += 8 * kTeams) {
-      float f[8];
-      float4 v[8];
+    for (int k0 = 0; k0 < nr; k0 += kFlight * kTeams) {
+      float f[kFlight];
+      float4 v[kFlight];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      for (int q = 0; q < kFlight; ++q) {
         const int k = k0 + q * kTeams + team;
         f[q] = __shfl_sync(kAll, wt, k & 31);
         if (k >= nr) f[q] = 0.f;
         if (f[q] != 0.f) v[q] = load_o(part + (base + k) * WARPS);
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
+      for (int q = 0; q < kFlight; ++q)
         if (f[q] != 0.f) {   // (an empty result was not written)
           acc.x = fmaf(f[q], v[q].x, acc.x);
           acc.y = fmaf(f[q], v[q].y, acc.y);
@@ -199,7 +200,7 @@ cudaError_t launch(const Problem& p, const Work& w, const Split& s, const Cuts& 
 
 template <typename T>
 cudaError_t launch_t(const Problem& p, const Work& w, const Split& s, const Cuts& cuts, cudaStream_t st) {
-  const bool many = w.splits > 8;
+  const bool many = w.splits > 8 && (int64_t)p.B * p.H * p.Sq * kWarps <= 8 * kWarps * kSms;   // while all run at once
   if (p.D == 64) return many ? launch<T, 64, 4>(p, w, s, cuts, st) : launch<T, 64, 1>(p, w, s, cuts, st);
   return many ? launch<T, 128, 4>(p, w, s, cuts, st) : launch<T, 128, 1>(p, w, s, cuts, st);
 }

@@ -16,10 +16,12 @@
 // reference maximum that moves with a slack.  What is its own:
 //   - a block of one row tile deals its key tiles to both row tiles of the
 //     kernel in turn, so that one's softmax overlaps the other's products;
-//   - K and V tiles are put together from a page list: the copy warp's lanes
-//     look up a page each, a tile ahead, and issue a TMA box of `piece` rows and
-//     64 columns each.  A piece without a page is copied from a page behind the
-//     pool: it arrives as zeros and counts its bytes;
+//   - K and V tiles are put together from a page list: a warp for K and one for
+//     V, whose lanes look up a page each, a tile ahead, and issue a TMA box of
+//     `piece` rows and 64 columns each (some 40 cycles a box).  A piece without a page is copied from a page
+//     behind the pool: it arrives as zeros and counts its bytes;
+//   - K and V tiles alternate in one ring of as many slots as the shared memory
+//     holds: what is on its way bounds the rate that an SM reads at;
 //   - Q rows come from wherever (entry, query, head) puts them: each softmax
 //     thread loads its own row of the next item while the tensor cores finish
 //     the current one's, so rows pack without gaps whatever the strides.
@@ -50,7 +52,8 @@ static_assert(kSplitRegs <= kThreads * ((65536 / kThreads) & ~7), "register spli
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kSlack = 8.0f;     // log2 units
-constexpr int kNotes = 8;          // key tiles whose pages are noted: stages + 3 at least (see the copy warp)
+constexpr int kMaxSlots = 13;      // tiles of the ring
+constexpr int kNotes = 16;         // key tiles whose pages are noted (see the copy of K)
 
 // A row block's part of its tile list, as the roles read it.
 struct Item {
@@ -66,8 +69,8 @@ struct Item {
 };
 
 struct Bars {
-  uint64_t q_full[2];
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t q_full[2], q_seen, q_empty;
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t item_full[2], item_empty[2];
   uint64_t mma_done;
@@ -78,13 +81,25 @@ struct Bars {
 template <int D>
 struct Cfg {
   static constexpr int kChunks = D / 64;                  // 64-column (128-byte) chunks
-  static constexpr int kStages = D <= 64 ? 4 : 2;
-  static constexpr int kQTile = BM * D * 2;               // bytes
-  static constexpr int kKTile = BN * D * 2;
-  static constexpr int kSmem = 2 * kQTile + 2 * kStages * kKTile;
+  static constexpr int kTile = 128 * D * 2;               // bytes of a tile of Q, K or V
+  static constexpr int kTiles = D <= 64 ? 14 : 7;         // of shared memory: one or two of Q, the ring
+  static constexpr int kSmem = kTiles * kTile;
   static constexpr int kS0 = 0, kS1 = BN, kO0 = 2 * BN, kO1 = 2 * BN + D;
   static_assert(2 * BN + 2 * D <= 512, "TMEM budget");
-  static_assert(kNotes >= kStages + 3, "notes of key tiles");
+  static_assert(kTiles - 1 <= kMaxSlots && kNotes >= (kTiles - 1) / 2 + 4, "slots and notes");
+};
+
+// A place in the ring of n slots and its phase.
+struct Slot {
+  int s;
+  uint32_t ph;
+  __device__ __forceinline__ void next_tile(int n) {   // K's (or V's) slot of the next key tile
+    s += 2;
+    if (s >= n) {
+      s -= n;
+      ph ^= 1u;
+    }
+  }
 };
 
 // The lowest n bits (n may lie outside [0, 32]).
@@ -111,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;
-  uint8_t* k_s = q_s + 2 * C::kQTile;
-  uint8_t* v_s = k_s + C::kStages * C::kKTile;
+  const int n_slots = C::kTiles - (w.one_tile ? 1 : 2);
+  uint8_t* ring = q_s + (C::kTiles - n_slots) * C::kTile;
   __shared__ Bars sb;
   __shared__ Item items[2];
   __shared__ uint32_t no_page[kNotes];   // of a key tile: which of its pieces have no page
@@ -139,19 +154,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
     sb.abort = 0;
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sb.k_full[s], 1);
-      mbar_init(&sb.k_empty[s], 1);
-      mbar_init(&sb.v_full[s], 1);
-      mbar_init(&sb.v_empty[s], 1);
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(&sb.full[s], 1);
+      mbar_init(&sb.empty[s], 1);
     }
+    mbar_init(&sb.q_seen, 1);
+    mbar_init(&sb.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sb.q_full[i], BM);
       mbar_init(&sb.s_full[i], 1);
       mbar_init(&sb.p_full[i], BM);
       mbar_init(&sb.o_done[i], 1);
       mbar_init(&sb.item_full[i], 32);
-      mbar_init(&sb.item_empty[i], 2 + 2 * BM);   // the copy and MMA warps and every softmax thread
+      mbar_init(&sb.item_empty[i], 3 + 2 * BM);   // the copy and MMA warps and every softmax thread
     }
     mbar_init(&sb.mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -217,26 +232,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_arrive(&sb.item_full[buf]);
     }
-  } else if (warp == 8) {
+  } else if (warp == 8 || warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    // ---------------- copies: every lane a piece of a tile ----------------
+    // ---------------- copies of K (warp 8) and V: every lane a piece of a tile ----------------
+    const bool is_k = warp == 8;
+    const CUtensorMap* map = is_k ? &tm_k : &tm_v;
     const int pieces = BN / w.piece;   // 1 .. 16
     const int piece = lane % pieces, chunk = lane / pieces;
     const bool copies = chunk < C::kChunks;
     const int at = chunk * BN * 128 + piece * w.piece * 128;
-    // This lane's piece of tile i of an item: its page (n_pages: none) and row in it.
+    // This lane's piece of tile i of an item: its page (n_pages behind the last key, -1: there is none) and row in it.
     auto look_up = [&](const Item& it, int i, int& row) {
       const bool pre = i < it.np;
       const int r = (pre ? it.t0 + i : it.o0 + i - it.np) * BN + piece * w.piece;
       row = 0;
-      if (r >= (pre ? p.prefix : it.own_end)) return (int)x.n_pages;   // behind the last key: not masked as a missing page
+      if (r >= (pre ? p.prefix : it.own_end)) return (int)x.n_pages;
       const int pi = page_index(x, r);
       row = r - pi * x.page_size;
       const int32_t pg = __ldg((pre ? x.prefix_table : x.table + (int64_t)it.b * x.table_stride) + pi);
       return (uint32_t)pg < x.n_pages ? (int)pg : -1;
     };
-    int gt = 0;        // tiles whose K and V copies were issued
-    int k_only = -1;   // a tile whose K copy was issued but not its V copy
+    Slot sl{is_k ? 0 : 1, 0u};
+    int gt = 0;   // tiles copied
     bool ok = true;
     for (int k = 0; ok && k < my_items; ++k) {
       const int buf = k & 1;
@@ -246,44 +263,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       int row = 0, page = 0;
       if (n > 0) page = look_up(it, 0, row);
       for (int i = 0; i < n; ++i) {
-        const int s = gt % C::kStages;
-        const uint32_t ph = (uint32_t)(gt / C::kStages) & 1u;
         const uint32_t missing = __ballot_sync(0xffffffffu, page < 0 && chunk == 0);
         const int pg = page < 0 ? (int)x.n_pages : page, prow = row;
-        if (i + 1 < n) page = look_up(it, i + 1, row);   // arrives while this tile waits for its stage
-        if (!(ok = wait_warp(&sb.k_empty[s], ph ^ 1u, &sb.abort, p.status))) break;
+        if (i + 1 < n) page = look_up(it, i + 1, row);   // arrives while this tile waits for its slot
+        if (!(ok = wait_warp(&sb.empty[sl.s], sl.ph ^ 1u, &sb.abort, p.status))) break;
         if (lane == 0) {
-          // Slot gt % kNotes was read for tile gt - kNotes: S of tile gt - kStages is done, which followed the row
-          // tiles' reading of the notes up to tile gt - kStages - 3.
-          no_page[gt % kNotes] = missing;
-          mbar_expect_tx(&sb.k_full[s], C::kKTile);
+          // Note gt % kNotes was read for tile gt - kNotes.  The slot was free: the product that used it is done, of tile
+          // gt - n_slots / 2 - 1 or a later one, whose S followed the row tiles' reading of notes two tiles further back.
+          if (is_k) no_page[gt % kNotes] = missing;
+          mbar_expect_tx(&sb.full[sl.s], C::kTile);
         }
         __syncwarp();
         // Test hook (attn_test_inject): the first CTA's first K copy is
         // announced but never issued, so the MMA warp's wait runs out.
-        const bool dropped = drop_first_copy && gt == 0 && blockIdx.x == 0;
-        if (copies && !dropped) tma_load_4d(k_s + s * C::kKTile + at, &tm_k, &sb.k_full[s], chunk * 64, prow, g, pg);
-        if (!(ok = wait_warp(&sb.v_empty[s], ph ^ 1u, &sb.abort, p.status))) {
-          k_only = gt;
-          break;
-        }
-        if (lane == 0) mbar_expect_tx(&sb.v_full[s], C::kKTile);
-        __syncwarp();
-        if (copies) tma_load_4d(v_s + s * C::kKTile + at, &tm_v, &sb.v_full[s], chunk * 64, prow, g, pg);
+        const bool dropped = drop_first_copy && is_k && gt == 0 && blockIdx.x == 0;
+        if (copies && !dropped) tma_load_4d(ring + sl.s * C::kTile + at, map, &sb.full[sl.s], chunk * 64, prow, g, pg);
+        sl.next_tile(n_slots);
         ++gt;
       }
       if (ok && lane == 0) mbar_arrive(&sb.item_empty[buf]);
     }
-    // Copies still in flight land before the CTA can exit.  Earlier copies
-    // completed before their stage was refilled.
+    // Copies still in flight land before the CTA can exit: the last ones, whose slots were not refilled (the others
+    // completed before theirs were).
     if (lane == 0) {
-      for (int i = gt > C::kStages ? gt - C::kStages : 0; i < gt; ++i) {
-        const int s = i % C::kStages;
-        const uint32_t ph = (uint32_t)(i / C::kStages) & 1u;
-        drain_bar(&sb.k_full[s], ph, p.status);
-        drain_bar(&sb.v_full[s], ph, p.status);
+      Slot last{is_k ? 0 : 1, 0u};
+      for (int i = 0; i < gt; ++i) {
+        if (i >= gt - n_slots / 2) drain_bar(&sb.full[last.s], last.ph, p.status);
+        last.next_tile(n_slots);
       }
-      if (k_only >= 0) drain_bar(&sb.k_full[k_only % C::kStages], (uint32_t)(k_only / C::kStages) & 1u, p.status);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -291,13 +298,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issuer (warp-wide; one elected lane issues) ----------------
     constexpr uint32_t kIdQK = idesc_f16(BF16, false, BM, BN);
     constexpr uint32_t kIdPV = idesc_f16(BF16, true, BM, D);
-    const uint32_t q_addr = su32(q_s), k_addr = su32(k_s), v_addr = su32(v_s);
-    const uint64_t qd0 = sdesc(q_addr, 16, 1024), qd1 = sdesc(q_addr + C::kQTile, 16, 1024);
-    const uint64_t kd0 = sdesc(k_addr, 16, 1024), vd0 = sdesc(v_addr, BN * 128, 1024);
-    auto issue_qk = [&](int tt, int s) {
+    const uint32_t q_addr = su32(q_s), ring_addr = su32(ring);
+    const uint64_t qd0 = sdesc(q_addr, 16, 1024), kd0 = sdesc(ring_addr, 16, 1024);
+    const uint64_t vd0 = sdesc(ring_addr, BN * 128, 1024);
+    // S of row tile tt from the queries of tile `qt`.
+    auto issue_qk = [&](int tt, int qt, int s) {
       fence_after();
-      const uint64_t ad = tt ? qd1 : qd0;
-      const uint64_t bd0 = sdesc_add(kd0, (uint32_t)(s * C::kKTile));
+      const uint64_t ad = sdesc_add(qd0, (uint32_t)(qt * C::kTile));
+      const uint64_t bd0 = sdesc_add(kd0, (uint32_t)(s * C::kTile));
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t a = sdesc_add(ad, (uint32_t)((kk / 4) * BM * 128 + (kk % 4) * 32));
@@ -308,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto issue_pv = [&](int tt, int s, bool start) {
       fence_after();
-      const uint64_t bd0 = sdesc_add(vd0, (uint32_t)(s * C::kKTile));
+      const uint64_t bd0 = sdesc_add(vd0, (uint32_t)(s * C::kTile));
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk) {
         const uint64_t bd = sdesc_add(bd0, (uint32_t)(kk * 16 * 128));
@@ -324,100 +332,101 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seen >= BN) return;
       for (int u = seen * (C::kChunks * 8) + lane; u < BN * (C::kChunks * 8); u += 32) {
         const int row = u / (C::kChunks * 8), rest = u % (C::kChunks * 8);
-        *reinterpret_cast<uint4*>(v_s + s * C::kKTile + (rest / 8) * BN * 128 + row * 128 + (rest % 8) * 16) =
+        *reinterpret_cast<uint4*>(ring + s * C::kTile + (rest / 8) * BN * 128 + row * 128 + (rest % 8) * 16) =
             make_uint4(0, 0, 0, 0);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     };
-    int gt = 0, c0 = 0, c1 = 0;   // tiles, and P V steps of each row tile so far
+    int c0 = 0, c1 = 0;                // P V steps of each row tile so far
+    Slot ks{0, 0u}, vs{1, 0u};         // the next key tile to take S of, and the next to take P V of
     bool ok = true, issued = false;
-    auto k_ready = [&](int j) {
-      return wait_warp(&sb.k_full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, &sb.abort, p.status);
-    };
+    auto k_ready = [&]() { return wait_warp(&sb.full[ks.s], ks.ph, &sb.abort, p.status); };
     for (int k = 0; ok && k < my_items; ++k) {
       const int buf = k & 1;
       if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
       const Item& it = items[buf];
       const int n = it.n;
-      // (every phase of both, also where a row tile has nothing to do: a phase left out would be taken for the next)
+      // Every phase of both, also where a row tile has nothing to do; and q_seen keeps the row tiles within one phase of
+      // this warp: a wait takes a phase that is two ahead for one that has not come.
       if (!(ok = wait_warp(&sb.q_full[0], (uint32_t)k & 1u, &sb.abort, p.status))) break;
       if (!(ok = wait_warp(&sb.q_full[1], (uint32_t)k & 1u, &sb.abort, p.status))) break;
-      if (n > 0) {
+      if (lane == 0) mbar_arrive(&sb.q_seen);
+      bool start0 = true, start1 = true;
+      if (n > 0 && it.alt) {
         issued = true;
-        bool start0 = true, start1 = true;
-        if (it.alt) {
-          // Tile i belongs to row tile i % 2: P V of tile i, then S of tile i + 2.
-          for (int i = 0; i < 2 && i < n; ++i) {
-            if (!(ok = k_ready(gt + i))) break;
-            issue_qk(i, (gt + i) % C::kStages);
-            mma_commit_w(&sb.k_empty[(gt + i) % C::kStages]);
+        // Tile i belongs to row tile i % 2: P V of tile i, then S of tile i + 2.
+        auto next_s = [&](int i) {
+          if (!k_ready()) return false;
+          issue_qk(i & 1, 0, ks.s);
+          mma_commit_w(&sb.empty[ks.s]);
+          if (i + 1 == n) mma_commit_w(&sb.q_empty);   // that was the item's last S
+          ks.next_tile(n_slots);
+          return true;
+        };
+        for (int i = 0; ok && i < 2 && i < n; ++i) ok = next_s(i);
+        for (int i = 0; ok && i < n; ++i) {
+          const int t = i & 1;
+          if (!(ok = wait_warp(&sb.full[vs.s], vs.ph, &sb.abort, p.status))) break;
+          clear_tail(it, i, vs.s);
+          if (!(ok = wait_warp(&sb.p_full[t], (uint32_t)(t ? c1 : c0) & 1u, &sb.abort, p.status))) break;
+          issue_pv(t, vs.s, t ? start1 : start0);
+          mma_commit_w(&sb.empty[vs.s]);
+          vs.next_tile(n_slots);
+          if (t) {
+            start1 = false;
+            ++c1;
+          } else {
+            start0 = false;
+            ++c0;
           }
-          if (!ok) break;
-          for (int i = 0; i < n; ++i, ++gt) {
-            const int s = gt % C::kStages, t = i & 1;
-            const uint32_t ph = (uint32_t)(gt / C::kStages) & 1u;
-            if (!(ok = wait_warp(&sb.v_full[s], ph, &sb.abort, p.status))) break;
-            clear_tail(it, i, s);
-            if (!(ok = wait_warp(&sb.p_full[t], (uint32_t)(t ? c1 : c0) & 1u, &sb.abort, p.status))) break;
-            issue_pv(t, s, t ? start1 : start0);
-            mma_commit_w(&sb.v_empty[s]);
-            if (t) {
-              start1 = false;
-              ++c1;
-            } else {
-              start0 = false;
-              ++c0;
-            }
-            if (i + 2 < n) {
-              if (!(ok = k_ready(gt + 2))) break;
-              issue_qk(t, (gt + 2) % C::kStages);
-              mma_commit_w(&sb.k_empty[(gt + 2) % C::kStages]);
-            }
+          if (i + 2 < n) ok = next_s(i + 2);
+        }
+      } else if (n > 0) {
+        issued = true;
+        const int n0 = it.n0;
+        const bool some1 = it.some1 != 0;
+        if (!(ok = k_ready())) break;
+        if (n0 > 0) issue_qk(0, 0, ks.s);
+        if (some1) issue_qk(1, 1, ks.s);
+        mma_commit_w(&sb.empty[ks.s]);
+        ks.next_tile(n_slots);
+        bool rv = mbar_test(&sb.full[vs.s], vs.ph);   // the next V landed?
+        for (int i = 0; i < n; ++i) {
+          const bool more = i + 1 < n, has0 = i < n0;
+          const bool rp0 = !has0 || mbar_test(&sb.p_full[0], (uint32_t)c0 & 1u);
+          if (!(ok = wait_ready(rv, &sb.full[vs.s], vs.ph, &sb.abort, p.status))) break;
+          clear_tail(it, i, vs.s);
+          const bool rk = !more || mbar_test(&sb.full[ks.s], ks.ph);
+          // Row tile 0: P0 V, then the next S0.  (P of an item's first tile
+          // follows the threads' reading of the previous item's O, so O may be
+          // overwritten.)
+          if (has0) {
+            if (!(ok = wait_ready(rp0, &sb.p_full[0], (uint32_t)c0 & 1u, &sb.abort, p.status))) break;
+            issue_pv(0, vs.s, start0);
+            start0 = false;
+            ++c0;
           }
-        } else {
-          const int n0 = it.n0;
-          const bool some1 = it.some1 != 0;
-          if (!(ok = k_ready(gt))) break;
-          if (n0 > 0) issue_qk(0, gt % C::kStages);
-          if (some1) issue_qk(1, gt % C::kStages);
-          mma_commit_w(&sb.k_empty[gt % C::kStages]);
-          bool rv = mbar_test(&sb.v_full[gt % C::kStages], (uint32_t)(gt / C::kStages) & 1u);   // the next V landed?
-          for (int i = 0; i < n; ++i, ++gt) {
-            const int s = gt % C::kStages, s1 = (gt + 1) % C::kStages;
-            const uint32_t ph = (uint32_t)(gt / C::kStages) & 1u, ph1 = (uint32_t)((gt + 1) / C::kStages) & 1u;
-            const bool more = i + 1 < n, has0 = i < n0;
-            const bool rp0 = !has0 || mbar_test(&sb.p_full[0], (uint32_t)c0 & 1u);
-            if (!(ok = wait_ready(rv, &sb.v_full[s], ph, &sb.abort, p.status))) break;
-            clear_tail(it, i, s);
-            const bool rk = !more || mbar_test(&sb.k_full[s1], ph1);
-            // Row tile 0: P0 V, then the next S0.  (P of an item's first tile
-            // follows the threads' reading of the previous item's O, so O may be
-            // overwritten.)
-            if (has0) {
-              if (!(ok = wait_ready(rp0, &sb.p_full[0], (uint32_t)c0 & 1u, &sb.abort, p.status))) break;
-              issue_pv(0, s, start0);
-              start0 = false;
-              ++c0;
-            }
-            const bool rp1 = !some1 || mbar_test(&sb.p_full[1], (uint32_t)c1 & 1u);
-            if (more) {
-              if (!(ok = wait_ready(rk, &sb.k_full[s1], ph1, &sb.abort, p.status))) break;
-              if (i + 1 < n0) issue_qk(0, s1);
-            }
-            rv = more && mbar_test(&sb.v_full[s1], ph1);
-            // Row tile 1: P1 V, then the next S1.
-            if (some1) {
-              if (!(ok = wait_ready(rp1, &sb.p_full[1], (uint32_t)c1 & 1u, &sb.abort, p.status))) break;
-              issue_pv(1, s, start1);
-              start1 = false;
-              ++c1;
-            }
-            mma_commit_w(&sb.v_empty[s]);
-            if (more) {
-              if (some1) issue_qk(1, s1);
-              mma_commit_w(&sb.k_empty[s1]);
-            }
+          const bool rp1 = !some1 || mbar_test(&sb.p_full[1], (uint32_t)c1 & 1u);
+          if (more) {
+            if (!(ok = wait_ready(rk, &sb.full[ks.s], ks.ph, &sb.abort, p.status))) break;
+            if (i + 1 < n0) issue_qk(0, 0, ks.s);
+          }
+          const int v_done = vs.s;
+          vs.next_tile(n_slots);
+          rv = more && mbar_test(&sb.full[vs.s], vs.ph);
+          // Row tile 1: P1 V, then the next S1.
+          if (some1) {
+            if (!(ok = wait_ready(rp1, &sb.p_full[1], (uint32_t)c1 & 1u, &sb.abort, p.status))) break;
+            issue_pv(1, v_done, start1);
+            start1 = false;
+            ++c1;
+          }
+          mma_commit_w(&sb.empty[v_done]);
+          if (more) {
+            if (some1) issue_qk(1, 1, ks.s);
+            mma_commit_w(&sb.empty[ks.s]);
+            ks.next_tile(n_slots);
           }
         }
       }
@@ -430,8 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) drain_bar(&sb.mma_done, 0, p.status);
     }
     __syncwarp();
-  } else if (warp == 11) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------- softmax: one thread per query row ----------------
@@ -461,8 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    // Loads this thread's query row into its place of the tile (128-byte swizzle); zeros for a row that is not.
+    // Loads this thread's query row into its place of the tile (128-byte swizzle); zeros for a row that is not.  (Row
+    // tiles that hold the same rows share the first tile.)
     auto load_q = [&](const Item& it) {
+      if (it.alt && t == 1) {
+        mbar_arrive(&sb.q_full[1]);
+        return;
+      }
       int b, i, h;
       const bool here = row_of(it, b, i, h);
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.Q) + p.q.off + (int64_t)b * p.q.bs +
@@ -472,12 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = 0; u < D / 8; ++u) v[u] = here ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int u = 0; u < D / 8; ++u)
-        *reinterpret_cast<uint4*>(q_s + t * C::kQTile + (u / 8) * BM * 128 + r * 128 + (((u % 8) ^ (r & 7)) << 4)) = v[u];
+        *reinterpret_cast<uint4*>(q_s + t * C::kTile + (u / 8) * BM * 128 + r * 128 + (((u % 8) ^ (r & 7)) << 4)) = v[u];
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&sb.q_full[t]);
     };
     int j = 0;    // key tiles so far
     int gt = 0;   // key tiles of the items so far
+    uint32_t alt_phase = 0u;
     bool ok = my_items > 0 && wait_warp(&sb.item_full[0], 0u, &sb.abort, p.status);
     if (ok) load_q(items[0]);
     for (int k = 0; ok && k < my_items; ++k) {
@@ -625,9 +638,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       gt += n;
-      // The next item's queries: this row tile's last S, whose phase was waited for above, was its queries' last use.
+      // The next item's queries.  This row tile's last S, whose phase was waited for above, was its queries' last use, but
+      // for queries that both row tiles use (whose phases are the items of one row tile).
       if (k + 1 < my_items) {
         if (!(ok = wait_warp(&sb.item_full[buf ^ 1], (uint32_t)((k + 1) >> 1) & 1u, &sb.abort, p.status))) break;
+        if (!(ok = wait_warp(&sb.q_seen, (uint32_t)k & 1u, &sb.abort, p.status))) break;
+        if (t == 0 && it.alt && n > 0) {
+          if (!(ok = wait_warp(&sb.q_empty, alt_phase, &sb.abort, p.status))) break;
+          alt_phase ^= 1u;
+        }
         load_q(items[buf ^ 1]);
       }
       // ---- epilogue: O / l, special rows, LSE ----

@@ -233,6 +233,35 @@ def test_offsets_past_32_bits():
         assert torch.equal(out, near)
 
 
+@pytest.mark.parametrize("dt,D,Sq,B", [("bf16", 128, 1, 100), ("f16", 64, 30, 2)])
+def test_bounded_wait(dt, D, Sq, B):
+    """A copy that never comes: the call gives up after its limit, reports it, and the next call is right."""
+    c = sc.make(dt, D, B, Sq, 8, 8, 16, 8000, [Sq + 3 * b for b in range(B)], 61)
+    st = torch.cuda.current_stream().cuda_stream
+    want = sc.run(c)
+    assert attn.attn_device_status(st) == attn.ATTN_OK
+    assert attn.attn_test_inject(attn.ATTN_INJECT_DROP_FIRST_COPY) == attn.ATTN_OK
+    sc.run(c)
+    assert attn.attn_device_status(st) == attn.ATTN_ERR_DEVICE_TIMEOUT
+    assert torch.equal(sc.run(c), want)
+
+
+@pytest.mark.parametrize("dt,D,Sq,B,H,G,prefix", [
+    ("f16", 64, 30, 2, 8, 8, 8000), ("bf16", 128, 9, 30, 8, 2, 900), ("bf16", 64, 1, 300, 16, 8, 3000),
+    ("f16", 128, 140, 5, 8, 8, 700)])
+def test_many_times_over(dt, D, Sq, B, H, G, prefix):
+    """Items in which a row tile has nothing to do, again and again: no wait runs out, the bits stay."""
+    c = sc.make(dt, D, B, Sq, H, G, 16, prefix, [Sq + (7 * b) % 200 for b in range(B)], 71)
+    want = sc.run(c)
+    sc.check(c, want)
+    out = torch.empty_like(want)
+    for _ in range(60):
+        out.fill_(9.0)
+        sc.run(c, out=out)
+        assert torch.equal(out, want)
+    assert attn.attn_device_status(torch.cuda.current_stream().cuda_stream) == attn.ATTN_OK
+
+
 def test_refusals():
     c = sc.make("bf16", 128, 2, 3, 4, 2, 16, 100, [9, 12], 51)
     q, k, v, ptab, prefix, table = c["call"]
