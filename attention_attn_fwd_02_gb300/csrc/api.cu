@@ -473,8 +473,8 @@ size_t shared_bytes(const attn_problem* p, const attn_pages* pages, const attn_p
   const size_t a = n > 1 ? sums_ws_bytes(p, n) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
   shr::Work w;
   size_t c = 0;
-  if (shared_tc_plan(r, pages->page_size, w) && w.splits > 1) {
-    c = sums_ws_bytes(p, w.splits);
+  if (shared_tc_plan(r, pages->page_size, w)) {
+    c = shared_tc_bytes(r, w);
     if (p->q_len == 1) c += paged_own_bytes(own_problem(r), w.own_sms);   // behind the partial results
   }
   return a > b ? (a > c ? a : c) : (b > c ? b : c);
@@ -684,12 +684,9 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t rows = (size_t)p->batch * p->heads * p->q_len;
   int used = 0;
-  Split s{1, 1, nullptr, nullptr};
   shr::Work w;
   if (shared_tc_plan(r, x.page_size, w)) {
-    if (w.splits > 1) s = split_in(workspace, rows, w.splits, 0, p->head_dim, true);
-    void* ws_own = static_cast<char*>(workspace) + sums_ws_bytes(p, w.splits);   // (used with one query an entry)
-    rc = shared_tc_try(r, x, w, s, own_problem(r), make_ext(0, pages), ws_own, st, &used);
+    rc = shared_tc_try(r, x, w, own_problem(r), make_ext(0, pages), workspace, st, &used);
     if (rc || used) return rc;
   }
   if (p->q_len == 1) {
@@ -697,7 +694,7 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
     if (rc || used) return rc;
   }
   const int n = shared_plan(p, prefix);
-  s = Split{1, 1, nullptr, nullptr};
+  Split s{1, 1, nullptr, nullptr};
   if (n > 1) s = split_in(workspace, rows, n, 0, p->head_dim, true);
   rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;

@@ -1,5 +1,5 @@
 // shared.cu -- the tensor-core pass over a shared prefix: which problems it
-// takes and how they are divided into items (shared.h).
+// takes and how they are divided (shared.h).
 #include <math.h>
 
 #include "shared.h"
@@ -7,29 +7,96 @@
 
 namespace attn {
 
-int shared_tc64(const Problem& p, const Ext& x, const shr::Work& w, const Split& sp, cudaStream_t st);
-int shared_tc128(const Problem& p, const Ext& x, const shr::Work& w, const Split& sp, cudaStream_t st);
+int shared_tc64(const Problem& p, const Ext& x, const shr::Work& w, cudaStream_t st);
+int shared_tc128(const Problem& p, const Ext& x, const shr::Work& w, cudaStream_t st);
 
 namespace shr {
 namespace {
 
-constexpr int kMaxParts = 32;   // of a list
+constexpr int kMaxParts = 32;   // of an entry item's list
 constexpr double kUnit = 0.2;   // us of a cost unit of Shares
+constexpr double kPass = 5.0;   // us, a pass's fixed cost
+constexpr double kMerge = 4.0;  // us, a merge's
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// us: `items` items of `tiles` key tiles, dealt to the SMs in turn.
-double pass_us(int64_t items, int64_t tiles, bool alt) {
-  return (double)ceil_div(items, kSms) * ((double)tiles * (alt ? Shares::kTileAlt : Shares::kTile) + Shares::kEnd) * kUnit;
+// `count` units side by side of `tiles` key tiles, each of `tile` cost units.
+struct Run {
+  int64_t count, tiles;
+  int tile;
+  int64_t cost() const { return tiles * tile + Shares::kEnd; }
+};
+
+// The runs of a plan's list, in its order.  step(i, run): the i-th of them; the return value says how many there are.
+struct Runs {
+  const Problem& p;
+  const Work& w;
+  int64_t pre;
+  int64_t size() const { return w.joined ? w.blocks : 2 * (int64_t)p.G; }
+  Run at(int64_t i) const {
+    if (!w.joined) {   // a kv head's blocks of two row tiles, then the one that may have one
+      const bool last = i & 1;
+      return {last ? w.alt : w.blocks - w.alt, pre, last ? Shares::kTileAlt : Shares::kTile};
+    }
+    const int blk = w.blocks - 1 - (int)i;
+    const int64_t rows = (int64_t)p.Sq * p.qpg, end = (int64_t)(blk + 1) * 2 * kRows;
+    const int64_t q = ((end < rows ? end : rows) - 1) / p.qpg;   // the block's last query
+    int64_t own = p.Sk - p.prefix;
+    if (p.causal) {
+      const int64_t seen = q + 1 + (p.align_klens ? own - p.Sq : p.coff - p.prefix);
+      own = clamp64(seen, 0, own);
+    }
+    const int64_t tiles = pre + ceil_div(own, kKeys);   // (rows without keys have a unit too)
+    return {(int64_t)p.B * p.G, tiles > 0 ? tiles : 1, w.is_alt(blk) ? Shares::kTileAlt : Shares::kTile};
+  }
+  int64_t total() const {
+    int64_t t = 0;
+    for (int64_t i = 0; i < size(); ++i) t += at(i).count * at(i).cost();
+    return t;
+  }
+};
+
+// Cuts the list into s.ctas shares (each is to have a tile's cost at least), in the middle of units or, with `whole`,
+// at the nearest border of two.  Returns the most fragments of a unit.
+int cut(const Runs& runs, int64_t total, bool whole, Shares& s) {
+  int64_t i = 0, first = 0, begin = 0;   // run, its first unit, and where that begins
+  Run run = runs.at(0);
+  int most = 1;
+  for (int c = 0; c <= s.ctas; ++c) {
+    const int64_t t = total / s.ctas * c + total % s.ctas * c / s.ctas;
+    while (i + 1 < runs.size() && t - begin >= run.count * run.cost()) {
+      begin += run.count * run.cost();
+      first += run.count;
+      run = runs.at(++i);
+    }
+    const int64_t k = clamp64((t - begin) / run.cost(), 0, run.count);   // the units in front, of this run
+    int64_t at = (t - begin - k * run.cost()) / run.tile;
+    bool next = at >= run.tiles;   // in a unit's end
+    if (whole) {
+      next = 2 * at >= run.tiles;
+      at = 0;
+    }
+    if (k == run.count) next = false;
+    s.unit[c] = (int)(first + k + next);
+    s.tile[c] = next || k == run.count ? 0 : (int)at;
+    if (c == s.ctas) break;
+    s.frag[c] = 0;
+    if (s.tile[c] > 0) {   // one more than the last share's, where that began in the unit too
+      s.frag[c] = (int16_t)(s.unit[c - 1] == s.unit[c] ? s.frag[c - 1] + 1 : 1);
+      most = s.frag[c] + 1 > most ? s.frag[c] + 1 : most;
+    }
+  }
+  return most;
 }
 
-// The number of parts of `tiles` key tiles, for `blocks` row blocks, that takes the least time; part_us: what a partial
-// result of every row costs, merge_us: the merge, where more than one part asks for it.
-int best_parts(int64_t blocks, int64_t tiles, bool alt, double part_us, double merge_us, double* us) {
+// The number of parts of entry items' lists of `tiles` key tiles that takes the least time; part_us: a partial result of
+// every row, written and read.
+int best_parts(int64_t items, int64_t tiles, bool alt, double part_us, double* us) {
   int best = 1;
   *us = 0;
   for (int n = 1; n <= kMaxParts && n <= tiles; ++n) {
-    const double t = pass_us(blocks * n, ceil_div(tiles, n), alt) + ((n > 1) * merge_us) + (n << alt) * part_us;
+    const double list = (double)(ceil_div(tiles, n) * (alt ? Shares::kTileAlt : Shares::kTile) + Shares::kEnd) * kUnit;
+    const double t = (double)ceil_div(items * n, kSms) * list + n * part_us;
     if (n == 1 || t < *us) {
       *us = t;
       best = n;
@@ -38,38 +105,13 @@ int best_parts(int64_t blocks, int64_t tiles, bool alt, double part_us, double m
   return best;
 }
 
-}  // namespace
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-int Shares::cut(int heads) {
-  const int64_t full = (int64_t)tiles * kTile + kEnd, less = alt ? (int64_t)tiles * (kTile - kTileAlt) : 0;
-  const int64_t total = heads * (blocks * full - less);
-  int64_t begin = 0;   // of unit u, whose place in its kv head is k
-  int u = 0, k = 0, most = 1;
-  for (int c = 0; c <= ctas; ++c) {
-    const int64_t t = total * c / ctas;
-    const int units = heads * blocks;
-    auto cost = [&]() { return k == blocks - 1 ? full - less : full; };
-    while (u < units && t - begin >= cost()) {
-      begin += cost();
-      ++u;
-      k = k + 1 < blocks ? k + 1 : 0;
-    }
-    const int64_t at = (t - begin) / (alt && k == blocks - 1 ? kTileAlt : kTile);
-    const bool behind = u < units && at >= tiles;   // in a unit's end
-    unit[c] = u + behind;
-    tile[c] = u < units && !behind ? (int)at : 0;
-    if (c == ctas) break;
-    // The number of this share's first fragment: one more than the last share's, where that has tiles of the unit.
-    frag[c] = 0;
-    if (tile[c] > 0) {
-      const bool same = unit[c - 1] == unit[c];
-      frag[c] = (int16_t)(same ? frag[c - 1] + 1 : 1);
-      most = frag[c] + 1 > most ? frag[c] + 1 : most;
-    }
-  }
-  return most;
+int64_t kept_rows(const Problem& p, const Work& w) {
+  return w.joined ? (int64_t)w.list.ctas * 2 * 2 * kRows : (int64_t)p.B * p.H * p.Sq * w.splits;
 }
 
+}  // namespace
 }  // namespace shr
 
 bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
@@ -85,81 +127,107 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   while (page_size % w.piece) w.piece /= 2;
   const int64_t pre = ceil_div(p.prefix, kKeys), own = ceil_div(p.Sk - p.prefix, kKeys);
   const double part_us = (double)(all * p.G) * p.D * 8 / 6.0e6;   // a partial result of every row, written and read
-  constexpr double kMerge = 4.0, kPass = 5.0;                      // a merge's and a pass's fixed cost
+  auto has_half = [](int64_t n) { return (int)((n - 1) % (2 * kRows) < kRows); };   // the last block has one row tile
   // The prefix once for the packed rows of all entries.
-  Shares& s = w.pre;
-  s.tiles = (int)pre;
-  s.blocks = (int)ceil_div(all, 2 * kRows);
-  s.alt = (all - 1) % (2 * kRows) < kRows;
-  const int64_t total =
-      p.G * (s.blocks * (pre * Shares::kTile + Shares::kEnd) - s.alt * pre * (Shares::kTile - Shares::kTileAlt));
-  int ctas = kSms;
-  if (p.Sq == 1 && own > 0) {
-    // The decode pass over pages takes the own keys, side by side with the prefix's: each gets SMs by its cost, own
-    // lists being half as long as they can be.
-    const double us_own = (double)p.B * p.G * (p.Sk - p.prefix) * p.D * 2 / 6.0e6, us_all = (double)total * kUnit / kSms;
-    ctas = (int)(kSms * (us_all + kPass) / (us_all + us_own + 2 * kPass));
-    w.own_sms = kSms - ctas;
+  double us_packed = INFINITY;
+  if (pre > 0) {
+    w.blocks = (int)ceil_div(all, 2 * kRows);
+    w.alt = has_half(all);
+    const Runs runs{p, w, pre};
+    const int64_t total = runs.total();
+    int ctas = kSms;
+    if (p.Sq == 1 && own > 0) {
+      // The decode pass over pages takes the own keys, side by side with the prefix's: each gets SMs by its cost, own
+      // lists being half as long as they can be.
+      const double us_own = (double)p.B * p.G * (p.Sk - p.prefix) * p.D * 2 / 6.0e6;
+      const double us_all = (double)total * kUnit / kSms;
+      ctas = (int)(kSms * (us_all + kPass) / (us_all + us_own + 2 * kPass));
+    }
+    w.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, ctas);
+    w.own_slot = cut(runs, total, false, w.list);
+    us_packed = kPass + kMerge + (double)total / w.list.ctas * kUnit + w.own_slot * part_us;
+    w.one_tile = all <= kRows;
+    w.own_sms = kSms - w.list.ctas;
   }
-  s.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, ctas);
-  const int frags = s.cut(p.G);
-  w.own_slot = frags << s.alt;
-  const double us_pre = kPass + (double)total / s.ctas * kUnit;
   if (p.Sq == 1) {
     // The decode pass can take the prefix's keys too, once an entry, out of L2.
     const int per = p.qpg > 8 ? 16 : 8;
     const double us_each = (double)p.B * p.G * ceil_div(p.qpg, per) * p.prefix * p.D * 4 / 12.0e6;
-    if (us_pre + kMerge + frags * part_us + kPass > us_each) return false;
-    w.own_sms = kSms - s.ctas;
-    w.one_tile = all <= kRows;
     w.parts_b = own > 0;
     w.splits = w.own_slot + w.parts_b;
-    return true;
+    return us_packed + kPass <= us_each;
   }
   w.blocks_b = (int)ceil_div(rows, 2 * kRows);
-  const int64_t blocks_b = w.blocks_b * (int64_t)p.G * p.B;
-  if (blocks_b > 0x3fffffff / kMaxParts) return false;
-  // Each entry by itself: its rows walk the prefix and their own keys.
-  double us_joined = 0, us_own = 0;
-  const int parts_joined = best_parts(blocks_b, pre + own, false, part_us, kMerge, &us_joined);
-  if (parts_joined == 1) us_joined -= part_us;
-  w.alt_b = rows <= kRows;
-  w.parts_b = own > 0 ? best_parts(blocks_b, own, w.alt_b, part_us, 0.0, &us_own) : 0;
-  if (pre > 0 && p.B > 1 && us_pre + frags * part_us + us_own + kMerge < us_joined) {
-    w.splits = w.own_slot + (w.parts_b << w.alt_b);
-    w.one_tile = all <= kRows;
-  } else {
-    s = Shares{};
-    w.own_slot = w.alt_b = 0;
-    w.joined = 1;
-    w.parts_b = w.splits = parts_joined;
-  }
-  w.n_b = (int)(blocks_b * w.parts_b);
+  w.alt_b = has_half(rows);
+  const int64_t items = w.blocks_b * (int64_t)p.G * p.B;
+  if (items > 0x3fffffff / kMaxParts) return false;
+  double us_own = 0;
+  w.parts_b = own > 0 ? best_parts(items, own, rows <= kRows, part_us, &us_own) : 0;
+  w.splits = w.own_slot + w.parts_b;
+  w.n_b = (int)items * w.parts_b;
+  us_packed += us_own;
+  // Or each entry by itself: its rows walk the prefix and their own keys.
+  Work v{};
+  v.joined = 1;
+  v.piece = w.piece;
+  v.blocks = w.blocks_b;
+  v.alt = w.alt_b;
+  v.one_tile = rows <= kRows;
+  const Runs runs{p, v, pre};
+  const int64_t total = runs.total();
+  v.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, kSms);
+  // Cut units cost the write and the read of two fragments a share and the merge; whole ones leave the last shares' rest.
+  const double us_cut = kMerge + (double)v.list.ctas * 4 * kRows * p.D * 8 / 6.0e6;
+  const double us_unit = (double)runs.at(0).cost() * kUnit;
+  const bool whole = us_unit / 2 < us_cut && items >= v.list.ctas;
+  v.splits = cut(runs, total, whole, v.list) > 1;
+  const double us_joined = kPass + (double)total / v.list.ctas * kUnit + (whole ? us_unit / 2 : us_cut);
+  if (!(us_packed < us_joined)) w = v;
   return true;
 }
 
-int shared_tc_try(const Problem& p, const Ext& x, const shr::Work& w, const Split& s, const Problem& own, const Ext& x_own,
-                  void* ws_own, cudaStream_t st, int* used) {
+size_t shared_tc_bytes(const Problem& p, const shr::Work& w) {
+  using namespace shr;
+  if (w.splits == 0) return 0;
+  const size_t rows = (size_t)kept_rows(p, w);
+  return round256(rows * p.D * sizeof(float)) + 2 * round256(rows * sizeof(float)) +
+         round256(w.joined ? 0 : (size_t)w.blocks * p.G * sizeof(int));
+}
+
+int shared_tc_try(const Problem& p, const Ext& x, shr::Work& w, const Problem& own, const Ext& x_own, void* workspace,
+                  cudaStream_t st, int* used) {
+  using namespace shr;
   *used = 0;
   const int pages = (int)min(x.n_pages, 0x7fffffffu);
   if (pages < 1 || pages == 0x7fffffff) return ATTN_OK;
   if (!tma_layout_ok(p.Q, p.q, p.Sq, p.H, p.B) || !tma_layout_ok(p.K, p.k, x.page_size, p.G, pages) ||
       !tma_layout_ok(p.V, p.v, x.page_size, p.G, pages) || !tma_layout_ok(p.O, p.o, p.Sq, p.H, p.B))
     return ATTN_OK;
-  int rc = p.D == 64 ? shared_tc64(p, x, w, s, st) : shared_tc128(p, x, w, s, st);
+  if (w.splits > 0) {
+    const int64_t rows = kept_rows(p, w);
+    char* at = static_cast<char*>(workspace);
+    w.part_o = reinterpret_cast<float*>(at);
+    at += round256(rows * p.D * sizeof(float));
+    w.part_m = reinterpret_cast<float*>(at);
+    at += round256(rows * sizeof(float));
+    w.part_l = reinterpret_cast<float*>(at);
+    w.note = reinterpret_cast<int*>(at + round256(rows * sizeof(float)));
+  }
+  int rc = p.D == 64 ? shared_tc64(p, x, w, st) : shared_tc128(p, x, w, st);
   if (rc < 0) return ATTN_OK;  // tensor map refused: another pass
   *used = 1;
   if (rc) return rc;
   paged::Work decode{};
   const bool decoded = p.Sq == 1 && own.Sk > 0;
   if (decoded) {   // (its types and layouts are among the ones checked above)
-    const paged::OwnPart part{s.part_o + (int64_t)w.own_slot * p.D, s.part_lse + w.own_slot, s.part_l + w.own_slot,
+    const paged::OwnPart part{w.part_o + (int64_t)w.own_slot * p.D, w.part_m + w.own_slot, w.part_l + w.own_slot,
                               w.splits, w.own_sms, nullptr};
-    if (!paged_own(own, x_own, part, ws_own, st, &decode, &rc)) return ATTN_ERR_UNSUPPORTED;
+    void* ws = static_cast<char*>(workspace) + shared_tc_bytes(p, w);
+    if (!paged_own(own, x_own, part, ws, st, &decode, &rc)) return ATTN_ERR_UNSUPPORTED;
     if (rc) return rc;
   }
-  if (w.splits == 1) return ATTN_OK;
-  return launch_shared_merge(p, w, s, decoded ? &decode : nullptr, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (w.splits == 0) return ATTN_OK;
+  return launch_shared_merge(p, w, decoded ? &decode : nullptr, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace attn

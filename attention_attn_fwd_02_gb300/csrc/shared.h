@@ -11,59 +11,69 @@ constexpr int kRows = 128;    // query rows of a tile
 constexpr int kKeys = 128;    // keys of a tile
 constexpr int kSms = 152;
 
-// How the CTAs share the prefix.  A row is a (entry, query, head of the kv
-// head's group) triple, in this order; the rows of all entries are packed into
-// blocks of two row tiles, and a unit -- a block of a kv head -- walks all of the
-// prefix's key tiles.  The tiles of all units, laid end to end, are cut into shares of
-// equal cost, one a CTA; a unit's result is the merge of its fragments, one of
-// each CTA that has tiles of it.
+// A list of units cut into shares of equal cost, one a CTA: a unit is a block of
+// rows, of one or two row tiles, with its key tiles.  Units lie end to end;
+// share c begins at tile `tile[c]` of unit `unit[c]`, and what it has of a unit
+// is a fragment, the first of them number frag[c] of its unit.  (Worked out on
+// the host: the kernel's registers have no room for 64-bit divisions.)
 struct Shares {
-  // Costs, about 0.2 us each: a key tile of both row tiles, of the one row tile that a kv head's last block may have,
-  // and what an item costs besides.
-  static constexpr int kTile = 7, kTileAlt = 3, kEnd = 10;
-  int ctas, tiles;        // shares; key tiles of the prefix
-  int blocks, alt;        // row blocks of a kv head; 1: the last has one row tile
-  // Share c begins at tile `tile[c]` of unit `unit[c]`; the first fragment's number in its unit.  (Worked out on the
-  // host: the kernels' registers have no room for 64-bit divisions.)
+  // Costs, about 0.2 us each: a key tile of both row tiles, of one, and what a fragment costs besides.
+  static constexpr int kTile = 7, kTileAlt = 4, kEnd = 10;
+  int ctas;               // 0: there is no list
   int unit[kSms + 1];
-  int16_t frag[kSms];
   int tile[kSms + 1];
-
-  __host__ __device__ bool is_alt(int u) const { return alt && u % blocks == blocks - 1; }
-  // Cuts the tiles of `heads` kv heads; ctas has to leave every share a tile's cost at least.  Returns the most
-  // fragments of a unit.
-  int cut(int heads);
+  int16_t frag[kSms];
 };
 
-// How a problem is divided into items, by value to the kernels.  Prefix items are
-// fragments of units (above).  Entry items take the rows of one entry and walk a
-// part of its own key tiles, behind the prefix's with `joined`.  An item of one
-// row tile (alt) deals its key tiles to both row tiles of the kernel in turn,
-// which then hold the same rows and give a partial result each.  A row's
-// partial results are its unit's fragments, then its entry items'.
+// How a problem is divided, by value to the kernels.  A row is a (entry, query,
+// head of the kv head's group) triple, in this order.
+//   packed   The rows of all entries are packed into blocks of 256, and a unit
+//            (kv head by kv head, its blocks in turn) walks the prefix's key tiles.
+//            The entries' own keys are walked by entry items, rows of one entry
+//            (in turn over the CTAs), or by the decode pass for one query an
+//            entry.  A row's partial results, its unit's fragments and then its
+//            own keys', are merged.
+//   joined   A unit is a block of 256 rows of one entry (the last blocks, which
+//            see the most keys, in front, then entry by entry, kv head by kv
+//            head) and walks the prefix's tiles and behind them its own, as many as
+//            k_len allows: shares go by these, and an entry with fewer keys has
+//            shorter fragments.  Whole units write O; a share keeps its first
+//            fragment, where it began in the middle of a unit, and its last,
+//            where it ends in one, for the merge.
+// A block whose rows fit one row tile (`alt`: the last one) deals its key tiles
+// to both row tiles of the kernel, which then hold the same rows, in turn.
 struct Work {
-  Shares pre;                     // pre.ctas = 0: no prefix items
-  int blocks_b, parts_b, alt_b;   // entry items: row blocks of an entry and kv head, parts of its list
+  Shares list;
   int joined;
+  int blocks, alt;                // row blocks of a kv head (packed) or of an entry and kv head (joined)
+  int blocks_b, alt_b, parts_b;   // entry items (packed): row blocks of an entry and kv head, parts of their lists
   int n_b;                        // entry items
   int piece;                      // rows of a copy: the largest power of two up to 128 that divides a page
-  int own_slot;                   // first partial result of the entry items (or of the decode pass over own keys)
-  int splits;                     // partial results of a row (1: the items write O)
+  int own_slot;                   // packed: first partial result of own keys
+  int splits;                     // packed: partial results of a row.  joined: 1 if a share keeps any
   int one_tile;                   // every item has one row tile
   int own_sms;                    // SMs that the decode pass over own keys is planned for
+  // Partial results: numerators over their sums, natural maxima (-inf: no visible key), sums.  packed: [B H q_len][splits]
+  // in (entry, head, query) order; joined: [ctas][2][256].  note: packed, the number of each unit's fragments.
+  float *part_o, *part_m, *part_l;
+  int* note;
+
+  __host__ __device__ int block_of(int u, int B, int G) const { return joined ? blocks - 1 - u / (B * G) : u % blocks; }
+  __host__ __device__ bool is_alt(int block) const { return alt && block == blocks - 1; }
 };
 
 }  // namespace shr
 
 // The pass's plan, from the shape alone.  False: another pass takes the problem.
 bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w);
-// Enqueues a plan's passes; s: room for its partial results.  own, x_own, ws_own: for one query an entry, the problem of
-// the entries' own keys and the decode pass's workspace.  As prefill_tc_try.
-int shared_tc_try(const Problem& p, const Ext& x, const shr::Work& w, const Split& s, const Problem& own, const Ext& x_own,
-                  void* ws_own, cudaStream_t st, int* used);
+// Bytes of a plan's partial results and notes.
+size_t shared_tc_bytes(const Problem& p, const shr::Work& w);
+// Enqueues a plan's passes.  own, x_own: for one query an entry, the problem of the entries' own keys, whose decode pass
+// has its workspace behind the plan's.  As prefill_tc_try.
+int shared_tc_try(const Problem& p, const Ext& x, shr::Work& w, const Problem& own, const Ext& x_own, void* workspace,
+                  cudaStream_t st, int* used);
 // Merges a plan's partial results, as the programmatic dependent of the pass in front.  own: the decode pass over own
 // keys, whose cut units it joins too (null: there was none).
-cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const Split& s, const paged::Work* own,
-                                cudaStream_t st);
+cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const paged::Work* own, cudaStream_t st);
 
 }  // namespace attn

@@ -28,58 +28,16 @@ struct Cuts {
   int heads, n_hc;
 };
 
-// The fragments of unit u: of the last share that begins in front of the unit's end.
-__device__ __forceinline__ int fragments(const Shares& s, int u) {
-  int lo = 0, hi = s.ctas;   // share lo begins in unit u or in front of it, share hi behind it
-  while (hi - lo > 1) {
-    const int c = (lo + hi) / 2;
-    if (s.unit[c] <= u) lo = c;
-    else hi = c;
-  }
-  return s.unit[lo] < u ? 1 : s.frag[lo] + 1;
-}
-
-template <typename T, int D, int WARPS>
-__global__ void __launch_bounds__(32 * kWarps, 8) merge_kernel(const Problem p, const __grid_constant__ Work w,
-                                                            const Split s, const Cuts cuts) {
+// Merges the n results of a row (WARPS warps; every thread of them comes here).  load_m, load_l: a result's maximum and
+// sum; load_o: four columns of it.
+template <typename T, int D, int WARPS, typename M_, typename L_, typename O_>
+__device__ __forceinline__ void merge_row(const Problem& p, bool here, int64_t b, int h, int i, int n, M_ load_m,
+                                          L_ load_l, O_ load_o) {
   constexpr int kCols = D / 4, kTeams = 32 / kCols;   // lanes of a result's row, results side by side
   __shared__ float s_m[kWarps], s_l[kWarps];
   __shared__ float4 s_acc[kWarps][kCols];
   const int warp = threadIdx.x / 32, part = warp % WARPS;
-  const int64_t row = (int64_t)blockIdx.x * (kWarps / WARPS) + warp / WARPS;
   const int lane = threadIdx.x % 32, team = lane / kCols, d = lane % kCols * 4;
-  const int i = (int)(row % p.Sq), h = (int)(row / p.Sq % p.H);
-  const int64_t b = row / ((int64_t)p.Sq * p.H);
-  const bool here = b < p.B;
-  int n_a = 0, n_b = w.parts_b << w.alt_b;
-  if (w.pre.ctas && here) {
-    const int64_t r = (b * p.Sq + i) * p.qpg + h % p.qpg;
-    const int u = h / p.qpg * w.pre.blocks + (int)(r / (2 * kRows));
-    n_a = fragments(w.pre, u) << (w.pre.is_alt(u) ? 1 : 0);
-  }
-  paged::wait_for_previous();
-  int64_t first = 0, rest = 0;   // rows of a cut unit's first fragment and of the others
-  bool cut = false;
-  if (cuts.note && here) {
-    const int j = h % p.qpg, u = h / p.qpg * cuts.n_hc + j / cuts.heads;
-    const int2 note = cuts.note[b * p.G * cuts.n_hc + u];
-    cut = note.y > 0;
-    if (cut) {
-      n_b = note.y;
-      first = (int64_t)note.x * cuts.heads + j % cuts.heads;
-      rest = (int64_t)(note.x / 2) * 2 * cuts.heads + j % cuts.heads;
-    }
-  }
-  const int n = here ? n_a + n_b : 0;
-  // Result k of the row: own ones of a cut unit are in the decode pass's arrays.
-  auto own_row = [&](int f) { return f == 0 ? first : rest + (int64_t)f * 2 * cuts.heads; };
-  auto kept = [&](int k) { return row * w.splits + (k < n_a ? k : w.own_slot + k - n_a); };
-  auto load_m = [&](int k) { return cut && k >= n_a ? cuts.m[own_row(k - n_a)] : s.part_lse[kept(k)]; };
-  auto load_l = [&](int k) { return cut && k >= n_a ? cuts.l[own_row(k - n_a)] : s.part_l[kept(k)]; };
-  auto load_o = [&](int k) {
-    const float* o = cut && k >= n_a ? cuts.o + own_row(k - n_a) * D : s.part_o + kept(k) * D;
-    return *reinterpret_cast<const float4*>(o + d);
-  };
   const float sg = p.sink_on && part == 0 && here ? sink_logit(p, h) : -INFINITY;
   bool bad = isnan(sg) || sg == INFINITY;
   // This warp's results: part, part + WARPS, ...; the first 32 of them a lane each.
@@ -116,7 +74,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) merge_kernel(const Problem p, 
         const int k = k0 + q * kTeams + team;
         f[q] = __shfl_sync(kAll, wt, k & 31);
         if (k >= nr) f[q] = 0.f;
-        if (f[q] != 0.f) v[q] = load_o(part + (base + k) * WARPS);
+        if (f[q] != 0.f) v[q] = load_o(part + (base + k) * WARPS, d);
       }
 #pragma unroll
       for (int q = 0; q < kFlight; ++q)
@@ -182,9 +140,68 @@ __global__ void __launch_bounds__(32 * kWarps, 8) merge_kernel(const Problem p, 
     p.lse[b * p.lse_bs + (int64_t)h * p.lse_hs + i] = nan ? NAN : none ? -INFINITY : M + logf(sum);
 }
 
+// packed: a row's results are its unit's fragments and then its own keys' (shared.h).
 template <typename T, int D, int WARPS>
-cudaError_t launch(const Problem& p, const Work& w, const Split& s, const Cuts& cuts, cudaStream_t st) {
-  const int64_t blocks = ((int64_t)p.B * p.H * p.Sq * WARPS + kWarps - 1) / kWarps;
+__global__ void __launch_bounds__(32 * kWarps, 8)
+    merge_kernel(const Problem p, const __grid_constant__ Work w, const Cuts cuts) {
+  const int64_t row = (int64_t)blockIdx.x * (kWarps / WARPS) + threadIdx.x / 32 / WARPS;
+  const int i = (int)(row % p.Sq), h = (int)(row / p.Sq % p.H);
+  const int64_t b = row / ((int64_t)p.Sq * p.H);
+  const bool here = b < p.B;
+  const int64_t r = (b * p.Sq + i) * p.qpg + h % p.qpg;
+  const int unit = h / p.qpg * w.blocks + (int)(r / (2 * kRows));
+  const int j = h % p.qpg, u = cuts.note ? h / p.qpg * cuts.n_hc + j / cuts.heads : 0;
+  paged::wait_for_previous();
+  int n_a = 0, n_b = w.parts_b;
+  int64_t first = 0, rest = 0;   // rows of a cut unit's first fragment and of the others
+  bool cut = false;
+  if (here) {
+    n_a = w.note[unit];
+    if (cuts.note) {
+      const int2 note = cuts.note[b * p.G * cuts.n_hc + u];
+      cut = note.y > 0;
+      if (cut) {
+        n_b = note.y;
+        first = (int64_t)note.x * cuts.heads + j % cuts.heads;
+        rest = (int64_t)(note.x / 2) * 2 * cuts.heads + j % cuts.heads;
+      }
+    }
+  }
+  // Result k of the row: own ones of a cut unit are in the decode pass's arrays.
+  auto own_row = [&](int f) { return f == 0 ? first : rest + (int64_t)f * 2 * cuts.heads; };
+  auto kept = [&](int k) { return row * w.splits + (k < n_a ? k : w.own_slot + k - n_a); };
+  merge_row<T, D, WARPS>(
+      p, here, b, h, i, here ? n_a + n_b : 0,
+      [&](int k) { return cut && k >= n_a ? cuts.m[own_row(k - n_a)] : w.part_m[kept(k)]; },
+      [&](int k) { return cut && k >= n_a ? cuts.l[own_row(k - n_a)] : w.part_l[kept(k)]; },
+      [&](int k, int d) {
+        const float* o = cut && k >= n_a ? cuts.o + own_row(k - n_a) * D : w.part_o + kept(k) * D;
+        return *reinterpret_cast<const float4*>(o + d);
+      });
+}
+
+// joined: the fragments of the unit that share c began in the middle of and ends.
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(32 * kWarps, 8) join_kernel(const Problem p, const __grid_constant__ Work w) {
+  constexpr int kPer = kWarps / WARPS;   // rows of a CTA
+  const int c = blockIdx.x / (2 * kRows / kPer);
+  const int local = blockIdx.x % (2 * kRows / kPer) * kPer + threadIdx.x / 32 / WARPS;
+  if (w.list.tile[c] == 0 || w.list.unit[c + 1] == w.list.unit[c]) return;
+  const int u = w.list.unit[c], n = w.list.frag[c] + 1, c0 = c - w.list.frag[c];
+  const int row = w.block_of(u, p.B, p.G) * 2 * kRows + local, i = row / p.qpg;
+  const int h = u % p.G * p.qpg + row - i * p.qpg;
+  const bool here = i < p.Sq;
+  paged::wait_for_previous();
+  // The first fragment is the last of its share, the others are their shares' first.
+  auto at = [&](int f) { return ((int64_t)(c0 + f) * 2 + (f == 0 ? 1 : 0)) * (2 * kRows) + local; };
+  merge_row<T, D, WARPS>(
+      p, here, u / p.G % p.B, h, i, here ? n : 0, [&](int f) { return w.part_m[at(f)]; },
+      [&](int f) { return w.part_l[at(f)]; },
+      [&](int f, int d) { return *reinterpret_cast<const float4*>(w.part_o + at(f) * D + d); });
+}
+
+template <typename... Args>
+cudaError_t launch(void (*kern)(Args...), int64_t blocks, cudaStream_t st, Args... args) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -195,25 +212,31 @@ cudaError_t launch(const Problem& p, const Work& w, const Split& s, const Cuts& 
   c.stream = st;
   c.attrs = &at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, merge_kernel<T, D, WARPS>, p, w, s, cuts);
+  return cudaLaunchKernelEx(&c, kern, args...);
 }
 
-template <typename T>
-cudaError_t launch_t(const Problem& p, const Work& w, const Split& s, const Cuts& cuts, cudaStream_t st) {
-  const bool many = w.splits > 8 && (int64_t)p.B * p.H * p.Sq * kWarps <= 8 * kWarps * kSms;   // while all run at once
-  if (p.D == 64) return many ? launch<T, 64, 4>(p, w, s, cuts, st) : launch<T, 64, 1>(p, w, s, cuts, st);
-  return many ? launch<T, 128, 4>(p, w, s, cuts, st) : launch<T, 128, 1>(p, w, s, cuts, st);
+template <typename T, int D>
+cudaError_t merge(const Problem& p, const Work& w, const Cuts& cuts, cudaStream_t st) {
+  if (w.joined) {
+    int most = 0;
+    for (int c = 0; c < w.list.ctas; ++c) most = w.list.frag[c] > most ? w.list.frag[c] : most;
+    if (most >= 4) return launch(join_kernel<T, D, 4>, (int64_t)w.list.ctas * 2 * kRows, st, p, w);
+    return launch(join_kernel<T, D, 1>, (int64_t)w.list.ctas * 2 * kRows / kWarps, st, p, w);
+  }
+  const int64_t rows = (int64_t)p.B * p.H * p.Sq;
+  if (w.splits > 8 && rows <= 8 * kSms) return launch(merge_kernel<T, D, 4>, rows, st, p, w, cuts);   // while all run at once
+  return launch(merge_kernel<T, D, 1>, (rows + kWarps - 1) / kWarps, st, p, w, cuts);
 }
 
 }  // namespace
 }  // namespace shr
 
-cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const Split& s, const paged::Work* own,
-                                cudaStream_t st) {
+cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const paged::Work* own, cudaStream_t st) {
   shr::Cuts cuts{};
   if (own && own->own.note) cuts = {own->part_o, own->part_m, own->part_l, own->own.note, own->heads, own->n_hc};
-  return p.dtype == ATTN_F16 ? shr::launch_t<__half>(p, w, s, cuts, st)
-                             : shr::launch_t<__nv_bfloat16>(p, w, s, cuts, st);
+  if (p.dtype == ATTN_F16)
+    return p.D == 64 ? shr::merge<__half, 64>(p, w, cuts, st) : shr::merge<__half, 128>(p, w, cuts, st);
+  return p.D == 64 ? shr::merge<__nv_bfloat16, 64>(p, w, cuts, st) : shr::merge<__nv_bfloat16, 128>(p, w, cuts, st);
 }
 
 }  // namespace attn

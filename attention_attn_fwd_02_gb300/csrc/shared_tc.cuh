@@ -62,7 +62,7 @@ struct Item {
   int t0, np, o0, n;     // np prefix tiles from t0, then n - np own tiles from o0
   int n0;                // the tiles of row tile 0: the first n0 (not alt)
   int own_end;           // own keys that some row of the block sees
-  int alt, some1, slot;  // key tiles in turn; row tile 1 has rows; first partial result
+  int alt, some1, slot;  // key tiles in turn; row tile 1 has rows; the partial result (-1: O is written)
   __device__ __forceinline__ bool has(int t, int i) const {
     return alt ? (i & 1) == t : t ? some1 != 0 : i < n0;
   }
@@ -73,6 +73,7 @@ struct Bars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t item_full[2], item_empty[2];
+  uint64_t pair_have, pair_done;
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
@@ -119,18 +120,18 @@ __device__ __forceinline__ int own_seen(const Problem& p, int b, int i) { return
 template <int D, bool BF16, bool XF>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const Problem p, const Ext x, const __grid_constant__ Work w, const int wide_rows, const int drop_first_copy,
-                     const Split sp) {
+                     const Problem p, const Ext x, const __grid_constant__ Work w, const int wide_rows,
+                     const int drop_first_copy) {
   using C = Cfg<D>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* q_s = smem;
+  uint8_t* q_s = smem_raw;   // (on a 1024-byte boundary: launch() has looked)
   const int n_slots = C::kTiles - (w.one_tile ? 1 : 2);
   uint8_t* ring = q_s + (C::kTiles - n_slots) * C::kTile;
   __shared__ Bars sb;
   __shared__ Item items[2];
   __shared__ uint32_t no_page[kNotes];   // of a key tile: which of its pieces have no page
+  __shared__ float2 pair_ml[2][BM];      // items of one row tile: reference maxima and sums of both halves of the keys
 
   using S = Scores<XF>;   // (masks come with XF)
   constexpr float kRise = XF ? kSlack * kLn2 : kSlack;   // in the units of the scores
@@ -138,13 +139,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (2^-25) is 2^-30 of the row's largest probability (window_tc.cuh).
   constexpr float kLead = (BF16 ? 0.f : 5.f) * (XF ? kLn2 : 1.f);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  __shared__ int items_a, my_items;   // this CTA's prefix items (in front), and all of its items
+  __shared__ int items_a, my_items;   // this CTA's items of the list (in front), and all of its items
 
   paged::let_next_start();
   if (threadIdx.x == 32) {
     int n = 0;
-    if (const int c = blockIdx.x; c < w.pre.ctas) {
-      const int u0 = w.pre.unit[c], u1 = w.pre.unit[c + 1], t0 = w.pre.tile[c], t1 = w.pre.tile[c + 1];
+    if (const int c = blockIdx.x; c < w.list.ctas) {
+      const int u0 = w.list.unit[c], u1 = w.list.unit[c + 1], t0 = w.list.tile[c], t1 = w.list.tile[c + 1];
       n = u1 > u0 ? u1 - u0 + (t1 > 0) : t1 > t0;
     }
     items_a = n;
@@ -168,6 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sb.item_full[i], 32);
       mbar_init(&sb.item_empty[i], 3 + 2 * BM);   // the copy and MMA warps and every softmax thread
     }
+    mbar_init(&sb.pair_have, 2 * BM);
+    mbar_init(&sb.pair_done, 2 * BM);
     mbar_init(&sb.mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -185,48 +188,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // ---------------- items ----------------
     const int c = min((int)blockIdx.x, kSms - 1);
-    int u = w.pre.unit[c], tile = w.pre.tile[c];
+    const int pre = p.prefix / BN + (p.prefix % BN > 0);   // the prefix's tiles
+    int u = w.list.unit[c], tile = w.list.tile[c];
     for (int k = 0; k < my_items; ++k) {
       const int buf = k & 1;
       if (k >= 2 && !wait_warp(&sb.item_empty[buf], (uint32_t)((k >> 1) - 1) & 1u, &sb.abort, p.status)) break;
-      const int all = p.prefix / BN + (p.prefix % BN > 0);   // the prefix's tiles
       Item it;
-      int i0, i1;
-      if (k < items_a) {
+      const bool ends = k < items_a && u == w.list.unit[c + 1];   // the share ends in the middle of the unit
+      if (k < items_a && !w.joined) {
+        const int blk = u % w.blocks;
         it.b = -1;
-        it.g = u / w.pre.blocks;
-        it.row0 = u % w.pre.blocks * 2 * BM;
+        it.g = u / w.blocks;
+        it.row0 = blk * 2 * BM;
         it.rows = p.B * p.Sq * p.qpg;
         it.own_end = 0;
-        it.alt = w.pre.is_alt(u);
-        it.slot = (k == 0 ? w.pre.frag[c] : 0) << it.alt;   // (a unit that begins here has its first fragment here)
+        it.alt = w.is_alt(blk);
+        it.slot = k == 0 ? w.list.frag[c] : 0;   // (a unit that begins here has its first fragment here)
         it.t0 = tile;
-        it.np = it.n = it.n0 = (u == w.pre.unit[c + 1] ? w.pre.tile[c + 1] : w.pre.tiles) - tile;
+        it.np = it.n = it.n0 = (ends ? w.list.tile[c + 1] : pre) - tile;
         it.o0 = 0;
-        ++u;
-        tile = 0;
-      } else {   // the last row blocks, which see the most keys, first
-        int rest = (int)blockIdx.x + (k - items_a) * (int)gridDim.x;
-        const int part = rest % w.parts_b;
-        rest /= w.parts_b;
-        it.g = rest % p.G;
-        rest /= p.G;
-        it.b = rest % p.B;
-        const int blk = w.blocks_b - 1 - rest / p.B;
+        if (!ends && lane == 0) w.note[u] = it.slot + 1;
+      } else {
+        // The rows of one entry: a unit's part of its list, or an item's.
+        int blk, np = 0, part = 0;
+        if (w.joined) {
+          const int rest = u / p.G;
+          it.g = u - rest * p.G;
+          it.b = rest % p.B;
+          blk = w.blocks - 1 - rest / p.B;
+          it.alt = w.is_alt(blk);
+          it.slot = tile > 0 ? 0 : ends ? 1 : -1;
+          np = pre;
+        } else {
+          int rest = (int)blockIdx.x + (k - items_a) * (int)gridDim.x;
+          part = rest % w.parts_b;
+          rest /= w.parts_b;
+          it.g = rest % p.G;
+          rest /= p.G;
+          it.b = rest % p.B;
+          blk = w.blocks_b - 1 - rest / p.B;
+          it.alt = w.alt_b && blk == w.blocks_b - 1;
+          it.slot = w.own_slot + part;
+        }
         it.row0 = blk * 2 * BM;
         it.rows = p.Sq * p.qpg;
         it.own_end = own_seen(p, it.b, (min(it.row0 + 2 * BM, it.rows) - 1) / p.qpg);
         const int end0 = own_seen(p, it.b, (min(it.row0 + BM, it.rows) - 1) / p.qpg);
-        it.alt = w.alt_b;
-        it.slot = w.own_slot + (part << w.alt_b);
-        const int np = w.joined ? all : 0;
-        list_part(np + (it.own_end + BN - 1) / BN, part, w.parts_b, i0, i1);
+        int i0, i1;
+        const int all = np + (it.own_end + BN - 1) / BN;
+        if (w.joined) {
+          i0 = min(tile, all);
+          i1 = ends ? min(w.list.tile[c + 1], all) : all;
+        } else {
+          list_part(all, part, w.parts_b, i0, i1);
+        }
         it.t0 = min(i0, np);
         it.np = min(i1, np) - it.t0;
         it.o0 = max(i0 - np, 0);
         it.n = i1 - i0;
         it.n0 = min(max(np + (end0 + BN - 1) / BN - i0, 0), it.n);
       }
+      ++u;
+      tile = 0;
       it.some1 = it.row0 + BM < it.rows;
       if (lane == 0) items[buf] = it;
       __syncwarp();
@@ -490,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int j = 0;    // key tiles so far
     int gt = 0;   // key tiles of the items so far
-    uint32_t alt_phase = 0u;
+    uint32_t alt_phase = 0u, pair_phase = 0u;
     bool ok = my_items > 0 && wait_warp(&sb.item_full[0], 0u, &sb.abort, p.status);
     if (ok) load_q(items[0]);
     for (int k = 0; ok && k < my_items; ++k) {
@@ -652,41 +675,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue: O / l, special rows, LSE ----
       if (done > 0 && !(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
       fence_after();
-      const bool split = w.splits > 1;
+      // One row tile: each half of the keys has a result of every row, and each half of the threads takes half of the
+      // columns of both.  f: what this thread's own and the other result are weighed with.
+      const bool pair = it.alt && n > 1;
+      float f_own = 1.f, f_other = 0.f;
+      if (pair) {
+        pair_ml[t][r] = make_float2(m_ref, l);
+        fence_before();
+        mbar_arrive(&sb.pair_have);
+        if (!(ok = wait_warp(&sb.pair_have, pair_phase, &sb.abort, p.status))) break;
+        fence_after();
+        const float2 other = pair_ml[t ^ 1][r];
+        const float top = fmaxf(m_ref, other.x), mu = top == -INFINITY ? 0.f : top;
+        f_own = S::weight(m_ref, mu);
+        f_other = S::weight(other.x, mu);
+        l = t ? fmaf(f_other, other.y, f_own * l) : fmaf(f_own, l, f_other * other.y);   // (the same bits in both)
+        m_ref = top;
+      }
+      const bool split = it.slot >= 0;
+      const int c_begin = pair ? t * (D / 64) : 0, c_end = pair ? (t + 1) * (D / 64) : it.alt && t ? 0 : D / 32;
       // The sink logit joins the denominator (and rescales the accumulated O); with parts the merge adds it once.
       float M = S::natural(m_ref);
       const float o_mul = p.sink_on && !split && valid ? fold_sink<false>(M, l, sink_logit(p, h)) : 1.f;
       const bool hidden_row = (l == 0.f);         // no visible key; a NaN l stays a NaN row
-      const float inv = o_mul / l;
+      const float inv = o_mul / l, inv_own = inv * f_own, inv_other = inv * f_other;
       const float fill = p.masked_zero ? 0.f : NAN;
       T* orow = static_cast<T*>(p.O) + p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs + (int64_t)qi * p.o.rs;
-      const int64_t prow = (((int64_t)b * p.H + h) * p.Sq + qi) * w.splits + it.slot + (it.alt ? t : 0);
-      float* po = split ? sp.part_o + prow * D : nullptr;
+      const int64_t prow = w.joined ? ((int64_t)blockIdx.x * 2 + it.slot) * (2 * BM) + (it.alt ? r : t * BM + r)
+                                    : (((int64_t)b * p.H + h) * p.Sq + qi) * w.splits + it.slot;
+      float* po = w.part_o + prow * D;   // (not used when O is written)
+      const uint32_t other_tm = tmem + lane_off + (t ? C::kO0 : C::kO1);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = c_begin; c < c_end; ++c) {
         uint32_t o[32];
         if (done > 0) {
           tmem_ld32(o_tm + c * 32, o);
           tmem_ld_wait_regs<1>(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv_own);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
+        if (pair) {
+          uint32_t o2[32];
+          tmem_ld32(other_tm + c * 32, o2);
+          tmem_ld_wait_regs<1>(o2);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(fmaf(__uint_as_float(o2[e]), inv_other, __uint_as_float(o[e])));
+        }
         if (split) {
           if (valid && !hidden_row) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
 #pragma unroll
             for (int e = 0; e < 32; e += 8) store32(po + c * 32 + e, o + e);
           }
         } else {
           uint32_t y[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float a = hidden_row ? fill : __uint_as_float(o[e]) * inv;
-            const float bb = hidden_row ? fill : __uint_as_float(o[e + 1]) * inv;
-            y[e / 2] = pack2<BF16>(a, bb);
-          }
+          for (int e = 0; e < 32; e += 2)
+            y[e / 2] = pack2<BF16>(hidden_row ? fill : __uint_as_float(o[e]), hidden_row ? fill : __uint_as_float(o[e + 1]));
           if (valid) {
             if (wide_rows) {
               store32(orow + c * 32, y);
@@ -700,13 +748,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (valid) {
+      if (valid && !(it.alt && t)) {
         if (split) {
-          sp.part_lse[prow] = hidden_row ? -INFINITY : M;
-          sp.part_l[prow] = l;
+          w.part_m[prow] = hidden_row ? -INFINITY : M;
+          w.part_l[prow] = l;
         } else if (p.lse) {
           p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + qi] = hidden_row ? -INFINITY : S::lse(M, __log2f(l));
         }
+      }
+      if (pair) {   // both are done with both results, before either goes on to the next item's
+        fence_before();
+        mbar_arrive(&sb.pair_done);
+        if (!(ok = wait_warp(&sb.pair_done, pair_phase, &sb.abort, p.status))) break;
+        pair_phase ^= 1u;
       }
       fence_before();   // O's loads come before the next item's P, and so before its P V
       mbar_arrive(&sb.item_empty[buf]);
@@ -724,21 +778,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- host side -----------------------------------------------------------------------
 
 template <int D, bool BF16, bool XF>
-int launch(const Problem& p, const Ext& x, const Work& w, const Split& sp, cudaStream_t st) {
+int launch(const Problem& p, const Ext& x, const Work& w, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!tma_map_bhsd(&mk, p.K, p.dtype, D, x.page_size, p.G, (int)x.n_pages, p.k, w.piece) ||
       !tma_map_bhsd(&mv, p.V, p.dtype, D, x.page_size, p.G, (int)x.n_pages, p.v, w.piece))
     return -1;  // not describable: caller falls back
-  const int smem = Cfg<D>::kSmem + 1024;
+  const int smem = Cfg<D>::kSmem;
   auto kern = shared_tc_kernel<D, BF16, XF>;
   // setmaxnreg.inc waits until the block's register pool holds the larger
-  // count, so the pool the kernel is launched with must cover the split.
-  static const bool regs_ok = [] {
+  // count, so the pool the kernel is launched with must cover the split.  The
+  // tiles fill what the kernel's own variables leave of the shared memory, and
+  // lie on the swizzle's 1024-byte boundaries: the compiler pads the variables
+  // to the alignment of the array behind them.
+  static const bool fits = [] {
     cudaFuncAttributes a;
     if (cudaFuncGetAttributes(&a, (const void*)shared_tc_kernel<D, BF16, XF>) != cudaSuccess) return false;
-    return a.numRegs * kThreads >= kSplitRegs;
+    return a.numRegs * kThreads >= kSplitRegs && a.sharedSizeBytes % 1024 == 0 &&
+           a.sharedSizeBytes + Cfg<D>::kSmem <= 227 * 1024;
   }();
-  if (!regs_ok) return -1;
+  if (!fits) return -1;
   if (ensure_smem((const void*)kern, smem) != cudaSuccess) return ATTN_ERR_CUDA;
   // Rows of O on 32-byte boundaries take 32-byte stores.
   auto even = [](int64_t stride, int64_t extent) { return extent <= 1 || stride % 16 == 0; };
@@ -747,17 +805,17 @@ int launch(const Problem& p, const Ext& x, const Work& w, const Split& sp, cudaS
                        ? 1
                        : 0;
   const int drop = take_injection() == ATTN_INJECT_DROP_FIRST_COPY ? 1 : 0;
-  const int ctas = w.pre.ctas > w.n_b ? w.pre.ctas : w.n_b;
-  kern<<<(unsigned)(ctas < kSms ? ctas : kSms), kThreads, smem, st>>>(mk, mv, p, x, w, wide, drop, sp);
+  const int ctas = w.list.ctas > w.n_b ? w.list.ctas : w.n_b;
+  kern<<<(unsigned)(ctas < kSms ? ctas : kSms), kThreads, smem, st>>>(mk, mv, p, x, w, wide, drop);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 template <int D>
-int launch_d(const Problem& p, const Ext& x, const Work& w, const Split& sp, cudaStream_t st) {
+int launch_d(const Problem& p, const Ext& x, const Work& w, cudaStream_t st) {
   const bool xf = p.M != nullptr || p.softcap > 0.f || !(p.scale * kLog2e > 0.f);
   if (p.dtype == ATTN_BF16)
-    return xf ? launch<D, true, true>(p, x, w, sp, st) : launch<D, true, false>(p, x, w, sp, st);
-  return xf ? launch<D, false, true>(p, x, w, sp, st) : launch<D, false, false>(p, x, w, sp, st);
+    return xf ? launch<D, true, true>(p, x, w, st) : launch<D, true, false>(p, x, w, st);
+  return xf ? launch<D, false, true>(p, x, w, st) : launch<D, false, false>(p, x, w, st);
 }
 
 }  // namespace shr

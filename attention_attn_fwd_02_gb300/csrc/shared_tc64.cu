@@ -2,7 +2,7 @@
 #include "shared_tc.cuh"
 
 namespace attn {
-int shared_tc64(const Problem& p, const Ext& x, const shr::Work& w, const Split& sp, cudaStream_t st) {
-  return shr::launch_d<64>(p, x, w, sp, st);
+int shared_tc64(const Problem& p, const Ext& x, const shr::Work& w, cudaStream_t st) {
+  return shr::launch_d<64>(p, x, w, st);
 }
 }  // namespace attn
