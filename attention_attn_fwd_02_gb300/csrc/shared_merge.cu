@@ -140,6 +140,145 @@ __device__ __forceinline__ void merge_row(const Problem& p, bool here, int64_t b
     p.lse[b * p.lse_bs + (int64_t)h * p.lse_hs + i] = nan ? NAN : none ? -INFINITY : M + logf(sum);
 }
 
+// The same for up to kFew results of a row: a lane takes the same four columns of kRowsFew rows (of two rows in turn at
+// head_dim 64), whose loads are all under way together.  row_of: a row's place, its results' places and how many there
+// are (0: there is no such row), without a look at the maxima and sums that it fetches meanwhile.
+constexpr int kFew = 4;
+constexpr int kRowsFew = 2;
+
+struct FewRow {
+  bool here;
+  int b, h, i, n;
+  int64_t at[kFew];
+  float m[kFew], l[kFew];
+  __device__ __forceinline__ void fetch(const Work& w, int most) {
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+      m[k] = here && k < most ? w.part_m[at[k]] : -INFINITY;
+      l[k] = here && k < most ? w.part_l[at[k]] : 0.f;
+    }
+  }
+};
+
+template <typename T, int D>
+__device__ __forceinline__ void merge_few(const Problem& p, const Work& w, FewRow (&row)[kRowsFew]) {
+  constexpr int kCols = D / 4;
+  const int d = threadIdx.x % kCols * 4;
+  float4 v[kRowsFew][kFew];
+#pragma unroll
+  for (int q = 0; q < kRowsFew; ++q)
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+      if (k >= row[q].n) row[q].m[k] = -INFINITY;
+      v[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row[q].m[k] != -INFINITY) v[q][k] = *reinterpret_cast<const float4*>(w.part_o + row[q].at[k] * D + d);
+    }
+#pragma unroll
+  for (int q = 0; q < kRowsFew; ++q) {
+    const FewRow& r = row[q];
+    if (!r.here) continue;
+    const float sg = p.sink_on ? sink_logit(p, r.h) : -INFINITY;
+    bool bad = isnan(sg) || sg == INFINITY;
+    float M = bad ? -INFINITY : sg;
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+      if (!(r.m[k] < INFINITY)) bad = true;   // +inf or NaN
+      else M = fmaxf(M, r.m[k]);
+    }
+    const float mu = M == -INFINITY ? 0.f : M;
+    float sum = sg > -INFINITY ? expf(sg - mu) : 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+      if (r.m[k] == -INFINITY) continue;
+      const float f = r.l[k] * expf(r.m[k] - mu);
+      sum += f;
+      acc.x = fmaf(f, v[q][k].x, acc.x);
+      acc.y = fmaf(f, v[q][k].y, acc.y);
+      acc.z = fmaf(f, v[q][k].z, acc.z);
+      acc.w = fmaf(f, v[q][k].w, acc.w);
+    }
+    const bool nan = bad || isnan(sum), none = !nan && M == -INFINITY;
+    const float fill = none && p.masked_zero ? 0.f : NAN, inv = 1.f / sum;
+    T* out = static_cast<T*>(p.O) + p.o.off + r.b * p.o.bs + r.h * p.o.hs + r.i * p.o.rs + d;
+    const float a[4] = {acc.x, acc.y, acc.z, acc.w};
+    __align__(8) T y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(nan || none ? fill : a[e] * inv);
+    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+    if (p.lse && d == 0)
+      p.lse[r.b * p.lse_bs + r.h * p.lse_hs + r.i] = nan ? NAN : none ? -INFINITY : M + logf(sum);
+  }
+}
+
+// packed, with at most kFew results of a row (no decode pass among them).
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kWarps, 6) merge_few_kernel(const Problem p, const __grid_constant__ Work w) {
+  constexpr int kTeams = 128 / D;   // rows that a warp's lanes hold side by side
+  const uint32_t rows = (uint32_t)p.B * p.H * p.Sq, per_entry = (uint32_t)p.H * p.Sq;
+  const uint32_t row0 = (blockIdx.x * kWarps + threadIdx.x / 32) * (kRowsFew * kTeams) + threadIdx.x % 32 / (D / 4);
+  FewRow row[kRowsFew];
+  const int* note[kRowsFew];
+#pragma unroll
+  for (int q = 0; q < kRowsFew; ++q) {
+    FewRow& r = row[q];
+    const uint32_t id = row0 + q * kTeams;
+    r.here = id < rows;
+    const uint32_t in = id % per_entry;
+    r.b = (int)(id / per_entry);
+    r.h = (int)(in / (uint32_t)p.Sq);
+    r.i = (int)(in - r.h * (uint32_t)p.Sq);
+    const uint32_t g = (uint32_t)r.h / p.qpg, packed = ((uint32_t)r.b * p.Sq + r.i) * p.qpg + r.h - g * p.qpg;
+    note[q] = w.note + (r.here ? g * w.blocks + packed / (2 * kRows) : 0);
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) r.at[k] = (int64_t)id * w.splits + k;   // (by slot, so far)
+  }
+  paged::wait_for_previous();
+  int n_a[kRowsFew];
+#pragma unroll
+  for (int q = 0; q < kRowsFew; ++q) {
+    n_a[q] = *note[q];
+    row[q].fetch(w, w.splits);
+  }
+#pragma unroll
+  for (int q = 0; q < kRowsFew; ++q) {   // slots that the row does not use count as empty
+    row[q].n = row[q].here ? w.splits : 0;
+#pragma unroll
+    for (int k = 0; k < kFew; ++k)
+      if (k >= n_a[q] && k < w.own_slot) row[q].m[k] = -INFINITY;
+  }
+  merge_few<T, D>(p, w, row);
+}
+
+// joined, with at most kFew fragments of a unit.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kWarps, 6) join_few_kernel(const Problem p, const __grid_constant__ Work w) {
+  constexpr int kTeams = 128 / D, kPer = kWarps * kRowsFew * kTeams;   // rows of a CTA
+  const int c = blockIdx.x / (2 * kRows / kPer);
+  const int local0 =
+      blockIdx.x % (2 * kRows / kPer) * kPer + threadIdx.x / 32 * (kRowsFew * kTeams) + threadIdx.x % 32 / (D / 4);
+  if (w.list.tile[c] == 0 || w.list.unit[c + 1] == w.list.unit[c]) return;
+  const int u = w.list.unit[c], n = w.list.frag[c] + 1, c0 = c - w.list.frag[c];
+  const int row0 = w.block_of(u, p.B, p.G) * 2 * kRows, g = u % p.G, b = u / p.G % p.B;
+  FewRow row[kRowsFew];
+#pragma unroll
+  for (int q = 0; q < kRowsFew; ++q) {
+    FewRow& r = row[q];
+    const int local = local0 + q * kTeams;
+    r.b = b;
+    r.i = (row0 + local) / p.qpg;
+    r.h = g * p.qpg + row0 + local - r.i * p.qpg;
+    r.here = r.i < p.Sq;
+    r.n = r.here ? n : 0;
+#pragma unroll
+    for (int f = 0; f < kFew; ++f) r.at[f] = ((int64_t)(c0 + f) * 2 + (f == 0 ? 1 : 0)) * (2 * kRows) + local;
+  }
+  paged::wait_for_previous();
+#pragma unroll
+  for (int q = 0; q < kRowsFew; ++q) row[q].fetch(w, n);
+  merge_few<T, D>(p, w, row);
+}
+
 // packed: a row's results are its unit's fragments and then its own keys' (shared.h).
 template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(32 * kWarps, 8)
@@ -217,13 +356,15 @@ cudaError_t launch(void (*kern)(Args...), int64_t blocks, cudaStream_t st, Args.
 
 template <typename T, int D>
 cudaError_t merge(const Problem& p, const Work& w, const Cuts& cuts, cudaStream_t st) {
+  constexpr int kPer = kWarps * kRowsFew * (128 / D);   // rows of a CTA that merges few results of each
   if (w.joined) {
     int most = 0;
     for (int c = 0; c < w.list.ctas; ++c) most = w.list.frag[c] > most ? w.list.frag[c] : most;
-    if (most >= 4) return launch(join_kernel<T, D, 4>, (int64_t)w.list.ctas * 2 * kRows, st, p, w);
-    return launch(join_kernel<T, D, 1>, (int64_t)w.list.ctas * 2 * kRows / kWarps, st, p, w);
+    if (most >= kFew) return launch(join_kernel<T, D, 4>, (int64_t)w.list.ctas * 2 * kRows, st, p, w);
+    return launch(join_few_kernel<T, D>, (int64_t)w.list.ctas * 2 * kRows / kPer, st, p, w);
   }
   const int64_t rows = (int64_t)p.B * p.H * p.Sq;
+  if (w.splits <= kFew && !cuts.note) return launch(merge_few_kernel<T, D>, (rows + kPer - 1) / kPer, st, p, w);
   if (w.splits > 8 && rows <= 8 * kSms) return launch(merge_kernel<T, D, 4>, rows, st, p, w, cuts);   // while all run at once
   return launch(merge_kernel<T, D, 1>, (rows + kWarps - 1) / kWarps, st, p, w, cuts);
 }

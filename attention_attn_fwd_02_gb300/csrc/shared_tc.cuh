@@ -60,9 +60,16 @@ struct Item {
   int b, g;              // b < 0: a prefix item
   int row0, rows;        // first row, and the rows there are
   int t0, np, o0, n;     // np prefix tiles from t0, then n - np own tiles from o0
+  int turn;              // the list is walked from tile `turn` of it on, and round
   int n0;                // the tiles of row tile 0: the first n0 (not alt)
   int own_end;           // own keys that some row of the block sees
   int alt, some1, slot;  // key tiles in turn; row tile 1 has rows; the partial result (-1: O is written)
+  // The i-th tile of the walk: whether it is the prefix's, and its first key there.
+  __device__ __forceinline__ int key(int i, bool& pre) const {
+    i += i < n - turn ? turn : turn - n;
+    pre = i < np;
+    return (pre ? t0 + i : o0 + i - np) * kKeys;
+  }
   __device__ __forceinline__ bool has(int t, int i) const {
     return alt ? (i & 1) == t : t ? some1 != 0 : i < n0;
   }
@@ -189,11 +196,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- items ----------------
     const int c = min((int)blockIdx.x, kSms - 1);
     const int pre = p.prefix / BN + (p.prefix % BN > 0);   // the prefix's tiles
-    int u = w.list.unit[c], tile = w.list.tile[c];
+    int u = w.list.unit[c], tile = w.list.tile[c], walked = 0;
     for (int k = 0; k < my_items; ++k) {
       const int buf = k & 1;
       if (k >= 2 && !wait_warp(&sb.item_empty[buf], (uint32_t)((k >> 1) - 1) & 1u, &sb.abort, p.status)) break;
       Item it;
+      it.turn = 0;
+      if (!w.joined && k < items_a) {
+        // The share's last unit first: it may walk its tiles from the first on, as all CTAs then do side by side, and the
+        // others go on from where it ends (`walked`).  CTAs that read the same tiles at the same time read them out of
+        // their die's L2.
+        u = k == 0 ? w.list.unit[c] + items_a - 1 : w.list.unit[c] + k - 1;
+        tile = u == w.list.unit[c] ? w.list.tile[c] : 0;
+      }
       const bool ends = k < items_a && u == w.list.unit[c + 1];   // the share ends in the middle of the unit
       if (k < items_a && !w.joined) {
         const int blk = u % w.blocks;
@@ -203,10 +218,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.rows = p.B * p.Sq * p.qpg;
         it.own_end = 0;
         it.alt = w.is_alt(blk);
-        it.slot = k == 0 ? w.list.frag[c] : 0;   // (a unit that begins here has its first fragment here)
+        it.slot = tile > 0 ? w.list.frag[c] : 0;   // (a unit that begins here has its first fragment here)
         it.t0 = tile;
         it.np = it.n = it.n0 = (ends ? w.list.tile[c + 1] : pre) - tile;
         it.o0 = 0;
+        const int at = walked % pre - tile;
+        it.turn = at > 0 && at < it.n ? at : 0;
+        walked += it.n;
         if (!ends && lane == 0) w.note[u] = it.slot + 1;
       } else {
         // The rows of one entry: a unit's part of its list, or an item's.
@@ -266,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int at = chunk * BN * 128 + piece * w.piece * 128;
     // This lane's piece of tile i of an item: its page (n_pages behind the last key, -1: there is none) and row in it.
     auto look_up = [&](const Item& it, int i, int& row) {
-      const bool pre = i < it.np;
-      const int r = (pre ? it.t0 + i : it.o0 + i - it.np) * BN + piece * w.piece;
+      bool pre;
+      const int r = it.key(i, pre) + piece * w.piece;
       row = 0;
       if (r >= (pre ? p.prefix : it.own_end)) return (int)x.n_pages;
       const int pi = page_index(x, r);
@@ -350,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Zeroes the V rows of a tile's keys that no row of the item sees (they may hold anything).
     auto clear_tail = [&](const Item& it, int i, int s) {
-      const bool pre = i < it.np;
-      const int seen = (pre ? p.prefix - (it.t0 + i) * BN : it.own_end - (it.o0 + i - it.np) * BN);
+      bool pre;
+      const int k0 = it.key(i, pre), seen = (pre ? p.prefix : it.own_end) - k0;
       if (seen >= BN) return;
       for (int u = seen * (C::kChunks * 8) + lane; u < BN * (C::kChunks * 8); u += 32) {
         const int row = u / (C::kChunks * 8), rest = u % (C::kChunks * 8);
@@ -523,8 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int b, qi, h;
       const bool valid = row_of(it, b, qi, h);
       const bool idle = !__any_sync(0xffffffffu, valid);   // no row of this warp exists: its P is not used
-      // Keys of the prefix and own keys that the row sees; a row that does not exist hides nothing.
-      const int seen_pre = valid ? p.prefix : 0x7fffffff;
+      // Own keys that the row sees (the prefix's are all seen); a row that does not exist hides nothing.
       const int seen_own = !valid ? 0x7fffffff : it.b < 0 ? 0 : own_seen(p, b, qi);
       const float* mrow = nullptr;
       if (XF && p.M && valid)
@@ -535,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!it.has(t, i)) continue;
         if (!(ok = wait_warp(&sb.s_full[t], (uint32_t)j & 1u, &sb.abort, p.status))) break;
         fence_after();
-        const bool pre = i < it.np;
-        const int k0 = (pre ? it.t0 + i : it.o0 + i - it.np) * BN;
-        const int seen_n = (pre ? seen_pre : seen_own) - k0;   // the row sees the tile's first seen_n keys
+        bool pre;
+        const int k0 = it.key(i, pre);
+        const int seen_n = (pre && valid ? p.prefix : seen_own) - k0;   // the row sees the tile's first seen_n keys
         const uint32_t missing = no_page[(gt + i) % kNotes];
         // Which of columns 32 c .. of the tile the row sees.
         auto seen_bits = [&](int c) {
