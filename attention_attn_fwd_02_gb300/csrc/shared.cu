@@ -27,11 +27,11 @@ struct Run {
   int64_t cost() const { return tiles * tile + Shares::kEnd; }
 };
 
-// The runs of a plan's list, in its order.  step(i, run): the i-th of them; the return value says how many there are.
+// The runs of a plan's list, in its order; joined: the first `units` units (the others are dealt whole).
 struct Runs {
   const Problem& p;
   const Work& w;
-  int64_t pre;
+  int64_t pre, units = 0;
   int64_t size() const { return w.joined ? w.blocks : 2 * (int64_t)p.G; }
   Run at(int64_t i) const {
     if (!w.joined) {   // a kv head's blocks of two row tiles, then the one that may have one
@@ -39,6 +39,7 @@ struct Runs {
       return {last ? w.alt : w.blocks - w.alt, pre, last ? Shares::kTileAlt : Shares::kTile};
     }
     const int blk = w.blocks - 1 - (int)i;
+    const int64_t per = (int64_t)p.B * p.G;
     const int64_t rows = (int64_t)p.Sq * p.qpg, end = (int64_t)(blk + 1) * 2 * kRows;
     const int64_t q = ((end < rows ? end : rows) - 1) / p.qpg;   // the block's last query
     int64_t own = p.Sk - p.prefix;
@@ -47,7 +48,7 @@ struct Runs {
       own = clamp64(seen, 0, own);
     }
     const int64_t tiles = pre + ceil_div(own, kKeys);   // (rows without keys have a unit too)
-    return {(int64_t)p.B * p.G, tiles > 0 ? tiles : 1, w.is_alt(blk) ? Shares::kTileAlt : Shares::kTile};
+    return {clamp64(units - i * per, 0, per), tiles > 0 ? tiles : 1, w.is_alt(blk) ? Shares::kTileAlt : Shares::kTile};
   }
   int64_t total() const {
     int64_t t = 0;
@@ -56,27 +57,22 @@ struct Runs {
   }
 };
 
-// Cuts the list into s.ctas shares (each is to have a tile's cost at least), in the middle of units or, with `whole`,
-// at the nearest border of two.  Returns the most fragments of a unit.
-int cut(const Runs& runs, int64_t total, bool whole, Shares& s) {
+// Cuts the list into s.ctas shares (each is to have a tile's cost at least).  Returns the most fragments of a unit.
+// The first `more` shares cost `less` less than the others (the total counts that of all shares in).
+int cut(const Runs& runs, int64_t total, Shares& s, int64_t less = 0, int more = 0) {
   int64_t i = 0, first = 0, begin = 0;   // run, its first unit, and where that begins
   Run run = runs.at(0);
   int most = 1;
   for (int c = 0; c <= s.ctas; ++c) {
-    const int64_t t = total / s.ctas * c + total % s.ctas * c / s.ctas;
+    const int64_t t = total / s.ctas * c + total % s.ctas * c / s.ctas - less * (c < more ? c : more);
     while (i + 1 < runs.size() && t - begin >= run.count * run.cost()) {
       begin += run.count * run.cost();
       first += run.count;
       run = runs.at(++i);
     }
     const int64_t k = clamp64((t - begin) / run.cost(), 0, run.count);   // the units in front, of this run
-    int64_t at = (t - begin - k * run.cost()) / run.tile;
-    bool next = at >= run.tiles;   // in a unit's end
-    if (whole) {
-      next = 2 * at >= run.tiles;
-      at = 0;
-    }
-    if (k == run.count) next = false;
+    const int64_t at = (t - begin - k * run.cost()) / run.tile;
+    const bool next = k < run.count && at >= run.tiles;   // in a unit's end
     s.unit[c] = (int)(first + k + next);
     s.tile[c] = next || k == run.count ? 0 : (int)at;
     if (c == s.ctas) break;
@@ -144,7 +140,7 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
       ctas = (int)(kSms * (us_all + kPass) / (us_all + us_own + 2 * kPass));
     }
     w.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, ctas);
-    w.own_slot = cut(runs, total, false, w.list);
+    w.own_slot = cut(runs, total, w.list);
     us_packed = kPass + kMerge + (double)total / w.list.ctas * kUnit + w.own_slot * part_us;
     w.one_tile = all <= kRows;
     w.own_sms = kSms - w.list.ctas;
@@ -163,25 +159,44 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   if (items > 0x3fffffff / kMaxParts) return false;
   double us_own = 0;
   w.parts_b = own > 0 ? best_parts(items, own, rows <= kRows, part_us, &us_own) : 0;
-  w.splits = w.own_slot + w.parts_b;
   w.n_b = (int)items * w.parts_b;
   us_packed += us_own;
+  if (pre > 0 && w.n_b > 0) {
+    // CTAs with an entry item more than the others have less of the prefix, by what items cost whose lists are half as
+    // long as they can be.
+    const Runs packed{p, w, pre};
+    const int64_t less = ceil_div(own, 2 * w.parts_b) * (rows <= kRows ? Shares::kTileAlt : Shares::kTile) + Shares::kEnd;
+    const int grid = w.n_b > w.list.ctas ? (w.n_b < kSms ? w.n_b : kSms) : w.list.ctas, more = w.n_b % grid;
+    const int64_t total = packed.total() + less * more;
+    if (grid == w.list.ctas && more > 0 && total / grid - less >= 2 * Shares::kTile)
+      w.own_slot = cut(packed, total, w.list, less, more);
+  }
+  w.splits = w.own_slot + w.parts_b;
   // Or each entry by itself: its rows walk the prefix and their own keys.
   Work v{};
   v.joined = 1;
   v.piece = w.piece;
-  v.blocks = w.blocks_b;
-  v.alt = w.alt_b;
+  v.blocks = v.blocks_b = w.blocks_b;
+  v.alt = v.alt_b = w.alt_b;
+  v.parts_b = 1;
   v.one_tile = rows <= kRows;
-  const Runs runs{p, v, pre};
+  const double us_all = (double)Runs{p, v, pre, items}.total() * kUnit;
+  const Runs runs{p, v, pre, items % kSms};
   const int64_t total = runs.total();
-  v.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, kSms);
-  // Cut units cost the write and the read of two fragments a share and the merge; whole ones leave the last shares' rest.
-  const double us_cut = kMerge + (double)v.list.ctas * 4 * kRows * p.D * 8 / 6.0e6;
-  const double us_unit = (double)runs.at(0).cost() * kUnit;
-  const bool whole = us_unit / 2 < us_cut && items >= v.list.ctas;
-  v.splits = cut(runs, total, whole, v.list) > 1;
-  const double us_joined = kPass + (double)total / v.list.ctas * kUnit + (whole ? us_unit / 2 : us_cut);
+  const int ctas = (int)clamp64(total / (2 * Shares::kTile), 1, kSms);
+  // Cut units cost the write and the read of about a fragment and a half a share, and the merge; uncut ones leave SMs
+  // without work for most of a unit's time.
+  const double us_cut = kMerge + (double)ctas * 3 * kRows * p.D * 8 / 6.0e6;
+  const double us_left = total ? (double)runs.at(0).cost() * kUnit - (double)total / kSms * kUnit : 0.0;
+  double us_joined = kPass + us_all / kSms + us_left;
+  v.n_b = (int)items;
+  if (us_cut < us_left) {
+    us_joined = kPass + us_all / kSms + us_cut;
+    v.list.ctas = ctas;
+    v.first_b = (int)(items % kSms);
+    v.n_b = (int)(items - v.first_b);
+    v.splits = cut(runs, total, v.list) > 1;
+  }
   if (!(us_packed < us_joined)) w = v;
   return true;
 }

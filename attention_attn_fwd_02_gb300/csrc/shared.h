@@ -18,7 +18,7 @@ constexpr int kSms = 152;
 // the host: the kernel's registers have no room for 64-bit divisions.)
 struct Shares {
   // Costs, about 0.2 us each: a key tile of both row tiles, of one, and what a fragment costs besides.
-  static constexpr int kTile = 7, kTileAlt = 4, kEnd = 10;
+  static constexpr int kTile = 7, kTileAlt = 4, kEnd = 20;
   int ctas;               // 0: there is no list
   int unit[kSms + 1];
   int tile[kSms + 1];
@@ -35,19 +35,21 @@ struct Shares {
 //            own keys', are merged.
 //   joined   A unit is a block of 256 rows of one entry (the last blocks, which
 //            see the most keys, in front, then entry by entry, kv head by kv
-//            head) and walks the prefix's tiles and behind them its own, as many as
-//            k_len allows: shares go by these, and an entry with fewer keys has
-//            shorter fragments.  Whole units write O; a share keeps its first
-//            fragment, where it began in the middle of a unit, and its last,
-//            where it ends in one, for the merge.
+//            head) and walks the prefix's tiles and behind them its own.  As many
+//            units as every CTA can have the same number of are dealt whole
+//            (entry items) and write O.  The list has those left over, by the own
+//            tiles that k_len allows (an entry with fewer keys has shorter
+//            fragments): a share keeps its first fragment, where it began
+//            in the middle of a unit, and its last, where it ends in one, for
+//            the merge.
 // A block whose rows fit one row tile (`alt`: the last one) deals its key tiles
 // to both row tiles of the kernel, which then hold the same rows, in turn.
 struct Work {
   Shares list;
   int joined;
   int blocks, alt;                // row blocks of a kv head (packed) or of an entry and kv head (joined)
-  int blocks_b, alt_b, parts_b;   // entry items (packed): row blocks of an entry and kv head, parts of their lists
-  int n_b;                        // entry items
+  int blocks_b, alt_b, parts_b;   // entry items: row blocks of an entry and kv head, parts of their lists
+  int n_b, first_b;               // entry items, and the first one's number
   int piece;                      // rows of a copy: the largest power of two up to 128 that divides a page
   int own_slot;                   // packed: first partial result of own keys
   int splits;                     // packed: partial results of a row.  joined: 1 if a share keeps any

@@ -22,9 +22,9 @@
 //     behind the pool: it arrives as zeros and counts its bytes;
 //   - K and V tiles alternate in one ring of as many slots as the shared memory
 //     holds: what is on its way bounds the rate that an SM reads at;
-//   - Q rows come from wherever (entry, query, head) puts them: each softmax
-//     thread loads its own row of the next item while the tensor cores finish
-//     the current one's, so rows pack without gaps whatever the strides.
+//   - Q rows come from wherever (entry, query, head) puts them, with cp.async
+//     by the warp that finds the items, as soon as the item in front has taken
+//     its last S: rows pack without gaps whatever the strides.
 // P enters the product as one value of the element type, as in attn_fwd.
 #pragma once
 
@@ -76,7 +76,7 @@ struct Item {
 };
 
 struct Bars {
-  uint64_t q_full[2], q_seen, q_empty;
+  uint64_t q_full, q_empty;
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t item_full[2], item_empty[2];
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = q_s + (C::kTiles - n_slots) * C::kTile;
   __shared__ Bars sb;
   __shared__ Item items[2];
-  __shared__ uint32_t no_page[kNotes];   // of a key tile: which of its pieces have no page
+  __shared__ uint2 notes[kNotes];        // of a key tile: which of its pieces have no page; its first key, + 1: the prefix's
   __shared__ float2 pair_ml[2][BM];      // items of one row tile: reference maxima and sums of both halves of the keys
 
   using S = Scores<XF>;   // (masks come with XF)
@@ -166,10 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sb.full[s], 1);
       mbar_init(&sb.empty[s], 1);
     }
-    mbar_init(&sb.q_seen, 1);
+    mbar_init(&sb.q_full, 32);
     mbar_init(&sb.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sb.q_full[i], BM);
       mbar_init(&sb.s_full[i], 1);
       mbar_init(&sb.p_full[i], BM);
       mbar_init(&sb.o_done[i], 1);
@@ -193,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    // ---------------- items ----------------
+    // ---------------- items, and their queries ----------------
+    constexpr int kUnits = D / 8, kRowsAt = 32 / kUnits;   // 16-byte units of a row; rows that a copy of all lanes takes
     const int c = min((int)blockIdx.x, kSms - 1);
     const int pre = p.prefix / BN + (p.prefix % BN > 0);   // the prefix's tiles
     int u = w.list.unit[c], tile = w.list.tile[c], walked = 0;
@@ -229,23 +229,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // The rows of one entry: a unit's part of its list, or an item's.
         int blk, np = 0, part = 0;
-        if (w.joined) {
-          const int rest = u / p.G;
-          it.g = u - rest * p.G;
-          it.b = rest % p.B;
-          blk = w.blocks - 1 - rest / p.B;
-          it.alt = w.is_alt(blk);
-          it.slot = tile > 0 ? 0 : ends ? 1 : -1;
-          np = pre;
-        } else {
-          int rest = (int)blockIdx.x + (k - items_a) * (int)gridDim.x;
+        int rest = u;
+        if (k >= items_a) {   // items in turn, to and fro: the ones in front are longer
+          const int round = k - items_a, grid = (int)gridDim.x;
+          rest = w.first_b + round * grid + (round % 2 && (round + 1) * grid <= w.n_b ? grid - 1 - (int)blockIdx.x
+                                                                                       : (int)blockIdx.x);
           part = rest % w.parts_b;
           rest /= w.parts_b;
-          it.g = rest % p.G;
-          rest /= p.G;
-          it.b = rest % p.B;
-          blk = w.blocks_b - 1 - rest / p.B;
-          it.alt = w.alt_b && blk == w.blocks_b - 1;
+        }
+        it.g = rest % p.G;
+        rest /= p.G;
+        it.b = rest % p.B;
+        blk = w.blocks_b - 1 - rest / p.B;
+        it.alt = w.alt_b && blk == w.blocks_b - 1;
+        if (w.joined) {
+          it.slot = k >= items_a ? -1 : tile > 0 ? 0 : ends ? 1 : -1;
+          np = pre;
+        } else {
           it.slot = w.own_slot + part;
         }
         it.row0 = blk * 2 * BM;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end0 = own_seen(p, it.b, (min(it.row0 + BM, it.rows) - 1) / p.qpg);
         int i0, i1;
         const int all = np + (it.own_end + BN - 1) / BN;
-        if (w.joined) {
+        if (k < items_a) {
           i0 = min(tile, all);
           i1 = ends ? min(w.list.tile[c + 1], all) : all;
         } else {
@@ -272,6 +272,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) items[buf] = it;
       __syncwarp();
       mbar_arrive(&sb.item_full[buf]);
+      // Where this lane's rows lane, lane + 32, ... of the block are (-1: there is no such row).
+      int64_t at[2 * BM / 32];
+#pragma unroll
+      for (int j = 0; j < 2 * BM / 32; ++j) {
+        const int row = it.row0 + 32 * j + lane;
+        at[j] = -1;
+        if (row < it.rows) {
+          int q = row / p.qpg, b = it.b;
+          const int h = it.g * p.qpg + row - q * p.qpg;
+          if (b < 0) {
+            b = q / p.Sq;
+            q -= b * p.Sq;
+          }
+          at[j] = (int64_t)b * p.q.bs + (int64_t)h * p.q.hs + (int64_t)q * p.q.rs;
+        }
+      }
+      if (k > 0 && !wait_warp(&sb.q_empty, (uint32_t)(k - 1) & 1u, &sb.abort, p.status)) break;
+      const T* Q = static_cast<const T*>(p.Q) + p.q.off + lane % kUnits * 8;
+      const int rl = lane / kUnits, un = lane % kUnits;
+#pragma unroll
+      for (int j = 0; j < 2 * BM / 32; ++j) {
+        if (j >= BM / 32 && !it.some1) break;   // (row tiles that hold the same rows share the first tile)
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += kRowsAt) {
+          const int64_t from = __shfl_sync(0xffffffffu, at[j], r0 + rl);
+          const int row = 32 * j + r0 + rl;   // (128-byte swizzle)
+          paged::copy16(su32(q_s + row / BM * C::kTile + (un / 8) * BM * 128 + row % BM * 128 + (((un % 8) ^ (row & 7)) << 4)),
+                        Q + (from < 0 ? 0 : from), from < 0 ? 0 : 16);
+        }
+      }
+      paged::copy_commit();
+      paged::copy_wait<0>();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&sb.q_full);
     }
   } else if (warp == 8 || warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
@@ -306,12 +340,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n; ++i) {
         const uint32_t missing = __ballot_sync(0xffffffffu, page < 0 && chunk == 0);
         const int pg = page < 0 ? (int)x.n_pages : page, prow = row;
+        bool pre;
+        const uint32_t first_key = (uint32_t)it.key(i, pre) + (pre ? 1u : 0u);
         if (i + 1 < n) page = look_up(it, i + 1, row);   // arrives while this tile waits for its slot
         if (!(ok = wait_warp(&sb.empty[sl.s], sl.ph ^ 1u, &sb.abort, p.status))) break;
         if (lane == 0) {
           // Note gt % kNotes was read for tile gt - kNotes.  The slot was free: the product that used it is done, of tile
           // gt - n_slots / 2 - 1 or a later one, whose S followed the row tiles' reading of notes two tiles further back.
-          if (is_k) no_page[gt % kNotes] = missing;
+          if (is_k) notes[gt % kNotes] = make_uint2(missing, first_key);
           mbar_expect_tx(&sb.full[sl.s], C::kTile);
         }
         __syncwarp();
@@ -388,13 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
       const Item& it = items[buf];
       const int n = it.n;
-      // Every phase of both, also where a row tile has nothing to do; and q_seen keeps the row tiles within one phase of
-      // this warp: a wait takes a phase that is two ahead for one that has not come.
-      if (!(ok = wait_warp(&sb.q_full[0], (uint32_t)k & 1u, &sb.abort, p.status))) break;
-      if (!(ok = wait_warp(&sb.q_full[1], (uint32_t)k & 1u, &sb.abort, p.status))) break;
-      if (lane == 0) mbar_arrive(&sb.q_seen);
+      if (!(ok = wait_warp(&sb.q_full, (uint32_t)k & 1u, &sb.abort, p.status))) break;
       bool start0 = true, start1 = true;
-      if (n > 0 && it.alt) {
+      if (n == 0) {
+        if (lane == 0) mbar_arrive(&sb.q_empty);
+      } else if (it.alt) {
         issued = true;
         // Tile i belongs to row tile i % 2: P V of tile i, then S of tile i + 2.
         auto next_s = [&](int i) {
@@ -423,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (i + 2 < n) ok = next_s(i + 2);
         }
-      } else if (n > 0) {
+      } else {
         issued = true;
         const int n0 = it.n0;
         const bool some1 = it.some1 != 0;
@@ -431,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n0 > 0) issue_qk(0, 0, ks.s);
         if (some1) issue_qk(1, 1, ks.s);
         mma_commit_w(&sb.empty[ks.s]);
+        if (n == 1) mma_commit_w(&sb.q_empty);
         ks.next_tile(n_slots);
         bool rv = mbar_test(&sb.full[vs.s], vs.ph);   // the next V landed?
         for (int i = 0; i < n; ++i) {
@@ -467,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) {
             if (some1) issue_qk(1, 1, ks.s);
             mma_commit_w(&sb.empty[ks.s]);
+            if (i + 2 == n) mma_commit_w(&sb.q_empty);
             ks.next_tile(n_slots);
           }
         }
@@ -509,34 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    // Loads this thread's query row into its place of the tile (128-byte swizzle); zeros for a row that is not.  (Row
-    // tiles that hold the same rows share the first tile.)
-    auto load_q = [&](const Item& it) {
-      if (it.alt && t == 1) {
-        mbar_arrive(&sb.q_full[1]);
-        return;
-      }
-      int b, i, h;
-      const bool here = row_of(it, b, i, h);
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.Q) + p.q.off + (int64_t)b * p.q.bs +
-                                                        (int64_t)h * p.q.hs + (int64_t)i * p.q.rs);
-      uint4 v[D / 8];
-#pragma unroll
-      for (int u = 0; u < D / 8; ++u) v[u] = here ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int u = 0; u < D / 8; ++u)
-        *reinterpret_cast<uint4*>(q_s + t * C::kTile + (u / 8) * BM * 128 + r * 128 + (((u % 8) ^ (r & 7)) << 4)) = v[u];
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&sb.q_full[t]);
-    };
     int j = 0;    // key tiles so far
     int gt = 0;   // key tiles of the items so far
-    uint32_t alt_phase = 0u, pair_phase = 0u;
-    bool ok = my_items > 0 && wait_warp(&sb.item_full[0], 0u, &sb.abort, p.status);
-    if (ok) load_q(items[0]);
+    uint32_t pair_phase = 0u;
+    bool ok = true;
     for (int k = 0; ok && k < my_items; ++k) {
       const int buf = k & 1;
-      const Item& it = items[buf];   // (its phase was waited for with the queries)
+      if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
+      const Item& it = items[buf];
       const int n = it.n;
       int b, qi, h;
       const bool valid = row_of(it, b, qi, h);
@@ -552,10 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!it.has(t, i)) continue;
         if (!(ok = wait_warp(&sb.s_full[t], (uint32_t)j & 1u, &sb.abort, p.status))) break;
         fence_after();
-        bool pre;
-        const int k0 = it.key(i, pre);
+        const uint2 note = notes[(gt + i) % kNotes];
+        const uint32_t missing = note.x;
+        const bool pre = note.y & 1u;
+        const int k0 = (int)(note.y & ~1u);
         const int seen_n = (pre && valid ? p.prefix : seen_own) - k0;   // the row sees the tile's first seen_n keys
-        const uint32_t missing = no_page[(gt + i) % kNotes];
         // Which of columns 32 c .. of the tile the row sees.
         auto seen_bits = [&](int c) {
           uint32_t bits = low_bits(seen_n - 32 * c);
@@ -678,17 +695,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       gt += n;
-      // The next item's queries.  This row tile's last S, whose phase was waited for above, was its queries' last use, but
-      // for queries that both row tiles use (whose phases are the items of one row tile).
-      if (k + 1 < my_items) {
-        if (!(ok = wait_warp(&sb.item_full[buf ^ 1], (uint32_t)((k + 1) >> 1) & 1u, &sb.abort, p.status))) break;
-        if (!(ok = wait_warp(&sb.q_seen, (uint32_t)k & 1u, &sb.abort, p.status))) break;
-        if (t == 0 && it.alt && n > 0) {
-          if (!(ok = wait_warp(&sb.q_empty, alt_phase, &sb.abort, p.status))) break;
-          alt_phase ^= 1u;
-        }
-        load_q(items[buf ^ 1]);
-      }
       // ---- epilogue: O / l, special rows, LSE ----
       if (done > 0 && !(ok = wait_warp(&sb.o_done[t], (uint32_t)(j - 1) & 1u, &sb.abort, p.status))) break;
       fence_after();
