@@ -452,11 +452,12 @@ int check_shared(const attn_problem* p, const attn_pages* pages, const attn_pref
   return check_pages(pages, p->k_len);
 }
 
-// The CUDA-core pass's plan for a batch with a prefix: parts of each row block's tile list.
+// The CUDA-core passes' plan for a batch with a prefix: parts of each row block's tile list, as many as fill the SMs
+// some four times over (float32 on register tiles, of 32 rows or more) or more (rows of a few lanes each).
 int shared_plan(const attn_problem* p, const attn_prefix* x) {
-  const int64_t rows = (int64_t)p->q_len * (p->heads / p->kv_heads);
-  const int64_t blocks = (int64_t)(p->batch > 0 ? p->batch : 1) * p->kv_heads * ((rows + 15) / 16);
-  int64_t n = (4096 + blocks - 1) / blocks;
+  const int64_t rows = (int64_t)p->q_len * (p->heads / p->kv_heads), tile = p->dtype == ATTN_F32 && p->q_len > 1 ? 32 : 16;
+  const int64_t blocks = (int64_t)(p->batch > 0 ? p->batch : 1) * p->kv_heads * ((rows + tile - 1) / tile);
+  int64_t n = ((tile == 32 ? 608 : 4096) + blocks - 1) / blocks;
   n = n < 64 ? n : 64;
   const int64_t tiles = ((int64_t)x->rows + p->k_len + 127) / 128;
   n = n < tiles ? n : tiles;
@@ -696,7 +697,9 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   const int n = shared_plan(p, prefix);
   Split s{1, 1, nullptr, nullptr};
   if (n > 1) s = split_in(workspace, rows, n, 0, p->head_dim, true);
-  rc = from_cuda(launch_simt_ext(r, x, s, st));
+  rc = shared_f32_try(r, x, s, st, &used);
+  if (rc) return rc;
+  if (!used) rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;
   return n > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;
 }

@@ -25,8 +25,10 @@ struct Prep {
   uint8_t axis[128];      // of each rotated pair
 };
 
-// Enqueues the step with positions on several axes (prep_axes.cu).
-cudaError_t prep_axes(const Prep& p, bool kv8, int dtype, cudaStream_t st);
+// Enqueue the step with positions on several axes (prep_axes_*.cu).
+cudaError_t prep_axes_f32(const Prep& p, bool kv8, cudaStream_t st);
+cudaError_t prep_axes_f16(const Prep& p, bool kv8, cudaStream_t st);
+cudaError_t prep_axes_bf16(const Prep& p, bool kv8, cudaStream_t st);
 
 // Checks of a page list that holds `rows` rows an entry (defined in api.cu).
 int check_pages(const attn_pages* pages, int64_t rows);

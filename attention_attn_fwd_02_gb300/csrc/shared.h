@@ -74,6 +74,8 @@ size_t shared_tc_bytes(const Problem& p, const shr::Work& w);
 // has its workspace behind the plan's.  As prefill_tc_try.
 int shared_tc_try(const Problem& p, const Ext& x, shr::Work& w, const Problem& own, const Ext& x_own, void* workspace,
                   cudaStream_t st, int* used);
+// The float32 pass over prompts, each entry by itself; s: parts of the entries' tile lists.  As prefill_tc_try.
+int shared_f32_try(const Problem& p, const Ext& x, const Split& s, cudaStream_t st, int* used);
 // Merges a plan's partial results, as the programmatic dependent of the pass in front.  own: the decode pass over own
 // keys, whose cut units it joins too (null: there was none).
 cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const paged::Work* own, cudaStream_t st);
