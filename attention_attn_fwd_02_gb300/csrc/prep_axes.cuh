@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256, ctas_per_sm(FLAT, ONE)) prep_axes_kernel(
           sn[e] = make_float2(0.f, 0.f);
         }
       } else if constexpr (ONE) {
-        const int64_t at = (int64_t)min(max(pos[s][0], 0), p.max_pos - 1) * half + t * N;
+        const int at = min(max(pos[s][0], 0), p.max_pos - 1) * half + t * N;
 #pragma unroll
         for (int e = 0; e < P; e += 2) {
           const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cos + at + 2 * e));
@@ -152,12 +152,14 @@ __global__ void __launch_bounds__(256, ctas_per_sm(FLAT, ONE)) prep_axes_kernel(
           sn[e + 1] = make_float2(s4.z, s4.w);
         }
       } else {
+        int at[kPos];   // the token's rows of the tables, from the thread's first pair on
+#pragma unroll
+        for (int a = 0; a < kPos; ++a) at[a] = min(max(pos[s][a], 0), p.max_pos - 1) * half + t * N;
 #pragma unroll
         for (int e = 0; e < N; ++e) {   // each pair at its own axis's position
           const uint32_t a = mine[e / 4] >> (8 * (e % 4)) & 255u;
-          const int x = a < 2 ? (a == 0 ? pos[s][0] : pos[s][1]) : a == 2 ? pos[s][2] : pos[s][3];
-          const int64_t at = (int64_t)min(max(x, 0), p.max_pos - 1) * half + t * N + e;
-          const float c = __ldg(p.cos + at), y = __ldg(p.sin + at);
+          const int x = (a & 2u ? (a & 1u ? at[3] : at[2]) : a & 1u ? at[1] : at[0]) + e;
+          const float c = __ldg(p.cos + x), y = __ldg(p.sin + x);
           if (e % 2) {
             cs[e / 2].y = c;
             sn[e / 2].y = y;
@@ -303,7 +305,8 @@ cudaError_t launch_axes(const Prep& p, bool kv8, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_type(const Prep& p, bool kv8, cudaStream_t st) {
-  if (!takes_vec<T>(p, kv8)) return launch_rows<T, true>(p, kv8, st);
+  // (places in the tables are 32-bit numbers)
+  if (!takes_vec<T>(p, kv8) || (int64_t)p.max_pos * (p.rot / 2) > 0x7fffffff) return launch_rows<T, true>(p, kv8, st);
   switch (p.D / (2 * Vec<T>::N)) {
     case 2: return launch_axes<T, 2>(p, kv8, st);
     case 4: return launch_axes<T, 4>(p, kv8, st);
