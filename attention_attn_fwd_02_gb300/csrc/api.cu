@@ -474,8 +474,9 @@ size_t shared_bytes(const attn_problem* p, const attn_pages* pages, const attn_p
   const size_t a = n > 1 ? sums_ws_bytes(p, n) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
   shr::Work w;
   size_t c = 0;
-  if (shared_tc_plan(r, pages->page_size, w)) {
-    c = shared_tc_bytes(r, w);
+  const bool tc = shared_tc_plan(r, pages->page_size, w);
+  if (tc || shared_f32_plan(r, w)) {
+    c = tc ? shared_tc_bytes(r, w) : shared_f32_bytes(r, w);
     if (p->q_len == 1) c += paged_own_bytes(own_problem(r), w.own_sms);   // behind the partial results
   }
   return a > b ? (a > c ? a : c) : (b > c ? b : c);
@@ -688,6 +689,10 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   shr::Work w;
   if (shared_tc_plan(r, x.page_size, w)) {
     rc = shared_tc_try(r, x, w, own_problem(r), make_ext(0, pages), workspace, st, &used);
+    if (rc || used) return rc;
+  }
+  if (shared_f32_plan(r, w)) {
+    rc = shared_f32_packed(r, x, w, own_problem(r), make_ext(0, pages), workspace, st, &used);
     if (rc || used) return rc;
   }
   if (p->q_len == 1) {

@@ -57,6 +57,7 @@ struct Work {
   int own_sms;                    // SMs that the decode pass over own keys is planned for
   // Partial results: numerators over their sums, natural maxima (-inf: no visible key), sums.  packed: [B H q_len][splits]
   // in (entry, head, query) order; joined: [ctas][2][256].  note: packed, the number of each unit's fragments.
+  // (float32 has no list: every row has own_slot results of the prefix, and note is null)
   float *part_o, *part_m, *part_l;
   int* note;
 
@@ -74,8 +75,13 @@ size_t shared_tc_bytes(const Problem& p, const shr::Work& w);
 // has its workspace behind the plan's.  As prefill_tc_try.
 int shared_tc_try(const Problem& p, const Ext& x, shr::Work& w, const Problem& own, const Ext& x_own, void* workspace,
                   cudaStream_t st, int* used);
-// The float32 pass over prompts, each entry by itself; s: parts of the entries' tile lists.  As prefill_tc_try.
+// float32: the pass over each entry by itself (s: parts of the entries' tile lists), and the packed plan with its bytes
+// and passes, as for the tensor cores.
 int shared_f32_try(const Problem& p, const Ext& x, const Split& s, cudaStream_t st, int* used);
+bool shared_f32_plan(const Problem& p, shr::Work& w);
+size_t shared_f32_bytes(const Problem& p, const shr::Work& w);
+int shared_f32_packed(const Problem& p, const Ext& x, shr::Work& w, const Problem& own, const Ext& x_own, void* workspace,
+                      cudaStream_t st, int* used);
 // Merges a plan's partial results, as the programmatic dependent of the pass in front.  own: the decode pass over own
 // keys, whose cut units it joins too (null: there was none).
 cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const paged::Work* own, cudaStream_t st);

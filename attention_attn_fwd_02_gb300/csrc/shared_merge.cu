@@ -28,6 +28,13 @@ struct Cuts {
   int heads, n_hc;
 };
 
+// Four elements of a row of O (on a 16-byte boundary).
+template <typename T>
+__device__ __forceinline__ void store4(T* out, const T (&y)[4]) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(y);
+  else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+}
+
 // Merges the n results of a row (WARPS warps; every thread of them comes here).  load_m, load_l: a result's maximum and
 // sum; load_o: four columns of it.
 template <typename T, int D, int WARPS, typename M_, typename L_, typename O_>
@@ -131,10 +138,10 @@ __device__ __forceinline__ void merge_row(const Problem& p, bool here, int64_t b
     const bool plain = !nan && !none;
     T* out = static_cast<T*>(p.O) + p.o.off + b * p.o.bs + (int64_t)h * p.o.hs + (int64_t)i * p.o.rs + d;
     const float a[4] = {acc.x, acc.y, acc.z, acc.w};
-    __align__(8) T y[4];
+    __align__(16) T y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(plain ? a[e] * inv : fill);
-    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);   // (rows of O are on 16-byte boundaries)
+    store4(out, y);
   }
   if (p.lse && lane == 0)
     p.lse[b * p.lse_bs + (int64_t)h * p.lse_hs + i] = nan ? NAN : none ? -INFINITY : M + logf(sum);
@@ -202,10 +209,10 @@ __device__ __forceinline__ void merge_few(const Problem& p, const Work& w, FewRo
     const float fill = none && p.masked_zero ? 0.f : NAN, inv = 1.f / sum;
     T* out = static_cast<T*>(p.O) + p.o.off + r.b * p.o.bs + r.h * p.o.hs + r.i * p.o.rs + d;
     const float a[4] = {acc.x, acc.y, acc.z, acc.w};
-    __align__(8) T y[4];
+    __align__(16) T y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = from_f32<T>(nan || none ? fill : a[e] * inv);
-    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+    store4(out, y);
     if (p.lse && d == 0)
       p.lse[r.b * p.lse_bs + r.h * p.lse_hs + r.i] = nan ? NAN : none ? -INFINITY : M + logf(sum);
   }
@@ -228,8 +235,9 @@ __global__ void __launch_bounds__(32 * kWarps, 6) merge_few_kernel(const Problem
     r.b = (int)(id / per_entry);
     r.h = (int)(in / (uint32_t)p.Sq);
     r.i = (int)(in - r.h * (uint32_t)p.Sq);
+    note[q] = nullptr;
     const uint32_t g = (uint32_t)r.h / p.qpg, packed = ((uint32_t)r.b * p.Sq + r.i) * p.qpg + r.h - g * p.qpg;
-    note[q] = w.note + (r.here ? g * w.blocks + packed / (2 * kRows) : 0);
+    if (w.note) note[q] = w.note + (r.here ? g * w.blocks + packed / (2 * kRows) : 0);
 #pragma unroll
     for (int k = 0; k < kFew; ++k) r.at[k] = (int64_t)id * w.splits + k;   // (by slot, so far)
   }
@@ -237,7 +245,7 @@ __global__ void __launch_bounds__(32 * kWarps, 6) merge_few_kernel(const Problem
   int n_a[kRowsFew];
 #pragma unroll
   for (int q = 0; q < kRowsFew; ++q) {
-    n_a[q] = *note[q];
+    n_a[q] = note[q] ? *note[q] : w.own_slot;
     row[q].fetch(w, w.splits);
   }
 #pragma unroll
@@ -288,14 +296,14 @@ __global__ void __launch_bounds__(32 * kWarps, 8)
   const int64_t b = row / ((int64_t)p.Sq * p.H);
   const bool here = b < p.B;
   const int64_t r = (b * p.Sq + i) * p.qpg + h % p.qpg;
-  const int unit = h / p.qpg * w.blocks + (int)(r / (2 * kRows));
+  const int unit = w.note ? h / p.qpg * w.blocks + (int)(r / (2 * kRows)) : 0;
   const int j = h % p.qpg, u = cuts.note ? h / p.qpg * cuts.n_hc + j / cuts.heads : 0;
   paged::wait_for_previous();
   int n_a = 0, n_b = w.parts_b;
   int64_t first = 0, rest = 0;   // rows of a cut unit's first fragment and of the others
   bool cut = false;
   if (here) {
-    n_a = w.note[unit];
+    n_a = w.note ? w.note[unit] : w.own_slot;
     if (cuts.note) {
       const int2 note = cuts.note[b * p.G * cuts.n_hc + u];
       cut = note.y > 0;
@@ -375,6 +383,8 @@ cudaError_t merge(const Problem& p, const Work& w, const Cuts& cuts, cudaStream_
 cudaError_t launch_shared_merge(const Problem& p, const shr::Work& w, const paged::Work* own, cudaStream_t st) {
   shr::Cuts cuts{};
   if (own && own->own.note) cuts = {own->part_o, own->part_m, own->part_l, own->own.note, own->heads, own->n_hc};
+  if (p.dtype == ATTN_F32)
+    return p.D == 64 ? shr::merge<float, 64>(p, w, cuts, st) : shr::merge<float, 128>(p, w, cuts, st);
   if (p.dtype == ATTN_F16)
     return p.D == 64 ? shr::merge<__half, 64>(p, w, cuts, st) : shr::merge<__half, 128>(p, w, cuts, st);
   return p.D == 64 ? shr::merge<__nv_bfloat16, 64>(p, w, cuts, st) : shr::merge<__nv_bfloat16, 128>(p, w, cuts, st);

@@ -11,7 +11,7 @@ int window_f32_try(const Problem& p, int first, const Split& sp, cudaStream_t st
     return ATTN_OK;   // 16-byte loads and stores of rows
   const float sc = p.scale * S::kLog2;
   if (!(sc == sc) || isinf(sc)) return ATTN_OK;
-  const int rc = launch_head_dim<false>(p, make_ext(first, nullptr), sp, st);
+  const int rc = launch_head_dim<kPlain>(p, make_ext(first, nullptr), sp, sp.n_splits, st);
   if (rc < 0) return ATTN_OK;
   *used = 1;
   return rc;

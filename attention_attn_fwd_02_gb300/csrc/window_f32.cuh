@@ -49,9 +49,14 @@ struct Cfg {
   static constexpr int kCtas = kSmem <= 74 * 1024 ? 3 : 2;
 };
 
-template <int D, int TM, bool PAGED>
+// KIND: contiguous keys, an entry's prefix and own keys in pages, or the prefix alone for the packed rows of all
+// entries.  stride: partial results of a row.
+enum { kPlain = 0, kPaged = 1, kPacked = 2 };
+
+template <int D, int TM, int KIND>
 __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
-    window_f32_kernel(const Problem p, const Ext x, const Split sp, const int64_t row_blocks) {
+    window_f32_kernel(const Problem p, const Ext x, const Split sp, const int64_t row_blocks, const int stride) {
+  constexpr bool PAGED = KIND != kPlain, PACKED = KIND == kPacked;
   const int first = x.first;
   using C = Cfg<D, TM>;
   constexpr int BM = C::BM, PITCH = C::kPitch, NC = D / 32;
@@ -62,6 +67,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
   float* p_s = v_s + BN * D;
   __shared__ Vis row_v[BM];
   __shared__ int row_q[BM], row_h[BM], s_f[2], s_w[2];
+  __shared__ int row_b[PACKED ? BM : 1];   // PACKED: each row's entry
   // PAGED: where the rows of a tile (even, odd) are in K and V, and which of them have a page.
   __shared__ int64_t at_k[2][BN], at_v[2][BN];
   __shared__ uint32_t paged_keys[2];
@@ -72,10 +78,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
   blk /= sp.n_splits;
   const int64_t rb = blk % row_blocks;
   blk /= row_blocks;
-  const int g = (int)(blk % p.G), b = (int)(blk / p.G);
+  const int g = (int)(blk % p.G), b = PACKED ? 0 : (int)(blk / p.G);
   // Query and head of each row (-1: behind the last).
   auto query_of = [&](int row) { return row_q[row]; };
   auto head_of = [&](int row) { return row_h[row]; };
+  auto entry_of = [&](int row) { return PACKED ? row_b[PACKED ? row : 0] : b; };
   auto valid = [&](int row) { return row_q[row] >= 0; };
 
   if (tid == 0) {
@@ -85,10 +92,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
   __syncthreads();
   if (tid < BM) {
     const int64_t r = rb * BM + tid;
-    const int i = (int)(r / p.qpg);
-    row_q[tid] = i < p.Sq ? i : -1;
+    int i = (int)(r / p.qpg);
     row_h[tid] = g * p.qpg + (int)(r - (int64_t)i * p.qpg);
-    const Vis v = i < p.Sq ? row_vis(p, first, b, i) : Vis{0, 0, 0, 0};
+    bool here = i < p.Sq;
+    if constexpr (PACKED) {
+      const int e = i / p.Sq;
+      i -= e * p.Sq;
+      here = e < p.B;
+      row_b[tid] = here ? e : 0;
+    }
+    row_q[tid] = here ? i : -1;
+    const Vis v = !here ? Vis{0, 0, 0, 0} : PACKED ? Vis{0, 0, 0, p.prefix} : row_vis(p, first, b, i);
     row_v[tid] = v;
     if (v.fe > v.lo) {
       atomicMin(&s_f[0], v.lo);
@@ -105,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
   int t0 = 0, t1 = tl.n;
   if (sp.part_o) list_part(tl.n, split, sp.n_splits, t0, t1);
 
-  const float* Q = static_cast<const float*>(p.Q) + p.q.off + (int64_t)b * p.q.bs;
+  const float* Q = static_cast<const float*>(p.Q) + p.q.off;
   const float* K = static_cast<const float*>(p.K) + p.k.off + (PAGED ? 0 : (int64_t)b * p.k.bs) + (int64_t)g * p.k.hs;
   const float* V = static_cast<const float*>(p.V) + p.v.off + (PAGED ? 0 : (int64_t)b * p.v.bs) + (int64_t)g * p.v.hs;
   // The page of row `tid` of tile ti, and the row in it (tid < BN).
@@ -132,7 +146,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
     const int row = c / kChunks, d = c % kChunks * 4;
     const bool ok = valid(row);
     copy16(smem_u32(q_s + row * PITCH + d),
-           ok ? Q + (int64_t)head_of(row) * p.q.hs + (int64_t)query_of(row) * p.q.rs + d : Q, ok ? 16 : 0);
+           ok ? Q + (int64_t)entry_of(row) * p.q.bs + (int64_t)head_of(row) * p.q.hs + (int64_t)query_of(row) * p.q.rs + d
+              : Q,
+           ok ? 16 : 0);
   }
   // Rows no row of the CTA sees arrive as zeros and are not read.
   auto load = [&](float* dst, int pitch, const float* src, int64_t rs, const int64_t (&at)[2][BN], int ti) {
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
         for (int c = 0; c < 4; ++c) s[r][c] *= p.scale;
       }
       if (p.M && valid(row)) {
-        const float* mr = p.M + p.m.off + (int64_t)b * p.m.bs + (int64_t)head_of(row) * p.m.hs +
+        const float* mr = p.M + p.m.off + (int64_t)entry_of(row) * p.m.bs + (int64_t)head_of(row) * p.m.hs +
                           (int64_t)query_of(row) * p.m.rs + k0 + tx;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -276,15 +292,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
 #pragma unroll
     for (int x = 1; x < 8; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
     if (!valid(row)) continue;
-    const int i = query_of(row), h = head_of(row);
+    const int i = query_of(row), h = head_of(row), e = entry_of(row);
     float f = 1.f, M = S::natural(m[r]);
     if (!sp.part_o && p.sink_on) f = fold_sink<false>(M, l[r], sink_logit(p, h));
     const bool hidden = l[r] == 0.f;
     const float lse = hidden ? -INFINITY : S::lse(M, log2f(l[r]));
     const float fill = sp.part_o || p.masked_zero ? 0.f : NAN;
-    const int64_t at = ((int64_t)b * p.H + h) * p.Sq + i;
-    float* dst = sp.part_o ? sp.part_o + (at * sp.n_splits + split) * D
-                           : static_cast<float*>(p.O) + p.o.off + (int64_t)b * p.o.bs + (int64_t)h * p.o.hs +
+    const int64_t at = ((int64_t)e * p.H + h) * p.Sq + i;
+    float* dst = sp.part_o ? sp.part_o + (at * stride + split) * D
+                           : static_cast<float*>(p.O) + p.o.off + (int64_t)e * p.o.bs + (int64_t)h * p.o.hs +
                                  (int64_t)i * p.o.rs;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -294,43 +310,45 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
       *reinterpret_cast<float4*>(dst + c * 32 + tx * 4) = y;
     }
     if (tx == 0) {
-      if (sp.part_o) sp.part_lse[at * sp.n_splits + split] = sp.part_l && !hidden ? M : lse;
-      if (sp.part_l) sp.part_l[at * sp.n_splits + split] = l[r];
-      if (!sp.part_o && p.lse) p.lse[(int64_t)b * p.lse_bs + (int64_t)h * p.lse_hs + i] = lse;
+      if (sp.part_o) sp.part_lse[at * stride + split] = sp.part_l && !hidden ? M : lse;
+      if (sp.part_l) sp.part_l[at * stride + split] = l[r];
+      if (!sp.part_o && p.lse) p.lse[(int64_t)e * p.lse_bs + (int64_t)h * p.lse_hs + i] = lse;
     }
   }
 }
 
-template <int D, int TM, bool PAGED>
-int launch(const Problem& p, const Ext& x, const Split& sp, cudaStream_t st) {
+template <int D, int TM, int KIND>
+int launch(const Problem& p, const Ext& x, const Split& sp, int stride, cudaStream_t st) {
   using C = Cfg<D, TM>;
-  const int64_t row_blocks = ((int64_t)p.Sq * p.qpg + C::BM - 1) / C::BM;
-  const int64_t blocks = row_blocks * p.B * p.G * sp.n_splits;
+  const int64_t entries = KIND == kPacked ? 1 : p.B, rows = (int64_t)p.Sq * p.qpg * (KIND == kPacked ? p.B : 1);
+  const int64_t row_blocks = (rows + C::BM - 1) / C::BM;
+  const int64_t blocks = row_blocks * entries * p.G * sp.n_splits;
   if (blocks > INT_MAX) return -1;
-  auto kern = window_f32_kernel<D, TM, PAGED>;
+  auto kern = window_f32_kernel<D, TM, KIND>;
   if (ensure_smem((const void*)kern, C::kSmem) != cudaSuccess) return ATTN_ERR_CUDA;
-  kern<<<(unsigned)blocks, kThreads, C::kSmem, st>>>(p, x, sp, row_blocks);
+  kern<<<(unsigned)blocks, kThreads, C::kSmem, st>>>(p, x, sp, row_blocks, stride);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Four rows a thread when their CTAs fill the SMs, else two: more, shorter CTAs.
-template <int D, bool PAGED>
-int launch_d(const Problem& p, const Ext& x, const Split& sp, cudaStream_t st) {
-  const int64_t big = ((int64_t)p.Sq * p.qpg + 63) / 64 * p.B * p.G * sp.n_splits;
+template <int D, int KIND>
+int launch_d(const Problem& p, const Ext& x, const Split& sp, int stride, cudaStream_t st) {
+  const int64_t entries = KIND == kPacked ? 1 : p.B, rows = (int64_t)p.Sq * p.qpg * (KIND == kPacked ? p.B : 1);
+  const int64_t big = (rows + 63) / 64 * entries * p.G * sp.n_splits;
   if constexpr (D <= 128) {
-    if (big >= 2 * 152) return launch<D, 4, PAGED>(p, x, sp, st);
+    if (big >= 2 * 152) return launch<D, 4, KIND>(p, x, sp, stride, st);
   }
-  return launch<D, 2, PAGED>(p, x, sp, st);
+  return launch<D, 2, KIND>(p, x, sp, stride, st);
 }
 
 // The instance for a head_dim (-1: there is none, or the grid is too large).
-template <bool PAGED>
-int launch_head_dim(const Problem& p, const Ext& x, const Split& sp, cudaStream_t st) {
+template <int KIND>
+int launch_head_dim(const Problem& p, const Ext& x, const Split& sp, int stride, cudaStream_t st) {
   switch (p.D) {
-    case 32: return launch_d<32, PAGED>(p, x, sp, st);
-    case 64: return launch_d<64, PAGED>(p, x, sp, st);
-    case 128: return launch_d<128, PAGED>(p, x, sp, st);
-    case 256: return launch_d<256, PAGED>(p, x, sp, st);
+    case 32: return launch_d<32, KIND>(p, x, sp, stride, st);
+    case 64: return launch_d<64, KIND>(p, x, sp, stride, st);
+    case 128: return launch_d<128, KIND>(p, x, sp, stride, st);
+    case 256: return launch_d<256, KIND>(p, x, sp, stride, st);
     default: return -1;
   }
 }

@@ -72,6 +72,10 @@ CASES = [
     ("f32", 33, 2, 3, 4, 2, 16, 129, [33, 2], {}),
     ("f32", 128, 33, 1, 8, 2, 24, 1000, [(5 * i) % 64 for i in range(33)], {}),
     ("f32", 256, 2, 9, 4, 2, 16, 77, [9, 12], {}),
+    ("f32", 128, 60, 1, 16, 4, 16, 6003, [(5 * i) % 90 for i in range(60)], dict(softcap=4.0)),   # packed rows
+    ("f32", 64, 70, 1, 8, 8, 7, 7003, [(3 * i) % 40 for i in range(70)], dict(smooth_softmax=True)),
+    ("f32", 64, 20, 3, 8, 4, 16, 4001, [(5 * i) % 90 for i in range(20)], dict(prefix_holes=[3, 250], holes=[(19, 0)])),
+    ("f32", 128, 3, 2, 2, 2, 24, 3001, [2, 7, 0], dict(nhd=True, pad=4)),
     ("bf16", 128, 3, 1, 8, 2, 16, 400, [1, 50, 0], dict(i8="channel")),
     ("f16", 64, 3, 1, 8, 2, 16, 400, [1, 50, 0], dict(i8="tensor")),
     ("bf16", 128, 2, 6, 8, 2, 16, 100, [6, 50], dict(i8="channel")),
@@ -152,7 +156,7 @@ def test_climbing_scores(dt, Sq, step):
     sc.check(c, out, lse)
 
 
-@pytest.mark.parametrize("dt,Sq,B", [("bf16", 1, 6), ("f16", 5, 20), ("bf16", 150, 2), ("f32", 1, 6), ("f32", 20, 3)])
+@pytest.mark.parametrize("dt,Sq,B", [("bf16", 1, 6), ("f16", 5, 20), ("bf16", 150, 2), ("f32", 1, 6), ("f32", 20, 3), ("f32", 1, 70)])
 def test_writes_nothing_outside(dt, Sq, B):
     """Outputs with gaps, a guarded workspace, and pools that stay as they were."""
     H, D = 8, 128
@@ -175,7 +179,7 @@ def test_writes_nothing_outside(dt, Sq, B):
     assert same(k, ks) and same(v, vs)
 
 
-@pytest.mark.parametrize("dt,Sq,B", [("bf16", 1, 30), ("bf16", 5, 20), ("f16", 200, 2), ("f32", 1, 9), ("f32", 20, 3)])
+@pytest.mark.parametrize("dt,Sq,B", [("bf16", 1, 30), ("bf16", 5, 20), ("f16", 200, 2), ("f32", 1, 9), ("f32", 1, 90), ("f32", 20, 3)])
 def test_captured_replayed_and_on_other_streams(dt, Sq, B):
     """Two captured graphs that share a workspace, replayed in turn, and a call on another stream: the same bits."""
     cs = [sc.make(dt, 64, B, Sq, 8, 2, 16, 1300, [Sq + (5 * b + s) % 60 for b in range(B)], 31 + s) for s in range(2)]
