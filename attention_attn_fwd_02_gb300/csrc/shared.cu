@@ -134,10 +134,20 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
     int ctas = kSms;
     if (p.Sq == 1 && own > 0) {
       // The decode pass over pages takes the own keys, side by side with the prefix's: each gets SMs by its cost, own
-      // lists being half as long as they can be.
-      const double us_own = (double)p.B * p.G * (p.Sk - p.prefix) * p.D * 2 / 6.0e6;
-      const double us_all = (double)total * kUnit / kSms;
+      // lists being half as long as they can be (a unit's end costs the decode pass 2 us, three CTAs an SM; beside it
+      // the prefix's tiles take half as long again).  As many CTAs for each unit, where they are alike, so that no CTA
+      // has parts of two.  64 entries of 32/8 heads behind 8192 keys with up to 1024 own ones, by CTAs of the prefix's:
+      // 32 59.5 us, 40 54.0, 48 49.8, 56 48.8, 64 47.7, 72 58.3, and between these 41 57.3, 50 54.8; 32 entries behind
+      // 131072 with up to 512: 104 104.1, 120 104.2, 136 106.1.
+      const int64_t units = (int64_t)p.B * p.G * ceil_div(p.qpg, p.qpg > 8 ? 16 : 8);
+      const double us_own = (double)p.B * p.G * (p.Sk - p.prefix) * p.D * 2 / 6.0e6 + (double)units * 2.0 / (3 * kSms);
+      const double us_all = 1.5 * (double)total * kUnit / kSms;
       ctas = (int)(kSms * (us_all + kPass) / (us_all + us_own + 2 * kPass));
+      const int alike = w.blocks * p.G;
+      if ((w.blocks == 1 || !w.alt) && alike < kSms && 2 * ctas > alike) {
+        ctas = (ctas + alike / 2) / alike * alike;
+        if (ctas >= kSms) ctas -= alike;
+      }
     }
     w.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, ctas);
     w.own_slot = cut(runs, total, w.list);
