@@ -24,7 +24,9 @@
 //     holds: what is on its way bounds the rate that an SM reads at;
 //   - Q rows come from wherever (entry, query, head) puts them, with cp.async
 //     by the warp that finds the items, as soon as the item in front has taken
-//     its last S: rows pack without gaps whatever the strides.
+//     its last S: rows pack without gaps whatever the strides.  A CTA's first
+//     queries are loaded by the softmax threads, a row each, which have nothing
+//     else to do then (one warp takes 5 us for the rows, 256 threads 1).
 // P enters the product as one value of the element type, as in attn_fwd.
 #pragma once
 
@@ -76,7 +78,7 @@ struct Item {
 };
 
 struct Bars {
-  uint64_t q_full, q_empty;
+  uint64_t q_first, q_full, q_empty;
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t item_full[2], item_empty[2];
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sb.full[s], 1);
       mbar_init(&sb.empty[s], 1);
     }
+    mbar_init(&sb.q_first, 2 * BM);
     mbar_init(&sb.q_full, 32);
     mbar_init(&sb.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
@@ -272,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) items[buf] = it;
       __syncwarp();
       mbar_arrive(&sb.item_full[buf]);
+      if (k == 0) continue;   // (the softmax threads load the first queries)
       // Where this lane's rows lane, lane + 32, ... of the block are (-1: there is no such row).
       int64_t at[2 * BM / 32];
 #pragma unroll
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           at[j] = (int64_t)b * p.q.bs + (int64_t)h * p.q.hs + (int64_t)q * p.q.rs;
         }
       }
-      if (k > 0 && !wait_warp(&sb.q_empty, (uint32_t)(k - 1) & 1u, &sb.abort, p.status)) break;
+      if (!wait_warp(&sb.q_empty, (uint32_t)(k - 1) & 1u, &sb.abort, p.status)) break;
       const T* Q = static_cast<const T*>(p.Q) + p.q.off + lane % kUnits * 8;
       const int rl = lane / kUnits, un = lane % kUnits;
 #pragma unroll
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_warp(&sb.item_full[buf], (uint32_t)(k >> 1) & 1u, &sb.abort, p.status))) break;
       const Item& it = items[buf];
       const int n = it.n;
-      if (!(ok = wait_warp(&sb.q_full, (uint32_t)k & 1u, &sb.abort, p.status))) break;
+      if (!(ok = wait_warp(k ? &sb.q_full : &sb.q_first, (uint32_t)(k ? k - 1 : 0) & 1u, &sb.abort, p.status))) break;
       bool start0 = true, start1 = true;
       if (n == 0) {
         if (lane == 0) mbar_arrive(&sb.q_empty);
@@ -556,6 +560,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = it.n;
       int b, qi, h;
       const bool valid = row_of(it, b, qi, h);
+      if (k == 0) {
+        if (t == 0 || it.some1) {   // (row tiles that hold the same rows share the first tile)
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.Q) + p.q.off + (int64_t)b * p.q.bs +
+                                                            (int64_t)h * p.q.hs + (int64_t)qi * p.q.rs);
+          uint4* dst = reinterpret_cast<uint4*>(q_s + t * C::kTile + r * 128);
+          uint4 v[D / 8];
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u) v[u] = valid ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u) dst[(u / 8) * BM * 8 + ((u % 8) ^ (r & 7))] = v[u];
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        mbar_arrive(&sb.q_first);
+      }
       const bool idle = !__any_sync(0xffffffffu, valid);   // no row of this warp exists: its P is not used
       // Own keys that the row sees (the prefix's are all seen); a row that does not exist hides nothing.
       const int seen_own = !valid ? 0x7fffffff : it.b < 0 ? 0 : own_seen(p, b, qi);
