@@ -703,8 +703,8 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   Split s{1, 1, nullptr, nullptr};
   if (n > 1) s = split_in(workspace, rows, n, 0, p->head_dim, true);
   rc = shared_f32_try(r, x, s, st, &used);
-  if (rc) return rc;
-  if (!used) rc = from_cuda(launch_simt_ext(r, x, s, st));
+  if (rc || used) return rc;
+  rc = from_cuda(launch_simt_ext(r, x, s, st));
   if (rc) return rc;
   return n > 1 ? from_cuda(launch_combine(r, s, p->dtype, st)) : ATTN_OK;
 }

@@ -27,7 +27,19 @@ int shared_f32_try(const Problem& p, const Ext& x, const Split& sp, cudaStream_t
   const int rc = launch_head_dim<kPaged>(p, x, sp, sp.n_splits, st);
   if (rc < 0) return ATTN_OK;
   *used = 1;
-  return rc;
+  if (rc || sp.n_splits == 1) return rc;
+  cudaError_t e;
+  if (p.D == 64 || p.D == 128) {   // (5 questions of 33 tokens behind 501 keys, 5 parts: 33.5 us with the other merge)
+    shr::Work w{};
+    w.own_slot = w.splits = sp.n_splits;
+    w.part_o = sp.part_o;
+    w.part_m = sp.part_lse;
+    w.part_l = sp.part_l;
+    e = launch_shared_merge(p, w, nullptr, st);
+  } else {
+    e = launch_combine(p, sp, p.dtype, st);
+  }
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Rows against keys on register tiles run at some 20 TFLOP/s where their CTAs fill the SMs.  Each entry by itself, rows
