@@ -40,15 +40,8 @@ struct Runs {
     }
     const int blk = w.blocks - 1 - (int)i;
     const int64_t per = (int64_t)p.B * p.G;
-    const int64_t rows = (int64_t)p.Sq * p.qpg, end = (int64_t)(blk + 1) * 2 * kRows;
-    const int64_t q = ((end < rows ? end : rows) - 1) / p.qpg;   // the block's last query
-    int64_t own = p.Sk - p.prefix;
-    if (p.causal) {
-      const int64_t seen = q + 1 + (p.align_klens ? own - p.Sq : p.coff - p.prefix);
-      own = clamp64(seen, 0, own);
-    }
-    const int64_t tiles = pre + ceil_div(own, kKeys);   // (rows without keys have a unit too)
-    return {clamp64(units - i * per, 0, per), tiles > 0 ? tiles : 1, w.is_alt(blk) ? Shares::kTileAlt : Shares::kTile};
+    return {clamp64(units - i * per, 0, per), most_tiles(p, blk, (int)pre),
+            w.is_alt(blk) ? Shares::kTileAlt : Shares::kTile};
   }
   int64_t total() const {
     int64_t t = 0;
@@ -58,13 +51,12 @@ struct Runs {
 };
 
 // Cuts the list into s.ctas shares (each is to have a tile's cost at least).  Returns the most fragments of a unit.
-// The first `more` shares cost `less` less than the others (the total counts that of all shares in).
-int cut(const Runs& runs, int64_t total, Shares& s, int64_t less = 0, int more = 0) {
+int cut(const Runs& runs, int64_t total, Shares& s) {
   int64_t i = 0, first = 0, begin = 0;   // run, its first unit, and where that begins
   Run run = runs.at(0);
   int most = 1;
   for (int c = 0; c <= s.ctas; ++c) {
-    const int64_t t = total / s.ctas * c + total % s.ctas * c / s.ctas - less * (c < more ? c : more);
+    const int64_t t = total / s.ctas * c + total % s.ctas * c / s.ctas;
     while (i + 1 < runs.size() && t - begin >= run.count * run.cost()) {
       begin += run.count * run.cost();
       first += run.count;
@@ -85,12 +77,12 @@ int cut(const Runs& runs, int64_t total, Shares& s, int64_t less = 0, int more =
   return most;
 }
 
-// The number of parts of entry items' lists of `tiles` key tiles that takes the least time; part_us: a partial result of
-// every row, written and read.
+// The number of parts of entry items' lists of `tiles` key tiles that takes the least time, at most four items a CTA (the
+// lists may turn out short); part_us: a partial result of every row, written and read.
 int best_parts(int64_t items, int64_t tiles, bool alt, double part_us, double* us) {
   int best = 1;
   *us = 0;
-  for (int n = 1; n <= kMaxParts && n <= tiles; ++n) {
+  for (int n = 1; n <= kMaxParts && n <= tiles && (n == 1 || items * n <= 4 * kSms); ++n) {
     const double list = (double)(ceil_div(tiles, n) * (alt ? Shares::kTileAlt : Shares::kTile) + Shares::kEnd) * kUnit;
     const double t = (double)ceil_div(items * n, kSms) * list + n * part_us;
     if (n == 1 || t < *us) {
@@ -132,6 +124,7 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
     const Runs runs{p, w, pre};
     const int64_t total = runs.total();
     int ctas = kSms;
+    bool own_all = false;
     if (p.Sq == 1 && own > 0) {
       // The decode pass over pages takes the own keys, side by side with the prefix's: each gets SMs by its cost, own
       // lists being half as long as they can be (a unit's end costs the decode pass 2 us, three CTAs an SM; beside it
@@ -143,17 +136,22 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
       const double us_own = (double)p.B * p.G * (p.Sk - p.prefix) * p.D * 2 / 6.0e6 + (double)units * 2.0 / (3 * kSms);
       const double us_all = 1.5 * (double)total * kUnit / kSms;
       ctas = (int)(kSms * (us_all + kPass) / (us_all + us_own + 2 * kPass));
+      // No fewer than a third of the SMs: how many own keys there are is not known here, but that they may be many.
+      // Then the decode pass is planned for all SMs: its last CTAs follow the prefix's.
       const int alike = w.blocks * p.G;
+      if (ctas < kSms / 3) ctas = kSms / 3;
       if ((w.blocks == 1 || !w.alt) && alike < kSms && 2 * ctas > alike) {
         ctas = (ctas + alike / 2) / alike * alike;
         if (ctas >= kSms) ctas -= alike;
       }
+      const double us_first = kPass + us_all * kSms / ctas, us_beside = us_own * kSms / (kSms - ctas);
+      own_all = us_first + us_own < (us_first > us_beside ? us_first : us_beside);
     }
     w.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, ctas);
     w.own_slot = cut(runs, total, w.list);
     us_packed = kPass + kMerge + (double)total / w.list.ctas * kUnit + w.own_slot * part_us;
     w.one_tile = all <= kRows;
-    w.own_sms = kSms - w.list.ctas;
+    w.own_sms = own_all ? kSms : kSms - w.list.ctas;
   }
   if (p.Sq == 1) {
     // The decode pass can take the prefix's keys too, once an entry, out of L2.
@@ -167,20 +165,16 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   w.alt_b = has_half(rows);
   const int64_t items = w.blocks_b * (int64_t)p.G * p.B;
   if (items > 0x3fffffff / kMaxParts) return false;
+  // What is compared below is with own lists of some 2048 keys at most: how many there are is not known here, and where they
+  // are many, both divide them alike (16 entries of 5 tokens behind 20480 keys with 320 own ones: 46.7 us, or 129.5 each
+  // by itself, as room for 131072 own keys had it decided).
+  Problem e = p;
+  e.Sk = p.prefix + (int)clamp64(p.Sk - p.prefix, 0, p.Sq + 1024 < 2048 ? 2048 : (int64_t)p.Sq + 1024);
   double us_own = 0;
+  if (own > 0) best_parts(items, ceil_div(e.Sk - e.prefix, kKeys), rows <= kRows, part_us, &us_own);
+  us_packed += us_own;
   w.parts_b = own > 0 ? best_parts(items, own, rows <= kRows, part_us, &us_own) : 0;
   w.n_b = (int)items * w.parts_b;
-  us_packed += us_own;
-  if (pre > 0 && w.n_b > 0) {
-    // CTAs with an entry item more than the others have less of the prefix, by what items cost whose lists are half as
-    // long as they can be.
-    const Runs packed{p, w, pre};
-    const int64_t less = ceil_div(own, 2 * w.parts_b) * (rows <= kRows ? Shares::kTileAlt : Shares::kTile) + Shares::kEnd;
-    const int grid = w.n_b > w.list.ctas ? (w.n_b < kSms ? w.n_b : kSms) : w.list.ctas, more = w.n_b % grid;
-    const int64_t total = packed.total() + less * more;
-    if (grid == w.list.ctas && more > 0 && total / grid - less >= 2 * Shares::kTile)
-      w.own_slot = cut(packed, total, w.list, less, more);
-  }
   w.splits = w.own_slot + w.parts_b;
   // Or each entry by itself: its rows walk the prefix and their own keys.
   Work v{};
@@ -190,14 +184,14 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   v.alt = v.alt_b = w.alt_b;
   v.parts_b = 1;
   v.one_tile = rows <= kRows;
-  const double us_all = (double)Runs{p, v, pre, items}.total() * kUnit;
-  const Runs runs{p, v, pre, items % kSms};
-  const int64_t total = runs.total();
+  const double us_all = (double)Runs{e, v, pre, items}.total() * kUnit;
+  const Runs left{e, v, pre, items % kSms};
+  const int64_t total = left.total();
   const int ctas = (int)clamp64(total / (2 * Shares::kTile), 1, kSms);
   // Cut units cost the write and the read of about a fragment and a half a share, and the merge; uncut ones leave SMs
   // without work for most of a unit's time.
   const double us_cut = kMerge + (double)ctas * 3 * kRows * p.D * 8 / 6.0e6;
-  const double us_left = total ? (double)runs.at(0).cost() * kUnit - (double)total / kSms * kUnit : 0.0;
+  const double us_left = total ? (double)left.at(0).cost() * kUnit - (double)total / kSms * kUnit : 0.0;
   double us_joined = kPass + us_all / kSms + us_left;
   v.n_b = (int)items;
   if (us_cut < us_left) {
@@ -205,7 +199,8 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
     v.list.ctas = ctas;
     v.first_b = (int)(items % kSms);
     v.n_b = (int)(items - v.first_b);
-    v.splits = cut(runs, total, v.list) > 1;
+    const Runs runs{p, v, pre, items % kSms};
+    v.splits = cut(runs, runs.total(), v.list) > 1;
   }
   if (!(us_packed < us_joined)) w = v;
   return true;

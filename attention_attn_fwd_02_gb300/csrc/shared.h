@@ -37,11 +37,11 @@ struct Shares {
 //            see the most keys, in front, then entry by entry, kv head by kv
 //            head) and walks the prefix's tiles and behind them its own.  As many
 //            units as every CTA can have the same number of are dealt whole
-//            (entry items) and write O.  The list has those left over, by the own
-//            tiles that k_len allows (an entry with fewer keys has shorter
-//            fragments): a share keeps its first fragment, where it began
-//            in the middle of a unit, and its last, where it ends in one, for
-//            the merge.
+//            (entry items) and write O.  The list has those left over, as if every
+//            entry had the k_len own keys it may have; the tiles of one that has fewer are
+//            cut in the same proportions.  A share keeps its first fragment,
+//            where it began in the middle of a unit, and its last, where it
+//            ends in one, for the merge.
 // A block whose rows fit one row tile (`alt`: the last one) deals its key tiles
 // to both row tiles of the kernel, which then hold the same rows, in turn.
 struct Work {
@@ -64,6 +64,16 @@ struct Work {
   __host__ __device__ int block_of(int u, int B, int G) const { return joined ? blocks - 1 - u / (B * G) : u % blocks; }
   __host__ __device__ bool is_alt(int block) const { return alt && block == blocks - 1; }
 };
+
+// joined: the tiles of a unit of block `block`, at most, behind `pre` tiles of the prefix (rows without keys have one too).
+__host__ __device__ inline int most_tiles(const Problem& p, int block, int pre) {
+  const int64_t rows = (int64_t)p.Sq * p.qpg, end = (int64_t)(block + 1) * 2 * kRows;
+  const int64_t q = ((end < rows ? end : rows) - 1) / p.qpg;   // the block's last query
+  int64_t own = p.Sk - p.prefix;
+  if (p.causal) own = clamp64(q + 1 + (p.align_klens ? own - p.Sq : p.coff - p.prefix), 0, own);
+  const int tiles = pre + (int)((own + kKeys - 1) / kKeys);
+  return tiles > 0 ? tiles : 1;
+}
 
 }  // namespace shr
 

@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end0 = own_seen(p, it.b, (min(it.row0 + BM, it.rows) - 1) / p.qpg);
         int i0, i1;
         const int all = np + (it.own_end + BN - 1) / BN;
-        if (k < items_a) {
-          i0 = min(tile, all);
-          i1 = ends ? min(w.list.tile[c + 1], all) : all;
+        if (k < items_a) {   // (the shares on both sides of a cut find the same place for it)
+          const float part = (float)all / (float)most_tiles(p, blk, pre);
+          i0 = min((int)(tile * part), all);
+          i1 = ends ? min((int)(w.list.tile[c + 1] * part), all) : all;
         } else {
           list_part(all, part, w.parts_b, i0, i1);
         }

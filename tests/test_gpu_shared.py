@@ -43,6 +43,12 @@ CASES = [
     ("bf16", 128, 2, 130, 8, 2, 64, 300, [130, 400], {}),                                  # prompts
     ("f16", 128, 2, 300, 4, 1, 16, 129, [300, 150], {}),                                   # rows in front of the own keys
     ("bf16", 64, 1, 257, 3, 3, 128, 1, [600], {}),
+    ("bf16", 128, 64, 1, 8, 8, 16, 3000, [(7 * i) % 131 for i in range(64)], dict(max_rows=3000)),  # much room, few keys
+    ("f16", 64, 70, 1, 8, 8, 16, 5000, [(7 * i) % 131 for i in range(70)], dict(max_rows=9000)),
+    ("bf16", 128, 3, 150, 8, 2, 16, 700, [150, 151, 160], dict(max_rows=5000)),
+    ("f16", 64, 9, 12, 8, 2, 16, 3000, [12, 151, 0, 160, 1, 2, 3, 4, 5], dict(max_rows=4000)),
+    ("bf16", 128, 2, 600, 8, 2, 64, 129, [600, 100], dict(max_rows=2000, offset=40)),
+    ("f32", 64, 3, 40, 4, 2, 16, 300, [40, 41, 7], dict(max_rows=4000)),
     ("bf16", 64, 3, 70, 4, 4, 8, 500, [70, 71, 64], dict(causal=False)),
     ("f16", 128, 2, 40, 4, 2, 32, 260, [300, 40], dict(offset=100)),
     ("f16", 128, 2, 40, 4, 2, 32, 260, [300, 40], dict(offset=-20)),
