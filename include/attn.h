@@ -372,8 +372,14 @@ ATTN_API size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn
  * (ATTN_ERR_UNSUPPORTED); p->key_splits is not used.  Types, int8 pools, score
  * transforms, masked rows, LSE, determinism and errors as for
  * attn_decode_paged.  Rows of the pools that no row of their entry (of the
- * batch, in the prefix) sees are never read into the result; with q_len > 1
- * the V values of visible keys must be finite (attn_fwd). */
+ * batch, in the prefix) sees are never read into the result.  V values of keys
+ * that some row sees must be finite, or rows of their tile that hide the key,
+ * or give it a weight below the element type's range, may become NaN.
+ * Precision: f16/bf16 probabilities are rounded once to the element type
+ * before their product with V, as in attn_fwd, where the tensor cores take the
+ * problem (head_dim 64 and 128, page sizes that are multiples of 8, rows on
+ * 16-byte boundaries, and prefixes long enough to be read once); partial
+ * results and their merge are float32. */
 ATTN_API int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix, const void* q,
                              const void* k_pool, const void* v_pool, void* o, const float* mask,
                              const int32_t* k_lens, float* lse, void* workspace, size_t workspace_bytes,
