@@ -14,7 +14,11 @@
 //     rows are taken token after token, each with the angles of its own token.
 //
 // What bounds it: HBM for long prompts, the chain of loads for one token a
-// sequence, and instructions where the heads are narrow.
+// sequence, and instructions where the heads are narrow.  A video of 16384 tokens
+// (32/8 heads, head_dim 128, 411 MB) takes 75.5 us, 5.4 TB/s; both forms of
+// angles in one kernel (more registers) 82.  Two batches of 5003 tokens with
+// 12/4 heads of 64 and axes in turn: 19.4 us, a token's own items 34.9, places in the
+// tables in 64 bits 20.5, three CTAs an SM (spills) 22.5.
 #pragma once
 
 #include "prep.cuh"

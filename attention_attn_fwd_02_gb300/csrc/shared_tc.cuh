@@ -28,6 +28,16 @@
 //     queries are loaded by the softmax threads, a row each, which have nothing
 //     else to do then (one warp takes 5 us for the rows, 256 threads 1).
 // P enters the product as one value of the element type, as in attn_fwd.
+//
+// Measured (32 query heads over 8, head_dim 128, bf16): a key tile takes an SM
+// 1.45 us from HBM, whether one row tile reads it or two (6.9 TB/s on all SMs),
+// and 1.55 us for two row tiles out of L2 (1.65 PFLOP/s; one row tile 0.65 to
+// 1.0).  A launch costs 12 to 15 us besides, most of it instruction fetch: a
+// CTA's first S is there after 7 us, its first P 5 us later (0.9 from the second
+// tile on), and the epilogue takes 3.  Four slots of the ring instead of five or six:
+// 115 -> 107 us behind 131072 keys.  Prefetches of later tiles into L2 read
+// half of HBM twice (537 -> 818 MB) and cost a third of the speed; a step of the
+// softmax warps on nothing, to fetch their instructions early, gained nothing.
 #pragma once
 
 #include <type_traits>
@@ -298,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rl = lane / kUnits, un = lane % kUnits;
 #pragma unroll
       for (int j = 0; j < 2 * BM / 32; ++j) {
-        if (j >= BM / 32 && !it.some1) break;   // (row tiles that hold the same rows share the first tile)
+        // (Behind the last row no warp takes a step; row tiles that hold the same rows share the first tile.)
+        if (it.row0 + 32 * j >= it.rows) break;
 #pragma unroll 4
         for (int r0 = 0; r0 < 32; r0 += kRowsAt) {
           const int64_t from = __shfl_sync(0xffffffffu, at[j], r0 + rl);
