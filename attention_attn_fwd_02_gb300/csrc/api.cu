@@ -464,22 +464,26 @@ int shared_plan(const attn_problem* p, const attn_prefix* x) {
   return n < 1 ? 1 : (int)n;
 }
 
-// Workspace of attn_fwd_shared, whichever pass a call's alignment takes.
-size_t shared_bytes(const attn_problem* p, const attn_pages* pages, const attn_prefix* x) {
-  if (p->batch == 0 || p->q_len == 0) return 0;
-  int status = 0;
-  const Problem r = with_prefix(
-      resolve(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, &status), x);
-  const int n = shared_plan(p, x);
-  const size_t a = n > 1 ? sums_ws_bytes(p, n) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
+// The plans of attn_fwd_shared's passes (r: the problem with its prefix), and the workspace that holds whichever a call's
+// alignment takes.
+struct SharedPlan {
+  bool tc, f32;   // there is a plan on the tensor cores, or of packed rows in float32: w
   shr::Work w;
+  int parts;      // of the CUDA-core passes
+  size_t bytes;
+};
+
+void plan_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* x, const Problem& r, SharedPlan& s) {
+  s.parts = shared_plan(p, x);
+  const size_t a = s.parts > 1 ? sums_ws_bytes(p, s.parts) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
+  s.tc = shared_tc_plan(r, pages->page_size, s.w);
+  s.f32 = !s.tc && shared_f32_plan(r, s.w);
   size_t c = 0;
-  const bool tc = shared_tc_plan(r, pages->page_size, w);
-  if (tc || shared_f32_plan(r, w)) {
-    c = tc ? shared_tc_bytes(r, w) : shared_f32_bytes(r, w);
-    if (p->q_len == 1) c += paged_own_bytes(own_problem(r), w.own_sms);   // behind the partial results
+  if (s.tc || s.f32) {
+    c = s.tc ? shared_tc_bytes(r, s.w) : shared_f32_bytes(r, s.w);
+    if (p->q_len == 1) c += paged_own_bytes(own_problem(r), s.w.own_sms);   // behind the partial results
   }
-  return a > b ? (a > c ? a : c) : (b > c ? b : c);
+  s.bytes = a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
 // Workspace of attn_decode_paged, whichever pass a call's alignment takes.
@@ -663,7 +667,12 @@ int attn_decode_paged(const attn_problem* p, const attn_pages* pages, int32_t fi
 
 size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix) {
   if (check_shared(p, pages, prefix) != ATTN_OK) return 0;
-  return shared_bytes(p, pages, prefix);
+  if (p->batch == 0 || p->q_len == 0) return 0;
+  const Problem r = with_prefix(
+      resolve(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr), prefix);
+  SharedPlan s;
+  plan_shared(p, pages, prefix, r, s);
+  return s.bytes;
 }
 
 int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix, const void* q,
@@ -675,31 +684,27 @@ int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_p
   rc = check_pointers(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse);
   if (rc) return rc;
   if (prefix->rows > 0 && (!k_pool || !v_pool)) return ATTN_ERR_INVALID_ARG;
-  const size_t need = shared_bytes(p, pages, prefix);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
-  if (need > 0 && !aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
-  int* status = nullptr;
-  rc = status_ptr(&status);
+  Problem r = with_prefix(resolve(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse, nullptr), prefix);
+  SharedPlan plan;
+  plan_shared(p, pages, prefix, r, plan);
+  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes)) return ATTN_ERR_WORKSPACE;
+  if (plan.bytes > 0 && !aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  rc = status_ptr(&r.status);
   if (rc) return rc;
-  const Problem r = with_prefix(resolve(p, q, k_pool, v_pool, o, mask, nullptr, k_lens, lse, status), prefix);
   const Ext x = make_ext(0, pages, prefix);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t rows = (size_t)p->batch * p->heads * p->q_len;
   int used = 0;
-  shr::Work w;
-  if (shared_tc_plan(r, x.page_size, w)) {
-    rc = shared_tc_try(r, x, w, own_problem(r), make_ext(0, pages), workspace, st, &used);
-    if (rc || used) return rc;
-  }
-  if (shared_f32_plan(r, w)) {
-    rc = shared_f32_packed(r, x, w, own_problem(r), make_ext(0, pages), workspace, st, &used);
+  if (plan.tc || plan.f32) {
+    rc = (plan.tc ? shared_tc_try : shared_f32_packed)(r, x, plan.w, own_problem(r), make_ext(0, pages), workspace, st,
+                                                       &used);
     if (rc || used) return rc;
   }
   if (p->q_len == 1) {
     rc = paged_try(r, x, workspace, st, &used);
     if (rc || used) return rc;
   }
-  const int n = shared_plan(p, prefix);
+  const int n = plan.parts;
   Split s{1, 1, nullptr, nullptr};
   if (n > 1) s = split_in(workspace, rows, n, 0, p->head_dim, true);
   rc = shared_f32_try(r, x, s, st, &used);

@@ -116,6 +116,9 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   const int64_t pre = ceil_div(p.prefix, kKeys), own = ceil_div(p.Sk - p.prefix, kKeys);
   const double part_us = (double)(all * p.G) * p.D * 8 / 6.0e6;   // a partial result of every row, written and read
   auto has_half = [](int64_t n) { return (int)((n - 1) % (2 * kRows) < kRows); };   // the last block has one row tile
+  // One query an entry, the decode pass can take the prefix's keys too, once an entry, out of L2.
+  const double us_each =
+      (double)p.B * p.G * ceil_div(p.qpg, p.qpg > 8 ? 16 : 8) * p.prefix * p.D * 4 / 12.0e6;
   // The prefix once for the packed rows of all entries.
   double us_packed = INFINITY;
   if (pre > 0) {
@@ -148,15 +151,14 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
       own_all = us_first + us_own < (us_first > us_beside ? us_first : us_beside);
     }
     w.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, ctas);
+    us_packed = kPass + kMerge + (double)total / w.list.ctas * kUnit + part_us;
+    if (p.Sq == 1 && us_packed + kPass > us_each) return false;
     w.own_slot = cut(runs, total, w.list);
-    us_packed = kPass + kMerge + (double)total / w.list.ctas * kUnit + w.own_slot * part_us;
+    us_packed += (w.own_slot - 1) * part_us;
     w.one_tile = all <= kRows;
     w.own_sms = own_all ? kSms : kSms - w.list.ctas;
   }
   if (p.Sq == 1) {
-    // The decode pass can take the prefix's keys too, once an entry, out of L2.
-    const int per = p.qpg > 8 ? 16 : 8;
-    const double us_each = (double)p.B * p.G * ceil_div(p.qpg, per) * p.prefix * p.D * 4 / 12.0e6;
     w.parts_b = own > 0;
     w.splits = w.own_slot + w.parts_b;
     return us_packed + kPass <= us_each;
