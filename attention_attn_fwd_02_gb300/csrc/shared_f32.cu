@@ -95,7 +95,7 @@ int shared_f32_packed(const Problem& p, const Ext& x, shr::Work& w, const Proble
   } else if (own.Sk > 0) {
     s = Split{1, 1, w.part_o + (int64_t)w.own_slot * p.D, w.part_m + w.own_slot, w.part_l + w.own_slot};
     rc = launch_head_dim<kPaged>(own, x_own, s, w.splits, st);
-    if (rc < 0) return ATTN_ERR_CUDA;   // (fewer CTAs than the prefix's)
+    if (rc < 0) return ATTN_ERR_CUDA;   // (no more than 2^30 CTAs: two rows an entry and kv head or more)
   }
   if (rc) return rc;
   return launch_shared_merge(p, w, decoded ? &decode : nullptr, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -272,6 +272,41 @@ def test_many_times_over(dt, D, Sq, B, H, G, prefix):
     assert attn.attn_device_status(torch.cuda.current_stream().cuda_stream) == attn.ATTN_OK
 
 
+@pytest.mark.parametrize("dt,D,Sq,B,H,G,prefix", [
+    ("bf16", 128, 1, 60, 8, 2, 4000), ("f16", 64, 1, 150, 8, 8, 3001), ("f16", 128, 4, 30, 8, 2, 3000),
+    ("bf16", 64, 3, 40, 4, 4, 5003), ("f32", 64, 1, 70, 8, 8, 5000), ("f32", 128, 3, 20, 8, 4, 3001)])
+@pytest.mark.parametrize("kind", ["mask", "sink", "cap"])
+def test_transforms_behind_long_prefixes(dt, D, Sq, B, H, G, prefix, kind):
+    """Masks, sinks and softcaps where the prefix is read once for all entries."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D + Sq + B)
+    lens, kw = [(7 * b) % 90 for b in range(B)], dict(masked_rows="zero")
+    if kind == "mask":
+        kw["mask"] = sb.mask_kinds(g, B, H, Sq, prefix + max(lens))
+    elif kind == "sink":
+        kw["head_sink"] = torch.linspace(-3.0, 8.0, H, device="cuda")
+    else:
+        kw["softcap"] = 3.0
+    c = sc.make(dt, D, B, Sq, H, G, 16, prefix, lens, 81, **kw)
+    out, lse = sc.run(c, return_lse=True)
+    sc.check(c, out, lse)
+
+
+@pytest.mark.parametrize("dt,Sq,B,prefix", [("bf16", 1, 4, 200), ("f16", 1, 60, 4000), ("bf16", 30, 3, 400), ("f32", 9, 3, 200)])
+def test_pages_named_more_than_once(dt, Sq, B, prefix):
+    """A page twice in the prefix's list, in two entries' lists, and in both kinds of list."""
+    c = sc.make(dt, 64, B, Sq, 8, 4, 16, prefix, [64] * B, 91, poison=False)
+    q, k, v, ptab, _, table = c["call"]
+    ptab[3] = ptab[1]
+    table[1] = table[0]
+    table[2, :2] = ptab[4:6]
+    rows = [torch.cat([p[ptab.long()].transpose(1, 2).flatten(0, 1)[:prefix].expand(B, -1, -1, -1),
+                       p[table.long()].transpose(2, 3).flatten(1, 2)], 1).transpose(1, 2) for p in (k, v)]
+    c["ref"] = (c["ref"][0], *rows, c["ref"][3])
+    out, lse = sc.run(c, return_lse=True)
+    sc.check(c, out, lse)
+
+
 def test_refusals():
     c = sc.make("bf16", 128, 2, 3, 4, 2, 16, 100, [9, 12], 51)
     q, k, v, ptab, prefix, table = c["call"]
