@@ -458,7 +458,8 @@ int shared_plan(const attn_problem* p, const attn_prefix* x) {
   const int64_t rows = (int64_t)p->q_len * (p->heads / p->kv_heads), tile = p->dtype == ATTN_F32 && p->q_len > 1 ? 32 : 16;
   const int64_t blocks = (int64_t)(p->batch > 0 ? p->batch : 1) * p->kv_heads * ((rows + tile - 1) / tile);
   int64_t n = ((tile == 32 ? 608 : 4096) + blocks - 1) / blocks;
-  n = n < 64 ? n : 64;
+  const int64_t most = tile == 32 && (p->head_dim == 64 || p->head_dim == 128) ? 256 : 64;   // (merges of a warp a column)
+  n = n < most ? n : most;
   const int64_t tiles = ((int64_t)x->rows + p->k_len + 127) / 128;
   n = n < tiles ? n : tiles;
   return n < 1 ? 1 : (int)n;

@@ -67,6 +67,7 @@ int cut(const Runs& runs, int64_t total, Shares& s) {
     const bool next = k < run.count && at >= run.tiles;   // in a unit's end
     s.unit[c] = (int)(first + k + next);
     s.tile[c] = next || k == run.count ? 0 : (int)at;
+    if (c > 0 && s.tile[c - 1] > 0 && s.unit[c] > s.unit[c - 1]) s.cut[s.n_cut++] = (int16_t)(c - 1);
     if (c == s.ctas) break;
     s.frag[c] = 0;
     if (s.tile[c] > 0) {   // one more than the last share's, where that began in the unit too
@@ -116,9 +117,9 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   const int64_t pre = ceil_div(p.prefix, kKeys), own = ceil_div(p.Sk - p.prefix, kKeys);
   const double part_us = (double)(all * p.G) * p.D * 8 / 6.0e6;   // a partial result of every row, written and read
   auto has_half = [](int64_t n) { return (int)((n - 1) % (2 * kRows) < kRows); };   // the last block has one row tile
-  // One query an entry, the decode pass can take the prefix's keys too, once an entry, out of L2.
-  const double us_each =
-      (double)p.B * p.G * ceil_div(p.qpg, p.qpg > 8 ? 16 : 8) * p.prefix * p.D * 4 / 12.0e6;
+  // One query an entry, the decode pass can take the prefix's keys too; it starts some 7 us faster than the two passes side
+  // by side and their merge (of 80 shapes the one that this says takes 0.7 % longer than the better one on average).
+  const double us_each = shr::decode_us(p, p.qpg > 8 ? 16 : 8, 2, 10.9e6, 8192) - 2.0;
   // The prefix once for the packed rows of all entries.
   double us_packed = INFINITY;
   if (pre > 0) {
@@ -152,7 +153,7 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
     }
     w.list.ctas = (int)clamp64(total / (2 * Shares::kTile), 1, ctas);
     us_packed = kPass + kMerge + (double)total / w.list.ctas * kUnit + part_us;
-    if (p.Sq == 1 && us_packed + kPass > us_each) return false;
+    if (p.Sq == 1 && us_packed > us_each) return false;
     w.own_slot = cut(runs, total, w.list);
     us_packed += (w.own_slot - 1) * part_us;
     w.one_tile = all <= kRows;
@@ -161,7 +162,7 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   if (p.Sq == 1) {
     w.parts_b = own > 0;
     w.splits = w.own_slot + w.parts_b;
-    return us_packed + kPass <= us_each;
+    return us_packed <= us_each;
   }
   w.blocks_b = (int)ceil_div(rows, 2 * kRows);
   w.alt_b = has_half(rows);
@@ -193,7 +194,12 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   // Cut units cost the write and the read of about a fragment and a half a share, and the merge; uncut ones leave SMs
   // without work for most of a unit's time.
   const double us_cut = kMerge + (double)ctas * 3 * kRows * p.D * 8 / 6.0e6;
-  const double us_left = total ? (double)left.at(0).cost() * kUnit - (double)total / kSms * kUnit : 0.0;
+  int64_t longest = 0;
+  for (int64_t i = 0; i < left.size(); ++i) {
+    const Run run = left.at(i);
+    if (run.count > 0 && run.cost() > longest) longest = run.cost();
+  }
+  const double us_left = (double)(longest * kSms - total) / kSms * kUnit;
   double us_joined = kPass + us_all / kSms + us_left;
   v.n_b = (int)items;
   if (us_cut < us_left) {

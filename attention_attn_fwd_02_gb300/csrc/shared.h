@@ -23,6 +23,8 @@ struct Shares {
   int unit[kSms + 1];
   int tile[kSms + 1];
   int16_t frag[kSms];
+  int n_cut;              // joined: the shares that end a unit which an earlier one began
+  int16_t cut[kSms];
 };
 
 // How a problem is divided, by value to the kernels.  A row is a (entry, query,
@@ -73,6 +75,22 @@ __host__ __device__ inline int most_tiles(const Problem& p, int block, int pre) 
   if (p.causal) own = clamp64(q + 1 + (p.align_klens ? own - p.Sq : p.coff - p.prefix), 0, own);
   const int tiles = pre + (int)((own + kKeys - 1) / kKeys);
   return tiles > 0 ? tiles : 1;
+}
+
+// Time of the decode pass over pages where it takes the prefix's keys too, once an entry and `per` heads of a kv head, in
+// us: out of L2 (l2: bytes a us), and at least once out of HBM.  Long lists of few units are cut into many fragments, which
+// one CTA a unit joins (`uncut`: keys of a list that a cluster takes).  32 entries or fewer at 16 bits, 8/2 heads, head_dim
+// 64 behind 42382 keys, one entry: 34.8 us; 8/1 heads of 128 behind 49285, 4 entries: 49.2; without a join 11 to 13 and
+// the copies' time.
+inline double decode_us(const Problem& p, int per, int es, double l2, int uncut) {
+  const double units = (double)p.B * p.G * ((p.qpg + per - 1) / per), keys = (double)p.prefix * p.D * 2 * es;
+  const double far = p.G * keys / 6.5e6, near = units * keys / l2;
+  double join = 0.0;
+  if (units * 8 <= 3 * kSms && p.Sk > uncut) {
+    const double width = (double)(p.qpg < per ? p.qpg : per) * p.D / 4 / 256;   // of the joining CTA's threads
+    join = 4.0 + 0.2 * 3 * kSms / units * (width < 0.25 ? 0.25 : width > 1 ? 1 : width);
+  }
+  return (near > far ? near : far) + join;
 }
 
 }  // namespace shr

@@ -42,27 +42,31 @@ int shared_f32_try(const Problem& p, const Ext& x, const Split& sp, cudaStream_t
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Rows against keys on register tiles run at some 20 TFLOP/s where their CTAs fill the SMs.  Each entry by itself, rows
+// Rows against keys on register tiles run at some 25 TFLOP/s where their CTAs fill the SMs.  Each entry by itself, rows
 // that are not there are computed too (tiles of 32 rows); one query an entry, the decode pass over pages reads the
 // prefix out of L2 at some 7.5 TB/s once an entry.  Packed, a pass, the merge and the partial results come on top.
-// (157 entries of 8/8 heads, head_dim 64, behind 39706 keys: 2698 us by the decode pass, 638 packed; 33 entries of 12/4
-// heads, head_dim 128, behind 24940: 471 and 380.)
+// (157 entries of 8/8 heads, head_dim 64, behind 39706 keys: 2698 us by the decode pass, 638 packed; 7 of 16/8 heads,
+// head_dim 64, behind 36567: 170 and 114; 3 of 8/4 heads, head_dim 128, behind 46887: 117 and 183.)  A CTA takes 3 us or
+// more a tile of 32 keys, so both lists are cut until their CTAs fill the SMs (9 entries of 2 tokens, 4/2 heads, head_dim
+// 64, behind 11635 keys with up to 1611 own ones: 172 us with 32 parts of the prefix and whole own lists, 51 now).
 bool shared_f32_plan(const Problem& p, shr::Work& w) {
   if (p.dtype != ATTN_F32 || p.kv_int8 || (p.D != 64 && p.D != 128) || p.prefix < 1 || p.B < 2) return false;
   const int64_t rows = (int64_t)p.Sq * p.qpg, all = rows * p.B, own = p.Sk - p.prefix;
   if (all > (1 << 30) || all * p.G > (1ll << 31)) return false;
-  auto product = [&](int64_t r, int64_t keys) { return 4.0 * (double)(r * p.G) * keys * p.D / 20.0e6; };
+  auto product = [&](int64_t r, int64_t keys) { return 4.0 * (double)(r * p.G) * keys * p.D / 25.0e6; };
   const double part_us = (double)(all * p.G) * p.D * 8 / 6.0e6;
   const int64_t blocks = ceil_div(all, 64) * p.G;
-  int64_t n = clamp64(ceil_div(608, blocks), 1, 32);
-  n = clamp64(n, 1, ceil_div(p.prefix, 128));
-  const double us_packed = 12.0 + product(ceil_div(all, 64) * 64, p.prefix) + (n + 1) * part_us;
-  const double us_each = p.Sq == 1 ? (double)p.B * p.G * ceil_div(p.qpg, 8) * p.prefix * p.D * 8 / 7.5e6
-                                   : product(ceil_div(rows, 32) * 32 * p.B, p.prefix);
+  const int64_t n = clamp64(ceil_div(608, blocks), 1, ceil_div(p.prefix, 128));
+  const int tile = all > 32 && blocks * n >= 2 * shr::kSms ? 64 : 32;   // (as launch_d takes them)
+  const double us_packed = 32.0 + product(ceil_div(all, tile) * tile, p.prefix) + (n + 1) * part_us;
+  const double us_each =
+      18.0 + (p.Sq == 1 ? shr::decode_us(p, 8, 4, 7.5e6, 4096) : product(ceil_div(rows, 32) * 32 * p.B, p.prefix));
   if (us_each < us_packed) return false;
   w = shr::Work{};
   w.own_slot = (int)n;
   w.parts_b = own > 0;
+  if (own > 0 && p.Sq > 1)   // (as many CTAs for the own keys)
+    w.parts_b = (int)clamp64(608 / (ceil_div(rows, 64) * p.B * p.G), 1, ceil_div(own, 128));
   w.splits = (int)n + w.parts_b;
   return true;
 }
@@ -93,7 +97,7 @@ int shared_f32_packed(const Problem& p, const Ext& x, shr::Work& w, const Proble
     if (!paged_own(own, x_own, part, static_cast<char*>(workspace) + shared_f32_bytes(p, w), st, &decode, &rc))
       return ATTN_ERR_UNSUPPORTED;
   } else if (own.Sk > 0) {
-    s = Split{1, 1, w.part_o + (int64_t)w.own_slot * p.D, w.part_m + w.own_slot, w.part_l + w.own_slot};
+    s = Split{w.parts_b, 1, w.part_o + (int64_t)w.own_slot * p.D, w.part_m + w.own_slot, w.part_l + w.own_slot};
     rc = launch_head_dim<kPaged>(own, x_own, s, w.splits, st);
     if (rc < 0) return ATTN_ERR_CUDA;   // (no more than 2^30 CTAs: two rows an entry and kv head or more)
   }

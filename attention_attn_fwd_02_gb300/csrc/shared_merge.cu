@@ -265,10 +265,9 @@ __global__ void __launch_bounds__(32 * kWarps, 6) merge_few_kernel(const Problem
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kWarps, 6) join_few_kernel(const Problem p, const __grid_constant__ Work w) {
   constexpr int kTeams = 128 / D, kPer = kWarps * kRowsFew * kTeams;   // rows of a CTA
-  const int c = blockIdx.x / (2 * kRows / kPer);
+  const int c = w.list.cut[blockIdx.x / (2 * kRows / kPer)];
   const int local0 =
       blockIdx.x % (2 * kRows / kPer) * kPer + threadIdx.x / 32 * (kRowsFew * kTeams) + threadIdx.x % 32 / (D / 4);
-  if (w.list.tile[c] == 0 || w.list.unit[c + 1] == w.list.unit[c]) return;
   const int u = w.list.unit[c], n = w.list.frag[c] + 1, c0 = c - w.list.frag[c];
   const int row0 = w.block_of(u, p.B, p.G) * 2 * kRows, g = u % p.G, b = u / p.G % p.B;
   FewRow row[kRowsFew];
@@ -334,13 +333,13 @@ __global__ void __launch_bounds__(32 * kWarps, 8)
 template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(32 * kWarps, 8) join_kernel(const Problem p, const __grid_constant__ Work w) {
   constexpr int kPer = kWarps / WARPS;   // rows of a CTA
-  const int c = blockIdx.x / (2 * kRows / kPer);
+  const int c = w.list.cut[blockIdx.x / (2 * kRows / kPer)];
   const int local = blockIdx.x % (2 * kRows / kPer) * kPer + threadIdx.x / 32 / WARPS;
-  if (w.list.tile[c] == 0 || w.list.unit[c + 1] == w.list.unit[c]) return;
   const int u = w.list.unit[c], n = w.list.frag[c] + 1, c0 = c - w.list.frag[c];
   const int row = w.block_of(u, p.B, p.G) * 2 * kRows + local, i = row / p.qpg;
   const int h = u % p.G * p.qpg + row - i * p.qpg;
   const bool here = i < p.Sq;
+  if (kPer == 1 && !here) return;   // (all of the CTA's threads)
   paged::wait_for_previous();
   // The first fragment is the last of its share, the others are their shares' first.
   auto at = [&](int f) { return ((int64_t)(c0 + f) * 2 + (f == 0 ? 1 : 0)) * (2 * kRows) + local; };
@@ -371,8 +370,10 @@ cudaError_t merge(const Problem& p, const Work& w, const Cuts& cuts, cudaStream_
   if (w.joined) {
     int most = 0;
     for (int c = 0; c < w.list.ctas; ++c) most = w.list.frag[c] > most ? w.list.frag[c] : most;
-    if (most >= kFew) return launch(join_kernel<T, D, 4>, (int64_t)w.list.ctas * 2 * kRows, st, p, w);
-    return launch(join_few_kernel<T, D>, (int64_t)w.list.ctas * 2 * kRows / kPer, st, p, w);
+    const int64_t rows = (int64_t)w.list.n_cut * 2 * kRows;
+    if (most >= 8 && rows <= 16 * kSms) return launch(join_kernel<T, D, 4>, rows, st, p, w);
+    if (most >= kFew) return launch(join_kernel<T, D, 1>, rows / kWarps, st, p, w);
+    return launch(join_few_kernel<T, D>, (int64_t)w.list.n_cut * 2 * kRows / kPer, st, p, w);
   }
   const int64_t rows = (int64_t)p.B * p.H * p.Sq;
   if (w.splits <= kFew && !cuts.note) return launch(merge_few_kernel<T, D>, (rows + kPer - 1) / kPer, st, p, w);
