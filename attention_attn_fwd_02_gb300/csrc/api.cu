@@ -452,14 +452,14 @@ int check_shared(const attn_problem* p, const attn_pages* pages, const attn_pref
   return check_pages(pages, p->k_len);
 }
 
-// The CUDA-core passes' plan for a batch with a prefix: parts of each row block's tile list, as many as fill the SMs
-// some four times over (float32 on register tiles, of 32 rows or more) or more (rows of a few lanes each).
-int shared_plan(const attn_problem* p, const attn_prefix* x) {
-  const int64_t rows = (int64_t)p->q_len * (p->heads / p->kv_heads), tile = p->dtype == ATTN_F32 && p->q_len > 1 ? 32 : 16;
-  const int64_t blocks = (int64_t)(p->batch > 0 ? p->batch : 1) * p->kv_heads * ((rows + tile - 1) / tile);
-  int64_t n = ((tile == 32 ? 608 : 4096) + blocks - 1) / blocks;
-  const int64_t most = tile == 32 && (p->head_dim == 64 || p->head_dim == 128) ? 256 : 64;   // (merges of a warp a column)
-  n = n < most ? n : most;
+// The CUDA-core passes' plan for a batch with a prefix: parts of each row block's tile list, by what register tiles cost
+// (float32), or as many as fill the SMs (rows of a few lanes each).
+int shared_plan(const attn_problem* p, const attn_prefix* x, const Problem& r) {
+  const int64_t rows = (int64_t)p->q_len * (p->heads / p->kv_heads);
+  if (p->dtype == ATTN_F32 && p->q_len > 1) return shared_f32_parts(r);
+  const int64_t blocks = (int64_t)(p->batch > 0 ? p->batch : 1) * p->kv_heads * ((rows + 15) / 16);
+  int64_t n = (4096 + blocks - 1) / blocks;
+  n = n < 64 ? n : 64;
   const int64_t tiles = ((int64_t)x->rows + p->k_len + 127) / 128;
   n = n < tiles ? n : tiles;
   return n < 1 ? 1 : (int)n;
@@ -475,7 +475,7 @@ struct SharedPlan {
 };
 
 void plan_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* x, const Problem& r, SharedPlan& s) {
-  s.parts = shared_plan(p, x);
+  s.parts = shared_plan(p, x, r);
   const size_t a = s.parts > 1 ? sums_ws_bytes(p, s.parts) : 0, b = p->q_len == 1 ? paged_ws_bytes(r, 0) : 0;
   s.tc = shared_tc_plan(r, pages->page_size, s.w);
   s.f32 = !s.tc && shared_f32_plan(r, s.w);

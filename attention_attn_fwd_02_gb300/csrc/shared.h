@@ -106,6 +106,7 @@ int shared_tc_try(const Problem& p, const Ext& x, shr::Work& w, const Problem& o
 // float32: the pass over each entry by itself and its merge (s: parts of the entries' tile lists), and the packed plan
 // with its bytes and passes, as for the tensor cores.
 int shared_f32_try(const Problem& p, const Ext& x, const Split& s, cudaStream_t st, int* used);
+int shared_f32_parts(const Problem& p);
 bool shared_f32_plan(const Problem& p, shr::Work& w);
 size_t shared_f32_bytes(const Problem& p, const shr::Work& w);
 int shared_f32_packed(const Problem& p, const Ext& x, shr::Work& w, const Problem& own, const Ext& x_own, void* workspace,

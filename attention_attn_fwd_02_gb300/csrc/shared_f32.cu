@@ -19,7 +19,39 @@ bool takes(const Problem& p, const Ext& x) {
          tma_layout_ok_es(p.V, p.v, x.page_size, p.G, pages, 4) && tma_layout_ok_es(p.O, p.o, p.Sq, p.H, p.B, 4);
 }
 
+// Parts of each row block's list of `keys` keys (groups: lists by kv head, of `rows` rows each) that take the least time,
+// in *us.  An SM takes its CTAs in rounds of as many as it holds; in each a tile of 32 keys takes what one CTA needs by
+// itself (head_dim 128: 4.1 us with 32 rows, 6.3 with 64) or what all need of the SM's shared memory and FMAs (2.8 and 4.2 a
+// CTA).  Rows of partial results are written and read.  (128 rows of 8 kv heads, head_dim 64, against 16384 keys: 377 us
+// in 19 parts, one and a third round, 266 in 14.)
+int best_parts(int64_t groups, int64_t rows, int64_t keys, int D, double* us) {
+  const int64_t tiles = ceil_div(keys, 32);
+  const double part_us = (double)(groups * rows) * D * 8 / 6.0e6;
+  int best = 1;
+  *us = 0;
+  for (int64_t n = 1; n <= 256 && n <= tiles; ++n) {
+    const int tm = row_tiles(D, groups * n, rows);   // rows a thread, as launch_d takes them
+    const int64_t sm = ceil_div(groups * ceil_div(rows, 16 * tm) * n, shr::kSms), held = D > 64 && tm == 4 ? 2 : 3;
+    const double alone = D * (tm == 4 ? 0.050 : 0.034), shared = D * (tm == 4 ? 0.0325 : 0.021);
+    const double list = (double)ceil_div(tiles, n), last = (double)(sm % held) * shared;
+    double t = (double)(sm / held) * (4.0 + list * (held * shared > alone ? held * shared : alone));
+    if (sm % held) t += 4.0 + list * (last > alone ? last : alone);
+    if (n > 1) t += 4.0 + (n + 1) * part_us + 0.04 * n;
+    if (n == 1 || t < *us) {
+      *us = t;
+      best = (int)n;
+    }
+    if (sm > 8 * held) break;
+  }
+  return best;
+}
+
 }  // namespace
+
+int shared_f32_parts(const Problem& p) {
+  double us;
+  return best_parts((int64_t)p.B * p.G, (int64_t)p.Sq * p.qpg, p.Sk, p.D, &us);
+}
 
 int shared_f32_try(const Problem& p, const Ext& x, const Split& sp, cudaStream_t st, int* used) {
   *used = 0;
@@ -42,32 +74,29 @@ int shared_f32_try(const Problem& p, const Ext& x, const Split& sp, cudaStream_t
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Rows against keys on register tiles run at some 25 TFLOP/s where their CTAs fill the SMs.  Each entry by itself, rows
-// that are not there are computed too (tiles of 32 rows); one query an entry, the decode pass over pages reads the
-// prefix out of L2 at some 7.5 TB/s once an entry.  Packed, a pass, the merge and the partial results come on top.
-// (157 entries of 8/8 heads, head_dim 64, behind 39706 keys: 2698 us by the decode pass, 638 packed; 7 of 16/8 heads,
-// head_dim 64, behind 36567: 170 and 114; 3 of 8/4 heads, head_dim 128, behind 46887: 117 and 183.)  A CTA takes 3 us or
-// more a tile of 32 keys, so both lists are cut until their CTAs fill the SMs (9 entries of 2 tokens, 4/2 heads, head_dim
-// 64, behind 11635 keys with up to 1611 own ones: 172 us with 32 parts of the prefix and whole own lists, 51 now).
+// Each entry by itself, rows that are not there are computed too (tiles of 32 rows); one query an entry, the decode pass over
+// pages reads the prefix out of L2 at some 7.5 TB/s once an entry, at some 22 TFLOP/s.  Packed, a pass, the merge and the
+// partial results come on top.  (157 entries of 8/8 heads, head_dim 64, behind 39706 keys: 2698 us by the decode pass, 638
+// packed; 7 of 16/8 heads, head_dim 64, behind 36567: 170 and 114; 3 of 8/4 heads, head_dim 128, behind 46887: 117 and
+// 183.  9 of 2 tokens, 4/2 heads, head_dim 64, behind 11635 keys with up to 1611 own ones: 172 us with 32 parts of the
+// prefix and whole own lists, 51 with the parts above.)
 bool shared_f32_plan(const Problem& p, shr::Work& w) {
   if (p.dtype != ATTN_F32 || p.kv_int8 || (p.D != 64 && p.D != 128) || p.prefix < 1 || p.B < 2) return false;
   const int64_t rows = (int64_t)p.Sq * p.qpg, all = rows * p.B, own = p.Sk - p.prefix;
   if (all > (1 << 30) || all * p.G > (1ll << 31)) return false;
-  auto product = [&](int64_t r, int64_t keys) { return 4.0 * (double)(r * p.G) * keys * p.D / 25.0e6; };
-  const double part_us = (double)(all * p.G) * p.D * 8 / 6.0e6;
-  const int64_t blocks = ceil_div(all, 64) * p.G;
-  const int64_t n = clamp64(ceil_div(608, blocks), 1, ceil_div(p.prefix, 128));
-  const int tile = all > 32 && blocks * n >= 2 * shr::kSms ? 64 : 32;   // (as launch_d takes them)
-  const double us_packed = 32.0 + product(ceil_div(all, tile) * tile, p.prefix) + (n + 1) * part_us;
-  const double us_each =
-      18.0 + (p.Sq == 1 ? shr::decode_us(p, 8, 4, 7.5e6, 4096) : product(ceil_div(rows, 32) * 32 * p.B, p.prefix));
+  const int64_t some = own < 2048 ? own : 2048;   // (how many own keys there are is not known here)
+  double us_prefix, us_own = 10.0, us_list;
+  const int n = best_parts(p.G, all, p.prefix, p.D, &us_prefix);
+  const int n_own = own > 0 && p.Sq > 1 ? best_parts((int64_t)p.B * p.G, rows, some, p.D, &us_own) : own > 0;
+  best_parts((int64_t)p.B * p.G, rows, p.prefix + some, p.D, &us_list);
+  const double us_packed = 12.0 + us_prefix + us_own;
+  const double us_copies = shr::decode_us(p, 8, 4, 7.5e6, 4096), us_fmas = 4.0 * p.B * p.H * p.prefix * p.D / 22.0e6;
+  const double us_each = p.Sq == 1 ? 18.0 + (us_copies > us_fmas ? us_copies : us_fmas) : 6.0 + us_list;
   if (us_each < us_packed) return false;
   w = shr::Work{};
-  w.own_slot = (int)n;
-  w.parts_b = own > 0;
-  if (own > 0 && p.Sq > 1)   // (as many CTAs for the own keys)
-    w.parts_b = (int)clamp64(608 / (ceil_div(rows, 64) * p.B * p.G), 1, ceil_div(own, 128));
-  w.splits = (int)n + w.parts_b;
+  w.own_slot = n;
+  w.parts_b = n_own;
+  w.splits = n + n_own;
   return true;
 }
 

@@ -40,6 +40,15 @@ constexpr int kThreads = 128;
 constexpr int BN = 32;
 using S = Scores<true>;   // (one instance with and without a mask: a product more for each D of a score)
 
+// acc + a b for both halves, in one instruction (rounded as two).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 acc) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%0, %1};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "+f"(acc.x), "+f"(acc.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return acc;
+}
+
 template <int D, int TM>
 struct Cfg {
   static constexpr int BM = 16 * TM;
@@ -266,17 +275,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, TM>::kCtas)
 #pragma unroll(D <= 64 ? 8 : 4)
     for (int j = 0; j < BN; ++j) {
       float pr[TM];
-#pragma unroll
-      for (int r = 0; r < TM; ++r) pr[r] = p_s[j * C::kPp + ty * TM + r];
+      const float* ps = p_s + j * C::kPp + ty * TM;
+      if constexpr (TM == 4) {
+        const float4 p4 = *reinterpret_cast<const float4*>(ps);
+        pr[0] = p4.x, pr[1] = p4.y, pr[2] = p4.z, pr[3] = p4.w;
+      } else {
+        const float2 p2 = *reinterpret_cast<const float2*>(ps);
+        pr[0] = p2.x, pr[1] = p2.y;
+      }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const float4 v4 = *reinterpret_cast<const float4*>(v_s + j * D + c * 32 + tx * 4);
 #pragma unroll
         for (int r = 0; r < TM; ++r) {
-          o[r][c][0] = fmaf(pr[r], v4.x, o[r][c][0]);
-          o[r][c][1] = fmaf(pr[r], v4.y, o[r][c][1]);
-          o[r][c][2] = fmaf(pr[r], v4.z, o[r][c][2]);
-          o[r][c][3] = fmaf(pr[r], v4.w, o[r][c][3]);
+          const float2 pp = make_float2(pr[r], pr[r]);
+          const float2 lo = fma2(pp, make_float2(v4.x, v4.y), make_float2(o[r][c][0], o[r][c][1]));
+          const float2 hi = fma2(pp, make_float2(v4.z, v4.w), make_float2(o[r][c][2], o[r][c][3]));
+          o[r][c][0] = lo.x;
+          o[r][c][1] = lo.y;
+          o[r][c][2] = hi.x;
+          o[r][c][3] = hi.y;
         }
       }
     }
@@ -332,12 +350,16 @@ int launch(const Problem& p, const Ext& x, const Split& sp, int stride, cudaStre
 
 // Four rows a thread when their CTAs fill the SMs, else two: more, shorter CTAs.  (In pages also two where a block has no
 // more rows: 77 entries of 28 tokens, 2/2 heads, head_dim 64, with 350 to 430 keys: 60.6 -> 39.6 us.)
+inline int row_tiles(int D, int64_t lists, int64_t rows) {
+  return D <= 128 && rows > 32 && (rows + 63) / 64 * lists >= 2 * 152 ? 4 : 2;
+}
+
 template <int D, int KIND>
 int launch_d(const Problem& p, const Ext& x, const Split& sp, int stride, cudaStream_t st) {
   const int64_t entries = KIND == kPacked ? 1 : p.B, rows = (int64_t)p.Sq * p.qpg * (KIND == kPacked ? p.B : 1);
-  const int64_t big = (rows + 63) / 64 * entries * p.G * sp.n_splits;
+  const int64_t lists = entries * p.G * sp.n_splits;
   if constexpr (D <= 128) {
-    if (big >= 2 * 152 && (KIND == kPlain || rows > 32)) return launch<D, 4, KIND>(p, x, sp, stride, st);
+    if (row_tiles(D, lists, KIND == kPlain && rows <= 32 ? 64 : rows) == 4) return launch<D, 4, KIND>(p, x, sp, stride, st);
   }
   return launch<D, 2, KIND>(p, x, sp, stride, st);
 }
