@@ -29,19 +29,20 @@ int best_parts(int64_t groups, int64_t rows, int64_t keys, int D, double* us) {
   const double part_us = (double)(groups * rows) * D * 8 / 6.0e6;
   int best = 1;
   *us = 0;
-  for (int64_t n = 1; n <= 256 && n <= tiles; ++n) {
+  for (int64_t n = 1, list = tiles; n <= 256 && n <= tiles; n = ceil_div(tiles, list - 1)) {   // (the fewest parts of a length)
+    list = ceil_div(tiles, n);
     const int tm = row_tiles(D, groups * n, rows);   // rows a thread, as launch_d takes them
-    const int64_t sm = ceil_div(groups * ceil_div(rows, 16 * tm) * n, shr::kSms), held = D > 64 && tm == 4 ? 2 : 3;
+    const int64_t sm = ceil_div(groups * ceil_div(rows, 16 * tm) * n, shr::kSms), held = D > 128 || (D > 64 && tm == 4) ? 2 : 3;
     const double alone = D * (tm == 4 ? 0.050 : 0.034), shared = D * (tm == 4 ? 0.0325 : 0.021);
-    const double list = (double)ceil_div(tiles, n), last = (double)(sm % held) * shared;
-    double t = (double)(sm / held) * (4.0 + list * (held * shared > alone ? held * shared : alone));
-    if (sm % held) t += 4.0 + list * (last > alone ? last : alone);
+    const double last = (double)(sm % held) * shared;
+    double t = (double)(sm / held) * (4.0 + (double)list * (held * shared > alone ? held * shared : alone));
+    if (sm % held) t += 4.0 + (double)list * (last > alone ? last : alone);
     if (n > 1) t += 4.0 + (n + 1) * part_us + 0.04 * n;
     if (n == 1 || t < *us) {
       *us = t;
       best = (int)n;
     }
-    if (sm > 8 * held) break;
+    if (sm > 8 * held || list == 1) break;
   }
   return best;
 }
