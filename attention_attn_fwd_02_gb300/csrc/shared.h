@@ -78,10 +78,9 @@ __host__ __device__ inline int most_tiles(const Problem& p, int block, int pre) 
 }
 
 // Time of the decode pass over pages where it takes the prefix's keys too, once an entry and `per` heads of a kv head, in
-// us: out of L2 (l2: bytes a us), and at least once out of HBM.  Long lists of few units are cut into many fragments, which
-// one CTA a unit joins (`uncut`: keys of a list that a cluster takes).  32 entries or fewer at 16 bits, 8/2 heads, head_dim
-// 64 behind 42382 keys, one entry: 34.8 us; 8/1 heads of 128 behind 49285, 4 entries: 49.2; without a join 11 to 13 and
-// the copies' time.
+// us: out of L2 (l2: bytes a us), and at least once out of HBM.  Long lists (over `uncut` keys, more than a cluster takes) of
+// few units are cut into many fragments, which one CTA a unit joins.  (One entry of 8/2 heads, head_dim 64, bf16, behind 42382
+// keys: 34.8 us, of them some 24 the join; 4 of 8/1 heads, head_dim 128, behind 49285: 49.2, some 30.)
 inline double decode_us(const Problem& p, int per, int es, double l2, int uncut) {
   const double units = (double)p.B * p.G * ((p.qpg + per - 1) / per), keys = (double)p.prefix * p.D * 2 * es;
   const double far = p.G * keys / 6.5e6, near = units * keys / l2;

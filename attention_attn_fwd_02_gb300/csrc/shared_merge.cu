@@ -370,6 +370,7 @@ cudaError_t merge(const Problem& p, const Work& w, const Cuts& cuts, cudaStream_
   if (w.joined) {
     int most = 0;
     for (int c = 0; c < w.list.ctas; ++c) most = w.list.frag[c] > most ? w.list.frag[c] : most;
+    // CTAs for the cut units alone (over all shares: 20 us for 20 units of 256 rows, 7 fragments each, against 6).
     const int64_t rows = (int64_t)w.list.n_cut * 2 * kRows;
     if (most >= 8 && rows <= 16 * kSms) return launch(join_kernel<T, D, 4>, rows, st, p, w);
     if (most >= kFew) return launch(join_kernel<T, D, 1>, rows / kWarps, st, p, w);

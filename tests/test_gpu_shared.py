@@ -292,6 +292,26 @@ def test_transforms_behind_long_prefixes(dt, D, Sq, B, H, G, prefix, kind):
     sc.check(c, out, lse)
 
 
+@pytest.mark.parametrize("dt,D,B,Sq,H,G,ps,prefix,short,full", [
+    ("bf16", 128, 2, 73, 12, 4, 128, 20040, 55, 79),      # few units, many shares of each
+    ("f16", 128, 2, 301, 8, 2, 32, 5288, 453, 624),
+    ("bf16", 64, 8, 261, 16, 8, 32, 1894, 1615, 2297),
+    ("f16", 64, 1, 471, 4, 1, 24, 119, 177, 1420),
+    ("bf16", 128, 2, 805, 8, 4, 16, 3001, 800, 817),      # last blocks of one row tile
+    ("f32", 64, 9, 2, 4, 2, 64, 11635, 237, 1611),        # own lists in parts
+    ("f32", 128, 1, 4, 4, 1, 32, 20615, 13, 13),
+    ("f32", 64, 77, 28, 2, 2, 32, 88, 348, 433),
+    ("f32", 128, 5, 60, 8, 4, 24, 500, 61, 500)])
+def test_cut_lists(dt, D, B, Sq, H, G, ps, prefix, short, full):
+    """Lists that are cut among CTAs, with a sink and without: own lists from `short` to `full` keys."""
+    lens = [short + (full - short) * b // max(B - 1, 1) for b in range(B)]
+    for kw in ({}, dict(smooth_softmax=True)):
+        c = sc.make(dt, D, B, Sq, H, G, ps, prefix, lens, 95, max_rows=full, **kw)
+        out, lse = sc.run(c, return_lse=True)
+        sc.check(c, out, lse)
+        assert torch.equal(sc.run(c), out)
+
+
 @pytest.mark.parametrize("dt,Sq,B,prefix", [("bf16", 1, 4, 200), ("f16", 1, 60, 4000), ("bf16", 30, 3, 400), ("f32", 9, 3, 200)])
 def test_pages_named_more_than_once(dt, Sq, B, prefix):
     """A page twice in the prefix's list, in two entries' lists, and in both kinds of list."""
