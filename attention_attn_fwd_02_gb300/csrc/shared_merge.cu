@@ -4,7 +4,9 @@
 // a row's partial results s, with the sink's logit as one more term of the
 // denominator, and LSE = M + log of that sum.  Which there are follows from the
 // plan (shared.h) and, for own keys that the decode pass cut, from its notes
-// (paged.cuh).
+// (paged.cuh).  A maximum of +inf or NaN or a sum of NaN makes the row NaN: the
+// passes' maxima pass over NaN scores, so that a part without any other has a
+// maximum of -inf, as an empty one does, and a sum of NaN.
 //
 // What bounds it: the latency of its loads.  A row of a decode step has up to some
 // twenty results: four warps take a row, each every fourth result; a lane reads
@@ -57,8 +59,8 @@ __device__ __forceinline__ void merge_row(const Problem& p, bool here, int64_t b
   const float l0 = one ? load_l(part + lane * WARPS) : 0.f;
   float M = bad ? -INFINITY : sg;
   for (int k = lane; k < mine; k += 32) {
-    const float m = k < 32 ? m0 : load_m(part + k * WARPS);
-    if (!(m < INFINITY)) bad = true;   // +inf or NaN
+    const float m = k < 32 ? m0 : load_m(part + k * WARPS), l = k < 32 ? l0 : load_l(part + k * WARPS);
+    if (!(m < INFINITY) || isnan(l)) bad = true;
     else M = fmaxf(M, m);
   }
 #pragma unroll
@@ -179,7 +181,7 @@ __device__ __forceinline__ void merge_few(const Problem& p, const Work& w, FewRo
   for (int q = 0; q < kRowsFew; ++q)
 #pragma unroll
     for (int k = 0; k < kFew; ++k) {
-      if (k >= row[q].n) row[q].m[k] = -INFINITY;
+      if (k >= row[q].n) row[q].m[k] = -INFINITY, row[q].l[k] = 0.f;
       v[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row[q].m[k] != -INFINITY) v[q][k] = *reinterpret_cast<const float4*>(w.part_o + row[q].at[k] * D + d);
     }
@@ -192,7 +194,7 @@ __device__ __forceinline__ void merge_few(const Problem& p, const Work& w, FewRo
     float M = bad ? -INFINITY : sg;
 #pragma unroll
     for (int k = 0; k < kFew; ++k) {
-      if (!(r.m[k] < INFINITY)) bad = true;   // +inf or NaN
+      if (!(r.m[k] < INFINITY) || isnan(r.l[k])) bad = true;
       else M = fmaxf(M, r.m[k]);
     }
     const float mu = M == -INFINITY ? 0.f : M;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps, 6) merge_few_kernel(const Problem
     row[q].n = row[q].here ? w.splits : 0;
 #pragma unroll
     for (int k = 0; k < kFew; ++k)
-      if (k >= n_a[q] && k < w.own_slot) row[q].m[k] = -INFINITY;
+      if (k >= n_a[q] && k < w.own_slot) row[q].m[k] = -INFINITY, row[q].l[k] = 0.f;
   }
   merge_few<T, D>(p, w, row);
 }
