@@ -107,8 +107,6 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   using namespace shr;
   if (p.dtype != ATTN_BF16 && p.dtype != ATTN_F16) return false;
   if (p.kv_int8 || (p.D != 64 && p.D != 128) || p.Sk < 1 || page_size % 8) return false;
-  const float sc = p.scale * 1.4426950408889634f;
-  if (!(sc == sc) || isinf(sc)) return false;
   const int64_t rows = (int64_t)p.Sq * p.qpg, all = rows * p.B;
   if (all > (1 << 30) || all * p.G > (1ll << 31)) return false;
   w = Work{};
@@ -227,7 +225,8 @@ int shared_tc_try(const Problem& p, const Ext& x, shr::Work& w, const Problem& o
   using namespace shr;
   *used = 0;
   const int pages = (int)min(x.n_pages, 0x7fffffffu);
-  if (pages < 1 || pages == 0x7fffffff) return ATTN_OK;
+  const float sc = p.scale * 1.4426950408889634f;
+  if (pages < 1 || pages == 0x7fffffff || !(sc == sc) || isinf(sc)) return ATTN_OK;
   if (!tma_layout_ok(p.Q, p.q, p.Sq, p.H, p.B) || !tma_layout_ok(p.K, p.k, x.page_size, p.G, pages) ||
       !tma_layout_ok(p.V, p.v, x.page_size, p.G, pages) || !tma_layout_ok(p.O, p.o, p.Sq, p.H, p.B))
     return ATTN_OK;

@@ -348,9 +348,13 @@ typedef struct {
   const int32_t* table;   /* DEVICE int32 [ceil(rows / page_size)]; may be NULL when rows == 0 */
 } attn_prefix;
 
-/* Bytes of device workspace attn_fwd_shared needs; from the shape alone
- * (batch, heads, q_len, k_len, prefix rows, page size).  0 when it needs none
- * and for an invalid problem. */
+/* Bytes of device workspace attn_fwd_shared needs.  What it depends on: batch,
+ * heads, kv_heads, q_len, k_len, head_dim, dtype, kv_dtype, the prefix's rows
+ * and page_size; with q_len > 1 also causal, causal_align and causal_offset
+ * (how the keys are cut follows what the rows see), so a size that was asked
+ * for one causal setting may be too small for another.  Nothing else (k_lens,
+ * layouts, masks, addresses) changes it.  0 when it needs none and for an
+ * invalid problem. */
 ATTN_API size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn_pages* pages,
                                                const attn_prefix* prefix);
 
