@@ -226,7 +226,7 @@ struct Ring {
   uint32_t ring;           // shared-memory address of this warp's stages
   int* key;                // [STAGES] first key of a stage
   uint32_t* vis;           // [STAGES] its visible keys, bit r = row r
-  int units, warp, lane, page, page_row;
+  int units, warp, lane, page;
   bool one_page, same;
 
   __device__ __forceinline__ Ring(const Work& work, const Cursor& at, int n_units, uint8_t* smem, int* keys,
@@ -245,16 +245,15 @@ struct Ring {
   // The page of row lane % KEYS of the next tile.
   __device__ __forceinline__ void look_up() {
     const int k = in.tl.tile(in.tile) * kTile + warp * KEYS + lane % KEYS;
-    page = -1;
-    page_row = 0;
-    if (visible(in.v, k)) page = page_of(w.x, in.b, k, page_row);
+    int row;   // (found again when the tile is copied: a register less, which the int8 instances would spill)
+    page = visible(in.v, k) ? page_of(w.x, in.b, k, row) : -1;
   }
   // Copies the next tile into stage s; with `more` moves on and looks up the pages of the tile behind it.
   __device__ __forceinline__ void issue(int s, bool more) {
     const Problem& p = w.p;
     const int k0 = in.tl.tile(in.tile) * kTile + warp * KEYS;
     const uint32_t mask = __ballot_sync(kAll, page >= 0);
-    const int g = in.u / w.n_hc, r = page_row, pg = max(page, 0);
+    const int g = in.u / w.n_hc, r = row_in_page(w.x, k0 + lane % KEYS), pg = max(page, 0);
     const int64_t ko = ((int64_t)pg * p.k.bs + (int64_t)g * p.k.hs + (int64_t)r * p.k.rs) * ES;
     const int64_t vo = same ? ko : ((int64_t)pg * p.v.bs + (int64_t)g * p.v.hs + (int64_t)r * p.v.rs) * ES;
     if (lane == 0) {
@@ -322,7 +321,7 @@ __device__ __forceinline__ void keep_row(const Work& w, int b, int h, int d, flo
 
 // Where a row's finished fragment goes.  M: reference maximum in the units of
 // Scores<NAT> (-inf: no visible key), L: sum relative to it, a: numerator of element d.
-template <typename T, bool NAT>
+template <typename T, bool NAT, bool OWN>
 __device__ __forceinline__ void put_row(const Work& w, bool whole, int cta, int slot, int b, int h, int hh, int d,
                                         float M, float L, float a) {
   const Problem& p = w.p;
@@ -337,7 +336,7 @@ __device__ __forceinline__ void put_row(const Work& w, bool whole, int cta, int 
     }
     return;
   }
-  if (w.own.o) {
+  if constexpr (OWN) {
     keep_row(w, b, h, d, M, L, a);
     return;
   }
@@ -351,13 +350,13 @@ __device__ __forceinline__ void put_row(const Work& w, bool whole, int cta, int 
 
 // What a row without a visible key returns, for all heads of entry b.  The
 // CTA's threads share it.
-template <typename T>
+template <typename T, bool OWN>
 __device__ __forceinline__ void fill_entry(const Work& w, int b) {
   const Problem& p = w.p;
   for (int x = threadIdx.x; x < p.H * p.D; x += kThreads) {
     const int h = x / p.D, d = x - h * p.D;
     float M = -INFINITY, L = 0.f;
-    if (w.own.o) {
+    if constexpr (OWN) {
       keep_row(w, b, h, d, M, L, 0.f);
       continue;
     }
@@ -372,23 +371,24 @@ __device__ __forceinline__ void fill_entry(const Work& w, int b) {
 
 // What every CTA of a pass without clusters does beside its units: its entries
 // without a visible key.
-template <typename T>
+template <typename T, bool OWN>
 __device__ __forceinline__ void fill_entries(const Work& w, int cta) {
   for (int b = cta; b < w.p.B; b += w.ctas)
     if (entry_tiles(w, b) == 0) {
-      fill_entry<T>(w, b);
-      if (w.own.note)
+      fill_entry<T, OWN>(w, b);
+      if (OWN && w.own.note)
         for (int u = threadIdx.x; u < w.p.G * w.n_hc; u += kThreads) note_kept(w, b, u);
     }
 }
 
 // Notes a cut unit that ends in share `cta` (whose first fragment it is), `first` tiles into its list.
+template <bool OWN>
 __device__ __forceinline__ void note_cut(const Work& w, const Share& s, int cta, const Cursor& c, int first) {
   const int64_t at = s.t0 - first;
   const int c0 = share_of(s.total, s.shares, at);
   // (Share c0 has a fragment in front of it if it begins in front of the last unit's end.)
   const int late = share_begin(s.total, s.shares, c0) < at - kEnd ? 1 : 0;
-  if (w.own.o) w.own.note[(int64_t)c.b * w.p.G * w.n_hc + c.u] = make_int2(2 * c0 + late, cta - c0 + 1);
+  if constexpr (OWN) w.own.note[(int64_t)c.b * w.p.G * w.n_hc + c.u] = make_int2(2 * c0 + late, cta - c0 + 1);
   else w.cuts[cta] = {c.b, c.u, c0, late};
 }
 
@@ -432,7 +432,7 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Merges the parts of the unit (b, heads h0 ..) that the cluster's CTAs hold; each CTA writes its share of the rows.
-template <typename T, bool NAT>
+template <typename T, bool NAT, bool OWN>
 __device__ __forceinline__ void cluster_join(const Work& w, const Part& part, int b, int h0, int nh) {
   const int D = w.p.D, n = w.cluster;
   cluster_sync();
@@ -454,7 +454,7 @@ __device__ __forceinline__ void cluster_join(const Work& w, const Part& part, in
       L = fmaf(f, l[q], L);
       A = fmaf(f, a[q], A);
     }
-    put_row<T, NAT>(w, true, 0, 0, b, h0 + hh, hh, d, M, L, A);
+    put_row<T, NAT, OWN>(w, true, 0, 0, b, h0 + hh, hh, d, M, L, A);
   }
   cluster_sync();   // no CTA leaves while its part is being read
 }

@@ -131,7 +131,8 @@ struct Cfg {
 };
 
 // XF: scores under a softcap or an additive mask.  MODE: how the units are divided.
-template <bool BF16, bool KV8, int D, int NT, bool XF, int MODE>
+// OWN: rows are kept for a merge (OwnPart).
+template <bool BF16, bool KV8, int D, int NT, bool XF, int MODE, bool OWN>
 __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) paged_mma_kernel(const Work w) {
   using C = Cfg<BF16, KV8, D, NT, MODE>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -165,14 +166,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     if (my) out.at_unit(w, units, cta);
   } else {
     let_next_start();
-    if (threadIdx.x == 0 && !w.own.o) w.cuts[cta].b = -1;
+    if (!OWN && threadIdx.x == 0) w.cuts[cta].b = -1;
     Share s;
     my = find_share(w, units, cta, lane, s, out);
     if (threadIdx.x == 0) share = s;
   }
   if (MODE != kCluster && my == 0) {
-    fill_entries<T>(w, cta);
-    if (w.own.o) wait_for_previous();
+    fill_entries<T, OWN>(w, cta);
+    if constexpr (OWN) wait_for_previous();
     return;
   }
   typename C::Stages ring(w, out, units, smem, st_key[0], st_vis[0]);
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     }
   };
   reset();
-  if constexpr (MODE != kCluster) fill_entries<T>(w, cta);   // (while the first copies are under way)
+  if constexpr (MODE != kCluster) fill_entries<T, OWN>(w, cta);   // (while the first copies are under way)
   const bool capped = XF && p.softcap > 0.f;
   const float cap_inv = capped ? 1.f / p.softcap : 0.f;
   // A row's reference is its maximum, less a lead where P is f16: there p = 2^(x - m_ref) is 2^11 at the maximum
@@ -444,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
       const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
       if constexpr (MODE == kShares)
         if (unit_ends && threadIdx.x == 0) {
-          if (!whole) note_cut(w, share, cta, out, first_tile);
-          else if (w.own.o) note_kept(w, out.b, out.u);
+          if (!whole) note_cut<OWN>(w, share, cta, out, first_tile);
+          else if (OWN) note_kept(w, out.b, out.u);
         }
       if (i + 1 < my) {   // the next unit's queries arrive during the merge
         out.template next<MODE>(w, units);
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
           const int dd = 64 * part + d;
           if (KV8) a *= p.v_scale[p.kv_per_channel ? g * D + dd : 0];
           if constexpr (MODE == kCluster) mine.put(D, hh, dd, M, L, a);
-          else put_row<T, XF>(w, whole, cta, slot, b, h0 + hh, hh, dd, M, L, a);
+          else put_row<T, XF, OWN>(w, whole, cta, slot, b, h0 + hh, hh, dd, M, L, a);
         }
         __syncthreads();
       }
@@ -510,26 +511,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<BF16, KV8, D, NT, MODE>::kCtas) 
     const int nh = min(C::kHeads, (g + 1) * p.qpg - h0);
     if (my == 0)
       for (int x = threadIdx.x; x < nh * D; x += kThreads) mine.put(D, x / D, x % D, -INFINITY, 0.f, 0.f);
-    cluster_join<T, XF>(w, mine, out.b, h0, nh);
+    cluster_join<T, XF, OWN>(w, mine, out.b, h0, nh);
   }
-  if (w.own.o) wait_for_previous();
+  if constexpr (OWN) wait_for_previous();
 }
 
-// Plans the pass; with `launch` enqueues it.
-template <bool BF16, bool KV8, int D, int NT>
-int pass_cfg(Work& w, bool launch, cudaStream_t st) {
+template <bool BF16, bool KV8, int D, int NT, bool OWN>
+int enqueue(const Work& w, cudaStream_t st) {
   using C = Cfg<BF16, KV8, D, NT, kShares>;   // (the same sizes for every mode)
-  plan_work(w, C::Stages::kTile, C::kHeads, C::kCtas);
-  if (!launch) return ATTN_OK;
   const bool xf = w.p.softcap > 0.f || w.p.M != nullptr;
   auto go = [&](auto mode) {
     constexpr int M = decltype(mode)::value;
-    return xf ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true, M>, w, C::kSmem, st)
-              : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false, M>, w, C::kSmem, st);
+    return xf ? launch_pass(paged_mma_kernel<BF16, KV8, D, NT, true, M, OWN>, w, C::kSmem, st)
+              : launch_pass(paged_mma_kernel<BF16, KV8, D, NT, false, M, OWN>, w, C::kSmem, st);
   };
   return w.cluster  ? go(std::integral_constant<int, kCluster>())
          : w.stride ? go(std::integral_constant<int, kWhole>())
                     : go(std::integral_constant<int, kShares>());
+}
+
+// The pass over own keys behind a shared prefix, instances of its own (paged_own_*.cu): its two kinds of results in one kernel
+// cost the pass over a whole cache registers (64 sequences of up to 8192 int8 rows: 132 -> 140 us).
+template <bool BF16, int D, int NT>
+int enqueue_own(const Work& w, cudaStream_t st);
+
+// Plans the pass; with `launch` enqueues it.
+template <bool BF16, bool KV8, int D, int NT>
+int pass_cfg(Work& w, bool launch, cudaStream_t st) {
+  using C = Cfg<BF16, KV8, D, NT, kShares>;
+  plan_work(w, C::Stages::kTile, C::kHeads, C::kCtas);
+  if (!launch) return ATTN_OK;
+  if (w.own.o) {
+    if constexpr (!KV8 && D <= 128) return enqueue_own<BF16, D, NT>(w, st);
+    return ATTN_ERR_UNSUPPORTED;   // (no plan of attn_fwd_shared comes here)
+  }
+  return enqueue<BF16, KV8, D, NT, false>(w, st);
 }
 
 // Two column tiles of heads a unit for more than eight heads a kv head (at

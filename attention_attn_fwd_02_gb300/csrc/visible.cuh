@@ -125,6 +125,12 @@ __device__ __forceinline__ int page_of(const Ext& x, int b, int k, int& row) {
   return (uint32_t)pg < x.n_pages ? pg : -1;
 }
 
+// The row of key k in its page, whichever page that is.
+__device__ __forceinline__ int row_in_page(const Ext& x, int k) {
+  if (k >= x.prefix) k -= x.prefix;
+  return k - page_index(x, k) * x.page_size;
+}
+
 // The CUDA-core forward with first keys and paged caches.
 cudaError_t launch_simt_ext(const Problem& p, const Ext& x, const Split& s, cudaStream_t st);
 
