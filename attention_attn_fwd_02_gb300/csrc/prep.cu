@@ -245,12 +245,6 @@ int check_prep(const attn_prep* p) {
   return ATTN_OK;
 }
 
-}  // namespace
-}  // namespace attn
-
-namespace attn {
-namespace {
-
 // attn_qkv_prep (axes null) and attn_qkv_prep_axes.
 int prep_impl(const attn_prep* p, const attn_pages* pages, const attn_axes* axes, const void* q, const void* k,
               const void* v, const void* q_weight, const void* k_weight, const float* cos, const float* sin,

@@ -20,7 +20,7 @@ struct Prep {
   uint32_t n_pages;
   const int32_t* table;
   int64_t table_stride;
-  int n_axes;             // 0: one position a token
+  int n_axes;             // 1: one position a token
   int64_t axis_stride;    // of the positions
   uint8_t axis[128];      // of each rotated pair
 };

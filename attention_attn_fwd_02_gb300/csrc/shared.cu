@@ -116,7 +116,7 @@ bool shared_tc_plan(const Problem& p, int page_size, shr::Work& w) {
   const double part_us = (double)(all * p.G) * p.D * 8 / 6.0e6;   // a partial result of every row, written and read
   auto has_half = [](int64_t n) { return (int)((n - 1) % (2 * kRows) < kRows); };   // the last block has one row tile
   // One query an entry, the decode pass can take the prefix's keys too; it starts some 7 us faster than the two passes side
-  // by side and their merge (of 80 shapes the one that this says takes 0.7 % longer than the better one on average).
+  // by side and their merge (of 163 shapes the one that this says takes 0.35 % longer than the better one on average).
   const double us_each = shr::decode_us(p, p.qpg > 8 ? 16 : 8, 2, 10.9e6, 8192) - 2.0;
   // The prefix once for the packed rows of all entries.
   double us_packed = INFINITY;

@@ -9,7 +9,7 @@ namespace shr {
 
 constexpr int kRows = 128;    // query rows of a tile
 constexpr int kKeys = 128;    // keys of a tile
-constexpr int kSms = 152;
+constexpr int kSms = paged::kSms;
 
 // A list of units cut into shares of equal cost, one a CTA: a unit is a block of
 // rows, of one or two row tiles, with its key tiles.  Units lie end to end;

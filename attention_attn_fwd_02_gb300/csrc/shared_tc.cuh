@@ -27,7 +27,11 @@
 //     its last S: rows pack without gaps whatever the strides.  A CTA's first
 //     queries are loaded by the softmax threads, a row each, which have nothing
 //     else to do then (one warp takes 5 us for the rows, 256 threads 1).
-// P enters the product as one value of the element type, as in attn_fwd.
+// P enters the product as one value of the element type, as in attn_fwd and by
+// choice: in two halves, as the decode pass takes it, a key tile would be three
+// products instead of two, 2.0 us instead of 1.33 of an SM's tensor time with two row
+// tiles, against 1.45 for its copy from HBM.  It costs 0.0023 instead of 0.0017
+// relative error in bf16, 0.00029 instead of 0.00021 in f16 (the output's rounding alone).
 //
 // Measured (32 query heads over 8, head_dim 128, bf16): a key tile takes an SM
 // 1.45 us from HBM, whether one row tile reads it or two (6.9 TB/s on all SMs),

@@ -367,8 +367,21 @@ ATTN_API size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn
  * attn_fwd, counted from the entry's first own row: all L_b of them without
  * causal, up to i + off_b with it (a row whose diagonal is in front of the own
  * keys sees the prefix alone).  The result is that of attn_fwd over the
- * concatenated keys; the prefix's keys are read once for all entries (short
- * prefixes and the types named below: once an entry, out of L2).
+ * concatenated keys.  What a problem takes, and how often it reads the prefix:
+ *   - f16/bf16, head_dim 64 or 128, page_size a multiple of 8, rows of Q, K, V
+ *     and O on 16-byte boundaries: the tensor cores, once for the rows of all
+ *     entries (with many queries an entry, once for each 256 of its rows and kv
+ *     head).  One query an entry with a short prefix or few entries: the next.
+ *   - One query an entry, head_dim 64, 128 or 256, K and V rows on 16-byte
+ *     boundaries, any page_size, int8 pools too (with f16/bf16 Q): the pass of
+ *     attn_decode_paged, once an entry, out of L2.
+ *   - float32 with rows on 16-byte boundaries: head_dim 64 and 128 once for all
+ *     entries where many share a long prefix, else, and at head_dim 32 and 256,
+ *     once for each 32 or 64 rows of an entry and kv head.
+ *   - Everything else: the CUDA cores, once for each few rows, one to two orders
+ *     slower.  More than one query an entry over int8 pools or, in f16/bf16, at
+ *     head_dim 256 is in this class, and so are all other head dims, and odd page
+ *     sizes and unaligned rows where they are not named above.
  * p->window_left must be -1 (ATTN_ERR_INVALID_ARG).  mask columns are the
  * concatenated keys: column prefix->rows is an entry's first own row.  List
  * values outside [0, n_pages) hold no rows, as for attn_decode_paged, in the
@@ -380,10 +393,10 @@ ATTN_API size_t attn_fwd_shared_workspace_size(const attn_problem* p, const attn
  * that some row sees must be finite, or rows of their tile that hide the key,
  * or give it a weight below the element type's range, may become NaN.
  * Precision: f16/bf16 probabilities are rounded once to the element type
- * before their product with V, as in attn_fwd, where the tensor cores take the
- * problem (head_dim 64 and 128, page sizes that are multiples of 8, rows on
- * 16-byte boundaries, and prefixes long enough to be read once); partial
- * results and their merge are float32. */
+ * before their product with V, as in attn_fwd, where the first of the classes
+ * above takes the problem (0.0023 relative against 0.0017 of rounding O alone in
+ * bf16, 0.00029 against 0.00021 in f16), and in two halves or not at all in the
+ * others; partial results and their merge are float32. */
 ATTN_API int attn_fwd_shared(const attn_problem* p, const attn_pages* pages, const attn_prefix* prefix, const void* q,
                              const void* k_pool, const void* v_pool, void* o, const float* mask,
                              const int32_t* k_lens, float* lse, void* workspace, size_t workspace_bytes,
@@ -494,8 +507,9 @@ ATTN_API int attn_probe_ex2(int32_t blocks, int32_t iters, float* sink, attn_str
 
 /* Test utility, not part of the attention path: arms a one-shot fault for the
  * tests of the kernels' bounded waits.  With ATTN_INJECT_DROP_FIRST_COPY, the
- * next launch of a tensor-core kernel (the prefill kernels and the decode
- * split passes; the CUDA-core kernels ignore it and leave it armed) makes its
+ * next launch of a tensor-core kernel that copies by TMA (attn_fwd's,
+ * attn_fwd_window's and attn_fwd_shared's, and the split passes of attn_decode;
+ * the others ignore it and leave it armed) makes its
  * first CTA announce its first key-tile copy to the copy's barrier without
  * issuing it.  The waits on that barrier then run out after about 2 s; the CTA
  * records ATTN_ERR_DEVICE_TIMEOUT in the status word (attn_device_status),
